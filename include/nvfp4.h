@@ -58,10 +58,12 @@ typedef struct CUstream_st* nvfp4_stream_t;   /* == cudaStream_t */
 #define NVFP4_ERR_WORKSPACE         -5   /* workspace missing or too small */
 #define NVFP4_ERR_TIMEOUT           -6   /* a bounded on-device wait gave up (device status word) */
 #define NVFP4_ERR_SCRATCH_LIMIT     -7   /* shape exceeds the fixed scratch of nvfp4_gemm_w4a16_noalloc */
+#define NVFP4_ERR_NO_PAGES          -8   /* the pool has no free page left (device status word) */
 
 /* ---- enums --------------------------------------------------------------- */
 #define NVFP4_DTYPE_F32   0
 #define NVFP4_DTYPE_BF16  1
+#define NVFP4_DTYPE_E4M3  2   /* key-value caches only */
 
 #define NVFP4_ST_COMPUTE  0   /* s_t = amax(|x|) / 2688 (1 if all zero), written to *s_t */
 #define NVFP4_ST_GIVEN    1   /* s_t read from *s_t (must be finite and > 0) */
@@ -98,6 +100,8 @@ typedef struct nvfp4_tensor {
 #define NVFP4_OP_GATHER_ARGMAX   4
 #define NVFP4_OP_GEMM_W4A4_QUANT 5
 #define NVFP4_OP_GROUPED_GEMM_W4A4 6
+#define NVFP4_OP_PAGED_ATTENTION 7
+#define NVFP4_OP_KV_PAGES        8
 
 /* ---- entry points ----------------------------------------------------------- */
 
@@ -344,6 +348,117 @@ int nvfp4_verify_accept(const void* H, int64_t batch, int n_draft, nvfp4_tensor_
                         int32_t* out_tokens, int32_t* n_accepted, void* workspace, size_t workspace_bytes,
                         nvfp4_stream_t stream);
 
+/* ---- attention over a paged key-value cache --------------------------------- */
+
+/* One layer's key-value cache: pools of pages, each of page_size positions of
+ * every kv head.
+ *   k, v     device [pages][heads][page_size][head_dim], bf16 or E4M3 codes,
+ *            16-byte aligned
+ *   k_scale, v_scale  device fp32 [heads], finite and > 0 (E4M3 only: a value
+ *            is code * scale of its head; ignored for bf16)
+ *   page_size 16, 32, 64 or 128; head_dim 64 or 128; pages * heads < 2^31
+ *   dtype    NVFP4_DTYPE_BF16 or NVFP4_DTYPE_E4M3 */
+typedef struct nvfp4_kv_cache {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t pages;
+  int32_t heads;
+  int32_t page_size;
+  int32_t head_dim;
+  int32_t dtype;
+} nvfp4_kv_cache_t;
+
+/* The sequences of a call. Position j of sequence b lies in row j % page_size
+ * of page table[b * table_stride + j / page_size].
+ *   table    device int32 [batch][max_pages], rows table_stride entries apart;
+ *            a page id outside [0, pages) means that no page is there
+ *   lens     device int32 [batch]: positions in use, the call's new ones among them
+ *   start    device int32 [batch + 1]: the new tokens of sequence b are rows
+ *            start[b] .. start[b + 1] - 1 of the call's token arrays, and its
+ *            last positions; NULL: max_new tokens for every sequence
+ *   batch    1 .. 4096
+ *   max_new  >= 1: the most new tokens of a sequence. It chooses the kernel;
+ *            with `start`, a sequence that has more is still computed. */
+typedef struct nvfp4_kv_seqs {
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* start;
+  int64_t table_stride;
+  int32_t batch;
+  int32_t max_pages;
+  int32_t max_new;
+  int32_t reserved;   /* 0 */
+} nvfp4_kv_seqs_t;
+
+/* Write the new tokens' keys and values into the cache's pages.
+ *   K, V   device bf16: row t (of `tokens`) starts at K + t * k_stride
+ *          elements and holds [heads][head_dim]; rows 16-byte aligned
+ * bf16 rows are copied; for E4M3, x / scale (IEEE division) is rounded to
+ * nearest even and saturates at 448. A row whose position is negative or has no
+ * page is skipped, and the device status word says NVFP4_ERR_INVALID_ARG. */
+int nvfp4_kv_append(nvfp4_kv_cache_t cache, nvfp4_kv_seqs_t seqs, const void* K, int64_t k_stride, const void* V,
+                    int64_t v_stride, int64_t tokens, nvfp4_stream_t stream);
+
+/* Attention of the new tokens over the cache, causal, with an optional sliding
+ * window and sinks. Token i of the n new ones of sequence b is at position
+ * p = lens[b] - n + i and sees the positions j with 0 <= j <= p that have a
+ * page and, with window > 0, for which p - j < window or j < sinks;
+ *   out = sum_j softmax_j(scale * q . k_j) v_j      (zeros if it sees none).
+ * Query head h reads kv head h / (q_heads / cache.heads).
+ *   Q        device bf16: token t's heads [q_heads][head_dim] at Q + t * q_stride
+ *            elements; rows 16-byte aligned
+ *   q_heads  a multiple of cache.heads
+ *   tokens   rows of Q and out; rows that no sequence covers are not written
+ *   window   0: none;  sinks >= 0 (ignored without a window)
+ *   out      device bf16 [tokens][q_heads][head_dim], 16-byte aligned
+ *   workspace  >= nvfp4_workspace_size(NVFP4_OP_PAGED_ATTENTION, batch, max_new,
+ *            q_heads, cache.heads, head_dim) bytes, 16-byte aligned. Its first
+ *            4096 bytes must be zero before the first call that uses it; every
+ *            call that completes leaves them zero. One call at a time may use it.
+ * Scores, softmax statistics and sums are fp32. Positions that a row does not
+ * see are left out of its sums whatever they hold, except that a key-value
+ * row of the same sequence that other new rows of the call see must be finite. */
+int nvfp4_paged_attention(const void* Q, int64_t q_stride, int q_heads, nvfp4_kv_cache_t cache, nvfp4_kv_seqs_t seqs,
+                          int64_t tokens, int window, int sinks, float scale, void* out, void* workspace,
+                          size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* Pages. refs[p] (device int32 [pages]) counts the table entries that hold
+ * page p; 0 means free. Pages are handed out lowest id first, in the order of
+ * the call's list. Where the pool runs out, entries stay without a page (-1) and
+ * the device status word says NVFP4_ERR_NO_PAGES; a list entry outside the
+ * table's rows is skipped (NVFP4_ERR_INVALID_ARG in the status word). Sequence
+ * lists must not name a row twice. `workspace`: >= nvfp4_workspace_size(
+ * NVFP4_OP_KV_PAGES, pages, entries of the list (or batch), 0, 0, 0) bytes,
+ * 16-byte aligned; scratch. */
+
+/* A page for every position of the sequences' new tokens whose table entry
+ * holds none (`table` is seqs.table, written). */
+int nvfp4_kv_reserve(nvfp4_kv_seqs_t seqs, int64_t tokens, int page_size, int32_t* table, int32_t* refs, int64_t pages,
+                     void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* Fork sequences: row dst[f] of the table becomes a copy of row src[f]. Full
+ * pages are shared (refs + 1); the positions in use of a partly filled last page
+ * are copied to a fresh page. Rows dst must be empty, distinct and not in src;
+ * a src may be forked many times.
+ *   table  device int32 [rows][max_pages];  lens  device int32 [rows] */
+int nvfp4_kv_fork(nvfp4_kv_cache_t cache, int32_t* table, int64_t table_stride, int max_pages, int32_t* lens, int rows,
+                  int32_t* refs, const int32_t* src, const int32_t* dst, int n, void* workspace,
+                  size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* Give up sequences: their pages' counts go down by one, their table rows to
+ * -1 and their lengths to 0. */
+int nvfp4_kv_release(int32_t* table, int64_t table_stride, int max_pages, int32_t* lens, int rows, int32_t* refs,
+                     int64_t pages, const int32_t* seqs, int n, nvfp4_stream_t stream);
+
+/* Move the live pages to the ids 0 .. live - 1: each live page with an id of
+ * `live` or more goes to a free id below (the i-th to the i-th), with its count
+ * and its table entries. The contents of the pages left behind stay as they are.
+ *   live   device int32 out: the number of live pages */
+int nvfp4_kv_compact(nvfp4_kv_cache_t cache, int32_t* table, int64_t table_stride, int max_pages, int rows,
+                     int32_t* refs, int32_t* live, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
 /* ---- helpers --------------------------------------------------------------- */
 
 /* Bytes of one matrix's block scales in the given layout. */
@@ -356,7 +471,9 @@ size_t nvfp4_scales_bytes(int64_t rows, int64_t K, int scale_layout);
  *   GROUPED_GEMM:  (T, H, I, E, topk)
  *   GATHER_ARGMAX: (M, n_idx, K, -, -)
  *   GEMM_W4A4_QUANT: (M, N, K, -, -)
- *   GROUPED_GEMM_W4A4: (T, H, I, E, topk) */
+ *   GROUPED_GEMM_W4A4: (T, H, I, E, topk)
+ *   PAGED_ATTENTION: (batch, max_new, q_heads, kv_heads, head_dim)
+ *   KV_PAGES:      (pages, entries of the list or batch, -, -, -) */
 size_t nvfp4_workspace_size(int op, int64_t a, int64_t b, int64_t c, int64_t e, int64_t topk);
 
 /* Human-readable name of a status code (static storage). */

@@ -16,12 +16,12 @@ import torch
 LIB_PATH = Path(__file__).resolve().parent / "libnvfp4.so"
 
 OK = 0
-ERR_INVALID_ARG, ERR_TIMEOUT = -1, -6
-DTYPE_F32, DTYPE_BF16 = 0, 1
+ERR_INVALID_ARG, ERR_TIMEOUT, ERR_NO_PAGES = -1, -6, -8
+DTYPE_F32, DTYPE_BF16, DTYPE_E4M3 = 0, 1, 2
 ST_COMPUTE, ST_GIVEN = 0, 1
 SCALES_ROWMAJOR, SCALES_MMA = 0, 1
 (OP_QUANTIZE, OP_GEMM_W4A16, OP_GEMM_W4A4, OP_GROUPED_GEMM, OP_GATHER_ARGMAX, OP_GEMM_W4A4_QUANT,
- OP_GROUPED_GEMM_W4A4) = range(7)
+ OP_GROUPED_GEMM_W4A4, OP_PAGED_ATTENTION, OP_KV_PAGES) = range(9)
 
 EXPORTS = [
     "nvfp4_quantize", "nvfp4_prepack_scales", "nvfp4_gemm_w4a16", "nvfp4_gemm_w4a4",
@@ -30,6 +30,8 @@ EXPORTS = [
     "nvfp4_read_device_status", "nvfp4_selftest_bounded_wait", "nvfp4_version",
     "nvfp4_gemm_w4a16_noalloc", "nvfp4_verify_accept", "nvfp4_probe_fp4_mma_rate",
     "nvfp4_gemm_w4a16_silu_mul", "nvfp4_gemm_w4a4_quant", "nvfp4_grouped_gemm_w4a4",
+    "nvfp4_kv_append", "nvfp4_paged_attention", "nvfp4_kv_reserve", "nvfp4_kv_fork", "nvfp4_kv_release",
+    "nvfp4_kv_compact",
 ]
 _NON_INT = ("nvfp4_scales_bytes", "nvfp4_workspace_size", "nvfp4_status_string")
 
@@ -39,6 +41,20 @@ class CTensor(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("s_t", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("K", ctypes.c_int64), ("batch", ctypes.c_int32),
                 ("scale_layout", ctypes.c_int32)]
+
+
+class CKVCache(ctypes.Structure):
+    """Mirror of nvfp4_kv_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class CKVSeqs(ctypes.Structure):
+    """Mirror of nvfp4_kv_seqs_t."""
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("start", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -66,6 +82,12 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_gather_rows.argtypes = [CTensor, vp, i64, vp, vp, vp]
         L.nvfp4_gemv_argmax.argtypes = [vp, i64, CTensor, vp, vp, vp, vp, sz, vp]
         L.nvfp4_verify_accept.argtypes = [vp, i64, i32, CTensor, vp, vp, vp, vp, sz, vp]
+        L.nvfp4_kv_append.argtypes = [CKVCache, CKVSeqs, vp, i64, vp, i64, i64, vp]
+        L.nvfp4_paged_attention.argtypes = [vp, i64, i32, CKVCache, CKVSeqs, i64, i32, i32, ctypes.c_float, vp, vp, sz, vp]
+        L.nvfp4_kv_reserve.argtypes = [CKVSeqs, i64, i32, vp, vp, i64, vp, sz, vp]
+        L.nvfp4_kv_fork.argtypes = [CKVCache, vp, i64, i32, vp, i32, vp, vp, vp, i32, vp, sz, vp]
+        L.nvfp4_kv_release.argtypes = [vp, i64, i32, vp, i32, vp, i64, vp, i32, vp]
+        L.nvfp4_kv_compact.argtypes = [CKVCache, vp, i64, i32, i32, vp, vp, vp, sz, vp]
         L.nvfp4_scales_bytes.argtypes = [i64, i64, i32]
         L.nvfp4_scales_bytes.restype = sz
         L.nvfp4_workspace_size.argtypes = [i32, i64, i64, i64, i64, i64]
@@ -331,6 +353,205 @@ def verify_accept(h: torch.Tensor, w: QTensor, draft_ids: torch.Tensor, workspac
     _check(lib().nvfp4_verify_accept(_ptr(h), batch, n_draft, w.c(), _ptr(draft_ids), _ptr(tokens), _ptr(n_acc),
                                      _ptr(ws), ws.numel(), _stream()), "nvfp4_verify_accept")
     return tokens, n_acc
+
+
+@dataclass
+class KVCache:
+    """One layer's paged key-value cache: pools k, v [pages][heads][page_size]
+    [head_dim], bf16, or float8_e4m3fn with a scale for each kv head
+    (value = code * scale)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+    def __post_init__(self):
+        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
+        _require_cuda(k, v, ks, vs)
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError("KVCache: k and v are contiguous pools [pages][heads][page_size][head_dim] of one type")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("KVCache: pools are bfloat16 or float8_e4m3fn")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        for t in (ks, vs) if e4m3 else ():
+            if t is None or t.dtype != torch.float32 or t.shape != (k.shape[1],) or not t.is_contiguous():
+                raise ValueError("KVCache: an E4M3 cache needs fp32 scales [heads]")
+        self._c = CKVCache(k.data_ptr(), v.data_ptr(), ks.data_ptr() if e4m3 else None, vs.data_ptr() if e4m3 else None,
+                           k.shape[0], k.shape[1], k.shape[2], k.shape[3], DTYPE_E4M3 if e4m3 else DTYPE_BF16)
+
+    def c(self) -> CKVCache:
+        return self._c
+
+
+def kv_cache(pages: int, heads: int, page_size: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
+             k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None, device="cuda") -> KVCache:
+    """An empty cache (E4M3 scales default to 1)."""
+    shape = (pages, heads, page_size, head_dim)
+    if dtype == torch.float8_e4m3fn:
+        k_scale = k_scale if k_scale is not None else torch.ones(heads, device=device)
+        v_scale = v_scale if v_scale is not None else torch.ones(heads, device=device)
+    return KVCache(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device),
+                   k_scale, v_scale)
+
+
+def _int32(t, name, dim=1):
+    if t.dtype != torch.int32 or t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: an int32 tensor of {dim} dimension(s), the last one contiguous, is needed")
+
+
+def _table_stride(table):
+    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+
+
+def _seqs(table, lens, start, max_new) -> CKVSeqs:
+    _require_cuda(table, lens, start)
+    _int32(table, "table", 2)
+    _int32(lens, "lens")
+    batch = lens.shape[0]
+    if table.shape[0] != batch:
+        raise ValueError("table: one row for each entry of lens is needed")
+    if start is not None:
+        _int32(start, "start")
+        if start.shape[0] != batch + 1:
+            raise ValueError("start: batch + 1 offsets are needed")
+    return CKVSeqs(table.data_ptr(), lens.data_ptr(), None if start is None else start.data_ptr(), _table_stride(table),
+                   batch, table.shape[1], max_new, 0)
+
+
+def _token_rows(x, heads, dim, name):
+    """x bf16 [T][heads][dim] with a token stride the kernels take (a copy if it has another layout)."""
+    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+        raise ValueError(f"{name}: bf16 [tokens][{heads}][{dim}] is needed")
+    s = x.stride()
+    if s[2] != 1 or (s[1] != dim and heads > 1) or s[0] % 8 or s[0] < heads * dim or x.data_ptr() % 16:
+        x = x.contiguous()
+        if x.data_ptr() % 16:
+            x = x.clone()
+    return x
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+              start: torch.Tensor | None = None, max_new: int = 1) -> None:
+    """Write the new tokens' k, v (bf16 [T][heads][head_dim], e.g. slices of a
+    fused projection) to their positions, the last ones of each sequence.
+    lens counts the new tokens; sequence b's are rows start[b] .. start[b + 1] - 1
+    (start None: max_new for every sequence)."""
+    _require_cuda(k, v)
+    c = cache.c()
+    k, v = _token_rows(k, c.heads, c.head_dim, "k"), _token_rows(v, c.heads, c.head_dim, "v")
+    if k.shape != v.shape:
+        raise ValueError("kv_append: k and v need the same shape")
+    T = k.shape[0]
+    row = c.heads * c.head_dim
+    _check(lib().nvfp4_kv_append(c, _seqs(table, lens, start, max_new), k.data_ptr(), k.stride(0) if T > 1 else row,
+                                 v.data_ptr(), v.stride(0) if T > 1 else row, T, _stream()), "nvfp4_kv_append")
+
+
+def attention_workspace(batch: int, max_new: int, q_heads: int, kv_heads: int, head_dim: int,
+                        device="cuda") -> torch.Tensor:
+    """A workspace for paged_attention calls of up to these sizes, zeroed as its first use needs it."""
+    return torch.zeros(max(workspace_size(OP_PAGED_ATTENTION, batch, max_new, q_heads, kv_heads, head_dim), 256),
+                       dtype=torch.uint8, device=device)
+
+
+def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
+                    start: torch.Tensor | None = None, max_new: int = 1, window: int = 0, sinks: int = 0,
+                    scale: float | None = None, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention of the new tokens' q (bf16 [T][q_heads][head_dim]) over
+    the cache, their own keys and values included (kv_append first). With
+    window > 0 a position sees the last `window` positions and the first
+    `sinks`. scale defaults to head_dim ** -0.5. A row that sees nothing gives
+    zeros. `workspace`: attention_workspace(...), kept between calls of one stream."""
+    _require_cuda(q)
+    c = cache.c()
+    if q.dim() != 3:
+        raise ValueError("q: bf16 [tokens][q_heads][head_dim] is needed")
+    T, heads, D = q.shape
+    q = _token_rows(q, heads, c.head_dim, "q")
+    if out is None:
+        o = torch.empty(T, heads, D, dtype=torch.bfloat16, device=q.device)
+    else:
+        o = out
+        if o.shape != (T, heads, D) or o.dtype != torch.bfloat16 or not o.is_contiguous():
+            raise ValueError("out: contiguous bf16 of q's shape is needed")
+    seqs = _seqs(table, lens, start, max_new)
+    ws = workspace if workspace is not None else attention_workspace(seqs.batch, max_new, heads, c.heads, D, q.device)
+    _check(lib().nvfp4_paged_attention(q.data_ptr(), q.stride(0) if T > 1 else heads * D, heads, c, seqs, T, window,
+                                       sinks, D ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr(),
+                                       ws.numel(), _stream()), "nvfp4_paged_attention")
+    return o
+
+
+def _pages_ws(workspace, pages, n, device):
+    return workspace if workspace is not None else _workspace(workspace_size(OP_KV_PAGES, pages, n), device)
+
+
+def kv_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int,
+               start: torch.Tensor | None = None, max_new: int = 1, workspace: torch.Tensor | None = None) -> None:
+    """Pages (lowest free ids first) for the positions of the new tokens whose
+    table entry holds none; refs int32 [pages] counts a page's users."""
+    _require_cuda(refs)
+    _int32(refs, "refs")
+    seqs = _seqs(table, lens, start, max_new)
+    tokens = seqs.batch * max_new if start is None else (1 << 30) - 1   # start says how many
+    ws = _pages_ws(workspace, refs.shape[0], seqs.batch, refs.device)
+    _check(lib().nvfp4_kv_reserve(seqs, tokens, page_size, table.data_ptr(), refs.data_ptr(), refs.shape[0],
+                                  ws.data_ptr(), ws.numel(), _stream()), "nvfp4_kv_reserve")
+
+
+def _pool_args(table, lens, refs, pages=None):
+    _require_cuda(table, lens, refs)
+    _int32(table, "table", 2)
+    _int32(refs, "refs")
+    if pages is not None and refs.shape[0] != pages:
+        raise ValueError("refs: one count for each page is needed")
+    if lens is not None:
+        _int32(lens, "lens")
+        if lens.shape[0] != table.shape[0]:
+            raise ValueError("lens: one length for each row of the table is needed")
+    return table.data_ptr(), _table_stride(table), table.shape[1]
+
+
+def kv_fork(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, src: torch.Tensor,
+            dst: torch.Tensor, workspace: torch.Tensor | None = None) -> None:
+    """Rows dst[f] of the table become forks of rows src[f]: full pages are
+    shared, the positions in use of a partly filled last page are copied to a
+    fresh page. dst rows must be empty, distinct and not in src."""
+    _require_cuda(src, dst)
+    _int32(src, "src")
+    _int32(dst, "dst")
+    if src.shape != dst.shape:
+        raise ValueError("kv_fork: src and dst need the same length")
+    c = cache.c()
+    args = _pool_args(table, lens, refs, c.pages)
+    n = src.shape[0]
+    ws = _pages_ws(workspace, c.pages, n, refs.device)
+    _check(lib().nvfp4_kv_fork(c, *args, lens.data_ptr(), table.shape[0], refs.data_ptr(), src.data_ptr(),
+                               dst.data_ptr(), n, ws.data_ptr(), ws.numel(), _stream()), "nvfp4_kv_fork")
+
+
+def kv_release(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seqs: torch.Tensor) -> None:
+    """Give up the sequences of rows seqs (distinct): their pages' counts go
+    down, their entries to -1 and their lengths to 0."""
+    _require_cuda(seqs)
+    _int32(seqs, "seqs")
+    args = _pool_args(table, lens, refs)
+    _check(lib().nvfp4_kv_release(*args, lens.data_ptr(), table.shape[0], refs.data_ptr(), refs.shape[0],
+                                  seqs.data_ptr(), seqs.shape[0], _stream()), "nvfp4_kv_release")
+
+
+def kv_compact(cache: KVCache, table: torch.Tensor, refs: torch.Tensor,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Move the live pages to the ids below their number (pages already there
+    stay); returns that number, int32 on the device."""
+    c = cache.c()
+    args = _pool_args(table, None, refs, c.pages)
+    live = torch.empty((), dtype=torch.int32, device=refs.device)
+    ws = _pages_ws(workspace, c.pages, 0, refs.device)
+    _check(lib().nvfp4_kv_compact(c, *args, table.shape[0], refs.data_ptr(), live.data_ptr(), ws.data_ptr(),
+                                  ws.numel(), _stream()), "nvfp4_kv_compact")
+    return live
 
 
 def read_device_status() -> int:

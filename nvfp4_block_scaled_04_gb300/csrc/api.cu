@@ -57,6 +57,40 @@ bool tensor_ok(const nvfp4_tensor_t& t) {
          (t.scale_layout == NVFP4_SCALES_ROWMAJOR || t.scale_layout == NVFP4_SCALES_MMA);
 }
 
+// a cache as the kernels take it: NVFP4_OK or what is wrong with it
+int cache_check(const nvfp4_kv_cache_t& c) {
+  if (!c.k || !c.v || c.pages < 1 || c.heads < 1) return NVFP4_ERR_INVALID_ARG;
+  if (c.dtype != NVFP4_DTYPE_BF16 && c.dtype != NVFP4_DTYPE_E4M3) return NVFP4_ERR_INVALID_ARG;
+  if (c.dtype == NVFP4_DTYPE_E4M3 && (!c.k_scale || !c.v_scale)) return NVFP4_ERR_INVALID_ARG;
+  if (c.page_size != 16 && c.page_size != 32 && c.page_size != 64 && c.page_size != 128)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (c.head_dim != 64 && c.head_dim != 128) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (c.heads > 1024 || c.pages >= (1ll << 31) / c.heads) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(c.k) || !aligned16(c.v)) return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
+int seqs_check(const nvfp4_kv_seqs_t& s, int64_t tokens, KvSeqs* out) {
+  if (!s.table || !s.lens || s.batch < 1 || s.max_pages < 0 || s.max_new < 1 || tokens < 0 || s.reserved != 0 ||
+      s.table_stride < s.max_pages)
+    return NVFP4_ERR_INVALID_ARG;
+  if (!s.start && tokens != static_cast<int64_t>(s.batch) * s.max_new) return NVFP4_ERR_INVALID_ARG;
+  if (s.batch > 4096 || tokens >= (1ll << 30) || s.max_pages >= (1 << 27)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  *out = {s.table, s.lens, s.start, s.table_stride, tokens, s.batch, s.max_pages, s.max_new};
+  return NVFP4_OK;
+}
+
+// table rows, lengths and reference counts of the calls on whole pools
+int pages_check(const int32_t* table, int64_t table_stride, int max_pages, int rows, const int32_t* refs) {
+  if (!table || !refs || max_pages < 0 || rows < 0 || table_stride < max_pages) return NVFP4_ERR_INVALID_ARG;
+  return NVFP4_OK;
+}
+
+int pages_ws_check(const void* ws, size_t bytes, int64_t pages, int64_t n) {
+  if (!ws || bytes < kv_pages_workspace_bytes(pages, n)) return NVFP4_ERR_WORKSPACE;
+  return aligned16(ws) ? NVFP4_OK : NVFP4_ERR_MISALIGNED;
+}
+
 }  // namespace
 }  // namespace nvfp4
 
@@ -76,6 +110,7 @@ const char* nvfp4_status_string(int status) {
     case NVFP4_ERR_WORKSPACE: return "workspace missing or too small";
     case NVFP4_ERR_TIMEOUT: return "bounded on-device wait timed out";
     case NVFP4_ERR_SCRATCH_LIMIT: return "shape exceeds the fixed scratch of the allocation-free entry point";
+    case NVFP4_ERR_NO_PAGES: return "no free page left in the key-value cache";
     default: return "unknown status";
   }
 }
@@ -96,6 +131,8 @@ size_t nvfp4_workspace_size(int op, int64_t a, int64_t b, int64_t c, int64_t e, 
     case NVFP4_OP_GROUPED_GEMM_W4A4: return grouped_w4a4_workspace_bytes(a, b, c, e, topk);
     case NVFP4_OP_GROUPED_GEMM: return grouped_workspace_bytes(a, b, c, e, topk);
     case NVFP4_OP_GATHER_ARGMAX: return a > 0 && c > 0 ? argmax_workspace_bytes(a, c) : 0;
+    case NVFP4_OP_PAGED_ATTENTION: return attention_workspace_bytes(a, b, c, e, topk);
+    case NVFP4_OP_KV_PAGES: return kv_pages_workspace_bytes(a, b);
     default: return 0;
   }
 }
@@ -272,6 +309,82 @@ int nvfp4_verify_accept(const void* H, int64_t batch, int n_draft, nvfp4_tensor_
   if (!workspace || workspace_bytes < argmax_workspace_bytes(M, W.K)) return NVFP4_ERR_WORKSPACE;
   return launch_gemv_argmax(static_cast<const uint16_t*>(H), M, W, nullptr, out_tokens, nullptr, workspace,
                             reinterpret_cast<cudaStream_t>(stream), draft_ids, n_draft, n_accepted);
+}
+
+int nvfp4_kv_append(nvfp4_kv_cache_t cache, nvfp4_kv_seqs_t seqs, const void* K, int64_t k_stride, const void* V,
+                    int64_t v_stride, int64_t tokens, nvfp4_stream_t stream) {
+  KvSeqs s;
+  if (int rc = cache_check(cache)) return rc;
+  if (int rc = seqs_check(seqs, tokens, &s)) return rc;
+  if (tokens == 0) return NVFP4_OK;
+  const int64_t row = static_cast<int64_t>(cache.heads) * cache.head_dim;
+  if (!K || !V || k_stride < row || v_stride < row) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || k_stride % 8 != 0 || v_stride % 8 != 0) return NVFP4_ERR_MISALIGNED;
+  return launch_kv_append(cache, s, K, V, k_stride, v_stride, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_paged_attention(const void* Q, int64_t q_stride, int q_heads, nvfp4_kv_cache_t cache, nvfp4_kv_seqs_t seqs,
+                          int64_t tokens, int window, int sinks, float scale, void* out, void* workspace,
+                          size_t workspace_bytes, nvfp4_stream_t stream) {
+  KvSeqs s;
+  if (int rc = cache_check(cache)) return rc;
+  if (int rc = seqs_check(seqs, tokens, &s)) return rc;
+  if (q_heads < 1 || q_heads % cache.heads != 0 || window < 0 || sinks < 0 || !(scale - scale == 0.0f))
+    return NVFP4_ERR_INVALID_ARG;
+  if (q_heads / cache.heads > 128) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (tokens == 0) return NVFP4_OK;
+  if (!Q || !out || q_stride < static_cast<int64_t>(q_heads) * cache.head_dim) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(out) || q_stride % 8 != 0) return NVFP4_ERR_MISALIGNED;
+  if (!workspace ||
+      workspace_bytes < attention_workspace_bytes(seqs.batch, seqs.max_new, q_heads, cache.heads, cache.head_dim))
+    return NVFP4_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
+  // positions stay below 2^30, so a longer window or more sinks mean the same
+  const int most = 1 << 30;
+  return launch_paged_attention(static_cast<const uint16_t*>(Q), q_stride, q_heads, cache, s,
+                                window < most ? window : most, sinks < most ? sinks : most, scale,
+                                static_cast<uint16_t*>(out), workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_kv_reserve(nvfp4_kv_seqs_t seqs, int64_t tokens, int page_size, int32_t* table, int32_t* refs, int64_t pages,
+                     void* workspace, size_t workspace_bytes, nvfp4_stream_t stream) {
+  KvSeqs s;
+  if (int rc = seqs_check(seqs, tokens, &s)) return rc;
+  if (table != seqs.table || !refs || pages < 1 || page_size < 1) return NVFP4_ERR_INVALID_ARG;
+  if (pages >= (1ll << 31)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (int rc = pages_ws_check(workspace, workspace_bytes, pages, seqs.batch)) return rc;
+  return launch_kv_reserve(s, page_size, table, refs, pages, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_kv_fork(nvfp4_kv_cache_t cache, int32_t* table, int64_t table_stride, int max_pages, int32_t* lens, int rows,
+                  int32_t* refs, const int32_t* src, const int32_t* dst, int n, void* workspace,
+                  size_t workspace_bytes, nvfp4_stream_t stream) {
+  if (int rc = cache_check(cache)) return rc;
+  if (int rc = pages_check(table, table_stride, max_pages, rows, refs)) return rc;
+  if (!lens || n < 0 || (n > 0 && (!src || !dst))) return NVFP4_ERR_INVALID_ARG;
+  if (n == 0) return NVFP4_OK;
+  if (int rc = pages_ws_check(workspace, workspace_bytes, cache.pages, n)) return rc;
+  return launch_kv_fork(cache, table, table_stride, max_pages, lens, rows, refs, src, dst, n, workspace,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_kv_release(int32_t* table, int64_t table_stride, int max_pages, int32_t* lens, int rows, int32_t* refs,
+                     int64_t pages, const int32_t* seqs, int n, nvfp4_stream_t stream) {
+  if (int rc = pages_check(table, table_stride, max_pages, rows, refs)) return rc;
+  if (!lens || pages < 1 || n < 0 || (n > 0 && !seqs)) return NVFP4_ERR_INVALID_ARG;
+  if (n == 0) return NVFP4_OK;
+  return launch_kv_release(table, table_stride, max_pages, lens, rows, refs, pages, seqs, n,
+                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_kv_compact(nvfp4_kv_cache_t cache, int32_t* table, int64_t table_stride, int max_pages, int rows,
+                     int32_t* refs, int32_t* live, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream) {
+  if (int rc = cache_check(cache)) return rc;
+  if (int rc = pages_check(table, table_stride, max_pages, rows, refs)) return rc;
+  if (!live) return NVFP4_ERR_INVALID_ARG;
+  if (int rc = pages_ws_check(workspace, workspace_bytes, cache.pages, 0)) return rc;
+  return launch_kv_compact(cache, table, table_stride, max_pages, rows, refs, live, workspace,
+                           reinterpret_cast<cudaStream_t>(stream));
 }
 
 int nvfp4_read_device_status(int* out, nvfp4_stream_t stream) {

@@ -67,6 +67,17 @@ NVFP4_DEV uint32_t f32_to_e4m3(float v) {
   return out & 0xFFu;
 }
 
+// Two fp32 -> two E4M3 codes (lo in the low byte), round to nearest even, saturating at 448.
+NVFP4_DEV uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint32_t out;
+  asm("{\n\t.reg .b16 s;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 s, %2, %1;\n\t"
+      "cvt.u32.u16 %0, s;\n\t}"
+      : "=r"(out)
+      : "f"(lo), "f"(hi));
+  return out;
+}
+
 // E4M3 code (0..0x7E) -> fp32 value, from the bit fields (exact).
 NVFP4_DEV float e4m3_to_f32(uint32_t c) {
   const uint32_t e = (c >> 3) & 0xFu, m = c & 7u;

@@ -1,0 +1,35 @@
+// Shared pieces of the paged key-value cache kernels: which sequences a call
+// deals with, and where a sequence's new rows lie.
+#pragma once
+
+#include "launch.h"
+#include "tc_util.cuh"
+
+namespace nvfp4 {
+
+// First new-token row of sequence b (b == batch: one past the last), clamped
+// to the rows the caller's arrays hold.
+NVFP4_DEV int kv_row0(const KvSeqs& s, int b) {
+  const int64_t r = s.start ? static_cast<int64_t>(s.start[b]) : static_cast<int64_t>(b) * s.max_new;
+  return static_cast<int>(r < 0 ? 0 : (r > s.tokens ? s.tokens : r));
+}
+
+// Length of sequence b, inside what position arithmetic in 32 bits can hold.
+NVFP4_DEV int kv_len(const KvSeqs& s, int b) { return min(max(s.lens[b], 0), 1 << 30); }
+
+NVFP4_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// 2^x (2 ulp), zero for -inf.
+NVFP4_DEV float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace nvfp4

@@ -66,6 +66,10 @@ int make_tmap_2d_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t o
 // given byte strides (which may overlap: dimension 2 can step inside 1).
 int make_tmap_3d_u8(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t stride1,
                     int64_t stride2, int box0, int box1, int box2, int swizzle);
+// 4-D uint8 tensor map: dimension 0 contiguous, dimensions 1..3 at the given
+// byte strides (in any order).
+int make_tmap_4d_u8(CUtensorMap* map, const void* base, const int64_t (&dims)[4], const int64_t (&strides)[3],
+                    const int (&box)[4], int swizzle);
 // 2-D 16-bit map (e.g. a bf16 output), rows of row_stride_bytes.
 int make_tmap_2d_u16(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t row_stride_bytes,
                      int box_inner, int box_outer, int swizzle);
@@ -134,5 +138,37 @@ int launch_grouped_w4a4(bool gateup, const uint8_t* a_codes, const uint8_t* a_sc
                         const int* tile_row0, const int* tile_rows, int64_t max_tiles, int inter, int hidden,
                         uint16_t* h_out, unsigned int* amax_bits, uint16_t* y_out, int64_t out_rows, bool pair,
                         cudaStream_t stream);
+
+// ---- paged key-value cache (kv_cache.cu, attention.cu)
+// The sequences of a call (nvfp4_kv_seqs_t) and the number of rows that the
+// caller's arrays of new tokens hold. Lengths, page ids and offsets come from
+// device memory: rows outside [0, tokens), positions below zero or past the
+// table and page ids outside [0, pages) are skipped by every kernel.
+struct KvSeqs {
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* start;     // NULL: max_new new tokens for every sequence
+  int64_t table_stride;
+  int64_t tokens;
+  int batch;
+  int max_pages;
+  int max_new;
+};
+int launch_kv_append(const nvfp4_kv_cache_t& c, const KvSeqs& s, const void* K, const void* V, int64_t k_stride,
+                     int64_t v_stride, cudaStream_t stream);
+size_t kv_pages_workspace_bytes(int64_t pages, int64_t n);
+int launch_kv_reserve(const KvSeqs& s, int page_size, int32_t* table, int32_t* refs, int64_t pages, void* ws,
+                      cudaStream_t stream);
+int launch_kv_fork(const nvfp4_kv_cache_t& c, int32_t* table, int64_t table_stride, int max_pages, int32_t* lens,
+                   int rows, int32_t* refs, const int32_t* src, const int32_t* dst, int n, void* ws,
+                   cudaStream_t stream);
+int launch_kv_release(int32_t* table, int64_t table_stride, int max_pages, int32_t* lens, int rows, int32_t* refs,
+                      int64_t pages, const int32_t* seqs, int n, cudaStream_t stream);
+int launch_kv_compact(const nvfp4_kv_cache_t& c, int32_t* table, int64_t table_stride, int max_pages, int rows,
+                      int32_t* refs, int32_t* live, void* ws, cudaStream_t stream);
+size_t attention_workspace_bytes(int64_t batch, int64_t max_new, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, const nvfp4_kv_cache_t& c,
+                           const KvSeqs& s, int window, int sinks, float scale, uint16_t* out, void* ws,
+                           cudaStream_t stream);
 
 }  // namespace nvfp4

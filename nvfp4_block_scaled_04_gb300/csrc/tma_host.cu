@@ -52,6 +52,23 @@ int make_tmap_3d_u8(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, 
   return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
+int make_tmap_4d_u8(CUtensorMap* map, const void* base, const int64_t (&dims)[4], const int64_t (&strides)[3],
+                    const int (&box)[4], int swizzle) {
+  auto encode = get_encode();
+  if (!encode) return NVFP4_ERR_CUDA;
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    if (i < 3) st[i] = static_cast<cuuint64_t>(strides[i]);
+  }
+  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), d, st, b, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, static_cast<CUtensorMapSwizzle>(swizzle),
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
 int make_tmap_2d_u16(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t row_stride_bytes,
                      int box_inner, int box_outer, int swizzle) {
   auto encode = get_encode();

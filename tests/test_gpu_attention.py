@@ -1,0 +1,228 @@
+"""Attention over a paged key-value cache against its definition in 64 bits.
+
+Bounds. An output is rounded once to bf16: 2^-9 of it, doubled for the fp32
+work before. Each weight p carries a relative error: from its score (fp32
+sums of exact products, |x| below about 50 in powers of two: 2^-17) and from
+its rounding for the second product, 2^-9 at most as one bf16, below 2^-16 as
+two bf16 halves, 2^-11 as one f16. So |error| <= 2^-8 |out| + c sum p |v| with
+c = 2^-8 where one bf16 carries p (blocks of many rows on a bf16 cache) and
+c = 2^-10 elsewhere."""
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_common import DEV, nv
+from tests.kv_oracle import Cache, attention, spread
+
+pytestmark = pytest.mark.gpu
+
+
+def device_cache(m, c):
+    up = lambda t: None if t is None else t.to(DEV)
+    return m.KVCache(up(c.k), up(c.v), up(c.k_scale), up(c.v_scale))
+
+
+def offsets(news):
+    return torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32)
+
+
+def queries(T, heads, dim, seed):
+    return (torch.randn(T, heads, dim, generator=torch.Generator().manual_seed(seed)) * 1.5).bfloat16()
+
+
+def bound(ref, size, rows_of_a_head, kv):
+    c = 2.0 ** -8 if kv == "bf16" and rows_of_a_head > 32 else 2.0 ** -10
+    return 2.0 ** -8 * np.abs(ref) + c * size + 1e-30
+
+
+def check(c, news, group, window=0, sinks=0, scale=None, uniform=False, seed=0):
+    m = nv()
+    T = sum(news)
+    q = queries(T, c.heads * group, c.dim, seed + 77)
+    ref, size = attention(c, q, news, window, sinks, scale)
+    out = torch.full((T, c.heads * group, c.dim), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ws = m.attention_workspace(len(news), max(news), c.heads * group, c.heads, c.dim)
+    args = dict(start=None if uniform else offsets(news).to(DEV), max_new=max(news), window=window, sinks=sinks,
+                scale=scale, workspace=ws)
+    lens = torch.tensor(c.lens, dtype=torch.int32, device=DEV)
+    dc = device_cache(m, c)
+    m.paged_attention(q.to(DEV), dc, c.table.to(DEV), lens, out=out, **args)
+    got = out.float().cpu().double().numpy()
+    assert m.read_device_status() == 0
+    assert np.isfinite(got).all()
+    worst = (np.abs(got - ref) / bound(ref, size, max(news) * group, c.kv)).max()
+    assert worst <= 1.0, worst
+    # the same call again, on the same workspace: the same bits, and the counters are back at zero
+    again = m.paged_attention(q.to(DEV), dc, c.table.to(DEV), lens, **args)
+    assert torch.equal(again.view(torch.int16), out.view(torch.int16))
+    assert not ws[:4096].any()
+    return got
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,group,page,lens", [
+    (1, 1, 16, [1]),
+    (2, 4, 64, [1, 2, 63, 64, 65]),
+    (8, 4, 16, [1999]),
+    (3, 5, 32, [700, 3, 129, 1, 1024, 333]),
+    (1, 8, 128, [5000, 128, 127]),
+    (2, 12, 64, [257, 600]),
+    (1, 27, 32, [513]),
+])
+def test_one_new_token(kv, dim, heads, group, page, lens):
+    c = Cache(lens, heads, page, dim, kv, seed=len(lens) + dim)
+    check(c, [1] * len(lens), group, uniform=True)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,group,dim,page,news,past", [
+    (8, 5, 128, 16, [4] * 5, [517, 0, 64, 1000, 61]),
+    (2, 3, 64, 64, [1, 0, 5, 2, 0], [100, 50, 0, 63, 0]),
+    (1, 1, 128, 32, [8, 8], [120, 2000]),
+    (2, 7, 64, 128, [3, 4], [126, 300]),
+])
+def test_a_few_new_tokens(kv, heads, group, dim, page, news, past):
+    c = Cache([a + b for a, b in zip(news, past)], heads, page, dim, kv, seed=3)
+    check(c, news, group)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,group,dim,page,news,past", [
+    (2, 4, 128, 64, [300], [0]),
+    (1, 5, 128, 16, [1, 130, 257], [0, 77, 600]),
+    (2, 1, 64, 32, [640, 33, 0], [0, 1000, 5]),
+    (1, 3, 64, 128, [129, 127], [1, 128]),
+    (1, 8, 128, 64, [513], [511]),
+    (1, 9, 128, 64, [65, 20], [3, 700]),
+])
+def test_prompts(kv, heads, group, dim, page, news, past):
+    c = Cache([a + b for a, b in zip(news, past)], heads, page, dim, kv, seed=4)
+    check(c, news, group)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 4), (100, 0), (128, 130), (700, 7), (5000, 64)])
+@pytest.mark.parametrize("news,past", [([1, 1, 1], [0, 700, 2100]), ([4, 2], [1000, 126]), ([300, 77], [0, 900])])
+def test_window_and_sinks(kv, dim, window, sinks, news, past):
+    c = Cache([a + b for a, b in zip(news, past)], 2, 32, dim, kv, seed=5)
+    check(c, news, 3, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news,past", [([1, 1], [900, 300]), ([200, 64], [800, 300])])
+def test_pages_given_up_are_not_seen(kv, news, past):
+    """Entries without a page inside and outside the window; ids out of range count as none."""
+    lens = [a + b for a, b in zip(news, past)]
+    c = Cache(lens, 2, 32, 128, kv, seed=6, gaps=[(0, e) for e in range(1, 20)] + [(1, 0), (1, 5)])
+    c.table[0, 3] = c.pages
+    c.table[1, 5] = 2 ** 31 - 1
+    check(c, news, 4)
+    check(c, news, 4, window=300, sinks=3)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [[1, 1, 1], [40, 1, 30]])
+def test_rows_that_see_nothing_are_zero(kv, news):
+    # lengths of zero, lengths below the number of new tokens, no page at all
+    c = Cache([news[0] - 1, 0, 100], 2, 16, 64, kv, seed=7, max_pages=8)
+    c.table[2] = -1
+    got = check(c, news, 2)
+    assert (got[0] == 0).all() and (got[news[0]:] == 0).all()
+
+
+def test_a_scale_of_its_own_and_large_scores():
+    c = Cache([300, 90], 2, 64, 128, "bf16", seed=8)
+    check(c, [1, 1], 4, scale=0.5, uniform=True)
+    check(c, [60, 70], 4, scale=0.25)
+
+
+@pytest.mark.parametrize("magnitude", [1e-30, 1e30])
+def test_queries_of_any_magnitude_on_an_8_bit_cache(magnitude):
+    m = nv()
+    c = Cache([200], 2, 16, 128, "e4m3", seed=9)
+    q = (queries(1, 8, 128, 1).double() * magnitude).bfloat16()
+    scale = 128 ** -0.5 / magnitude
+    ref, size = attention(c, q, [1], scale=scale)
+    got = m.paged_attention(q.to(DEV), device_cache(m, c), c.table.to(DEV), torch.tensor(c.lens, dtype=torch.int32,
+                                                                                          device=DEV), scale=scale)
+    got = got.float().cpu().double().numpy()
+    assert (np.abs(got - ref) <= bound(ref, size, 4, "e4m3")).all()
+
+
+@pytest.mark.parametrize("news", [[1, 1], [70, 90]])
+def test_nan_in_a_visible_place_shows(news):
+    m = nv()
+    c = Cache([100, 100], 1, 16, 64, "bf16", seed=10)
+    c.k[int(c.table[0, 0]), 0, 3, 5] = float("nan")
+    q = queries(sum(news), 2, 64, 3)
+    got = m.paged_attention(q.to(DEV), device_cache(m, c), c.table.to(DEV),
+                            torch.tensor(c.lens, dtype=torch.int32, device=DEV), start=offsets(news).to(DEV),
+                            max_new=max(news)).float().cpu()
+    assert torch.isnan(got[:news[0]]).all() and torch.isfinite(got[news[0]:]).all()
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [5, 2, 3], [90, 40, 8]])
+def test_layouts_of_the_arguments(news):
+    """q as a slice of a fused projection, a wider table, strided lengths' views, another stream."""
+    m = nv()
+    lens = [n + p for n, p in zip(news, [300, 17, 64])]
+    c = Cache(lens, 2, 16, 64, "bf16", seed=11)
+    T = sum(news)
+    qkv = torch.randn(T, 8 + 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
+    ref, size = attention(c, qkv[:, :8], news)
+    wide = torch.full((3, c.max_pages + 5), 2 ** 30, dtype=torch.int32)
+    wide[:, 2:2 + c.max_pages] = c.table
+    dev_wide = wide.to(DEV)
+    lens_d = torch.tensor([9] + lens, dtype=torch.int32, device=DEV)[1:]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    dc, fused, start = device_cache(m, c), qkv.to(DEV), offsets(news).to(DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = m.paged_attention(fused[:, :8], dc, dev_wide[:, 2:2 + c.max_pages], lens_d, start=start, max_new=max(news))
+    side.synchronize()
+    got = got.float().cpu().double().numpy()
+    assert (np.abs(got - ref) <= bound(ref, size, max(news) * 4, "bf16")).all()
+
+
+@pytest.mark.parametrize("kv,news", [("bf16", 1), ("e4m3", 1), ("bf16", 80)])
+def test_pools_past_4_gb(kv, news):
+    """The pages in use are the last ones of pools of more than 2^32 bytes (and elements)."""
+    m = nv()
+    size = 2 if kv == "bf16" else 1
+    c = Cache([700 + news], 4, 64, 128, kv, seed=12)
+    page_bytes = 4 * 64 * 128 * size
+    pages = (1 << 32) * 5 // 4 * size // page_bytes
+    dtype = c.k.dtype
+    pools = []
+    for pool in (c.k, c.v):
+        big = torch.empty(pages, 4, 64, 128, dtype=dtype, device=DEV)
+        big[-c.pages:].view(torch.uint8).copy_(pool.view(torch.uint8))
+        pools.append(big)
+    up = lambda t: None if t is None else t.to(DEV)
+    cache = m.KVCache(*pools, up(c.k_scale), up(c.v_scale))
+    table = torch.where(c.table >= 0, c.table + (pages - c.pages), c.table)
+    q = queries(news, 16, 128, 2)
+    ref, a = attention(c, q, [news])
+    got = m.paged_attention(q.to(DEV), cache, table.to(DEV), torch.tensor(c.lens, dtype=torch.int32, device=DEV),
+                            max_new=news).float().cpu().double().numpy()
+    assert (np.abs(got - ref) <= bound(ref, a, news * 4, kv)).all()
+
+
+def test_many_sequences():
+    c = Cache(spread(1, 60, 700, 1), 1, 16, 64, "bf16", seed=13)
+    check(c, [1] * 700, 2, uniform=True)
+
+
+def test_more_new_tokens_than_announced_are_computed():
+    m = nv()
+    c = Cache([150, 20], 1, 16, 64, "bf16", seed=14)
+    news = [50, 9]
+    q = queries(59, 2, 64, 5)
+    ref, size = attention(c, q, news)
+    got = m.paged_attention(q.to(DEV), device_cache(m, c), c.table.to(DEV),
+                            torch.tensor(c.lens, dtype=torch.int32, device=DEV), start=offsets(news).to(DEV), max_new=3)
+    got = got.float().cpu().double().numpy()
+    assert (np.abs(got - ref) <= bound(ref, size, 6, "bf16")).all()
