@@ -1,7 +1,10 @@
 // Attention over a paged key-value cache: which kernel a call takes.
 #include "attention_rows.cuh"
+#include "attention_tiles.cuh"
 #include "kv.cuh"
 #include "launch.h"
+
+#include <algorithm>
 
 namespace nvfp4 {
 
@@ -42,23 +45,56 @@ int launch_rows_nt(int nt, const ArParams& p, const CUtensorMap& mk, const CUten
   }
 }
 
-// One page of one head as [halves][rows][seg bytes], a copy box of `box` rows of it.
-int kv_map(CUtensorMap* map, const void* pool, const nvfp4_kv_cache_t& c, int box) {
+// One page of one head as [halves][rows][seg bytes], a copy box of `box` rows of `box_halves` halves.
+int kv_map(CUtensorMap* map, const void* pool, const nvfp4_kv_cache_t& c, int box, int box_halves) {
   const int64_t row = static_cast<int64_t>(c.head_dim) * (c.dtype == NVFP4_DTYPE_BF16 ? 2 : 1);
   const int64_t seg = row >= 128 ? 128 : 64, halves = row / seg;
   const int64_t dims[4] = {seg, c.page_size, halves, c.pages * c.heads};
   const int64_t strides[3] = {row, halves > 1 ? seg : row * c.page_size, row * c.page_size};
-  const int boxes[4] = {static_cast<int>(seg), box, static_cast<int>(halves), 1};
+  const int boxes[4] = {static_cast<int>(seg), box, box_halves, 1};
   return make_tmap_4d_u8(map, pool, dims, strides, boxes,
                          seg == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
+
+// Blocks of rows (256 at most, whole tokens) and kv heads of a call of the tile kernel, at most.
+int64_t tiles_items(int64_t tokens, int64_t batch, int64_t heads, int group) {
+  return heads * (tokens / (2 * (AT_ROWS / group)) + batch);
+}
+
+template <int D>
+int launch_tiles(const uint16_t* Q, int64_t q_stride, int q_heads, const nvfp4_kv_cache_t& c, AtParams& p,
+                 cudaStream_t stream) {
+  CUtensorMap mq, mk, mv;
+  const int64_t q_dims[4] = {128, q_heads, p.s.tokens, D / 64};
+  const int64_t q_strides[3] = {D * 2, q_stride * 2, 128};
+  const int q_box[4] = {128, p.group, AT_ROWS / p.group, 1};
+  if (int rc = make_tmap_4d_u8(&mq, Q, q_dims, q_strides, q_box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
+  const int box = c.page_size < AT_TILE ? c.page_size : AT_TILE;
+  if (int rc = kv_map(&mk, c.k, c, box, 1)) return rc;
+  if (int rc = kv_map(&mv, c.v, c, box, 1)) return rc;
+  const int64_t items = tiles_items(p.s.tokens, p.s.batch, c.heads, p.group);
+  const int ctas = sm_count();
+  // fewer items than half the SMs: each is split over its positions
+  p.parts = items < ctas ? static_cast<int>(ctas / items) : 1;
+  const int64_t units = items * p.parts;
+  const int rc = ensure_smem(attention_tiles_kernel<D>, AtShape<D>::SMEM);
+  if (rc) return rc;
+  return launch_ex(attention_tiles_kernel<D>, dim3(static_cast<unsigned>(units < ctas ? units : ctas)), dim3(AT_THREADS),
+                   AtShape<D>::SMEM, 1, true, stream, mq, mk, mv, p);
+}
+
+// Rows of a kv head from which the tile kernel takes a call.
+bool takes_tiles(int64_t rows) { return rows > 32; }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t batch, int64_t max_new, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
   if (batch <= 0 || max_new <= 0 || kv_heads <= 0 || q_heads <= 0 || head_dim <= 0) return 0;
-  const int nt = rows_nt(max_new * (q_heads / kv_heads));
-  return static_cast<size_t>(COUNTER_BYTES + static_cast<int64_t>(rows_grid(nt)) * 2 * 8 * nt * (head_dim + 2) * 4);
+  const int64_t rows = max_new * (q_heads / kv_heads);
+  const int nt = rows_nt(rows);
+  int64_t parts = static_cast<int64_t>(rows_grid(nt)) * 2 * 8 * nt;               // rows of partial sums
+  if (takes_tiles(rows)) parts = std::max(parts, static_cast<int64_t>(sm_count()) * 2 * AT_ROWS);
+  return static_cast<size_t>(COUNTER_BYTES + parts * (head_dim + 2) * 4);
 }
 
 int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, const nvfp4_kv_cache_t& c,
@@ -67,12 +103,32 @@ int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, con
   int* status = device_status_ptr();
   if (!status) return NVFP4_ERR_CUDA;
   const int group = q_heads / c.heads;
-  const int nt = rows_nt(static_cast<int64_t>(s.max_new) * group);
+  const int64_t rows = static_cast<int64_t>(s.max_new) * group;
+  if (takes_tiles(rows) && c.dtype == NVFP4_DTYPE_BF16 && group <= AT_ROWS / 2 && scale > 0.0f) {
+    AtParams p;
+    p.s = s;
+    p.out = out;
+    p.pages = c.pages;
+    p.heads = c.heads;
+    p.group = group;
+    p.page_size = c.page_size;
+    p.page_log2 = log2_of(c.page_size);
+    p.window = window;
+    p.sinks = sinks;
+    p.scale = scale * LOG2_E;
+    p.arrived = static_cast<unsigned*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + COUNTER_BYTES);
+    p.status = status;
+    return c.head_dim == 128 ? launch_tiles<128>(Q, q_stride, q_heads, c, p, stream)
+                             : launch_tiles<64>(Q, q_stride, q_heads, c, p, stream);
+  }
+  const int nt = rows_nt(rows);
   if (4 * rows_grid(nt) > COUNTER_BYTES) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   CUtensorMap mk, mv;
   const int box = c.page_size < AR_TILE ? c.page_size : AR_TILE;
-  if (int rc = kv_map(&mk, c.k, c, box)) return rc;
-  if (int rc = kv_map(&mv, c.v, c, box)) return rc;
+  const int halves = c.head_dim == 128 && c.dtype == NVFP4_DTYPE_BF16 ? 2 : 1;
+  if (int rc = kv_map(&mk, c.k, c, box, halves)) return rc;
+  if (int rc = kv_map(&mv, c.v, c, box, halves)) return rc;
   ArParams p;
   p.s = s;
   p.q = Q;

@@ -132,32 +132,6 @@ NVFP4_DEV bool ar_all(bool pred) {
 }
 NVFP4_DEV void ar_consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(AR_WARPS * 32) : "memory"); }
 
-// The tiles that a block of rows sees: [0, st) (sinks) and [w0, end).
-struct ArTiles {
-  int st, w0, count;
-  NVFP4_DEV int tile(int i) const { return i < st ? i : w0 + (i - st); }
-};
-
-// Tiles of the rows at positions p0..p1 (p1 < 0: none).
-NVFP4_DEV ArTiles ar_tiles(int p0, int p1, int window, int sinks, int key_end) {
-  ArTiles t;
-  const int end = (min(p1 + 1, key_end) + AR_TILE - 1) / AR_TILE;   // one past the last
-  t.st = 0;
-  t.w0 = 0;
-  if (window > 0) {
-    const int lo = p0 - window + 1;                                  // first position in a window
-    const int w0 = lo > 0 ? lo / AR_TILE : 0;
-    const int st = min((min(sinks, key_end) + AR_TILE - 1) / AR_TILE, end);
-    if (w0 > st) {
-      t.st = st;
-      t.w0 = w0;
-    }
-  }
-  t.count = end > t.w0 ? t.st + end - t.w0 : t.st;
-  if (end <= 0) t.count = 0;
-  return t;
-}
-
 // A piece of the line of tiles that lies inside one item.
 struct ArSeg {
   int b, h, rb;          // sequence, kv head, block of rows
@@ -219,7 +193,7 @@ NVFP4_DEV unsigned ar_seq_tiles(const ArParams& p, int b) {
     const int64_t all = (max(key_end, 0) + AR_TILE - 1) / AR_TILE;
     most = static_cast<int>(st + w < all ? st + w : all);
   } else {
-    most = ar_tiles(len - n, len - 1, p.window, p.sinks, key_end).count;
+    most = kv_tiles<AR_TILE>(len - n, len - 1, p.window, p.sinks, key_end).count;
   }
   return static_cast<unsigned>(max(most, 1)) * static_cast<unsigned>(blocks * p.heads);
 }
@@ -305,7 +279,7 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
     while (ok && walk.next(g)) {
       const int key_end = static_cast<int>(cap < g.len ? cap : g.len);
       const int r0 = g.rb * ROWS, r1 = min(r0 + ROWS, g.n * p.group) - 1;
-      const ArTiles tl = ar_tiles(g.len - g.n + r0 / p.group, g.len - g.n + r1 / p.group, p.window, p.sinks, key_end);
+      const KvTiles tl = kv_tiles<AR_TILE>(g.len - g.n + r0 / p.group, g.len - g.n + r1 / p.group, p.window, p.sinks, key_end);
       const int i1 = min(g.i1, tl.count);
       const int32_t* row = p.s.table + static_cast<int64_t>(g.b) * p.s.table_stride;
       // page ids of 32 boxes at a time, one per lane
@@ -372,7 +346,7 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
     const int key_end = static_cast<int>(cap < g.len ? cap : g.len);
     const int r0 = g.rb * ROWS, n_rows = min(ROWS, g.n * p.group - r0);
     const int p0 = g.len - g.n + r0 / p.group, p1 = g.len - g.n + (r0 + n_rows - 1) / p.group;
-    const ArTiles tl = ar_tiles(p0, p1, p.window, p.sinks, key_end);
+    const KvTiles tl = kv_tiles<AR_TILE>(p0, p1, p.window, p.sinks, key_end);
     const int i1 = min(g.i1, tl.count);
     // query fragments (B of m16n8k16: k = d, n = row), one eight-row tile per warp
     if (warp < NT) {

@@ -1,0 +1,678 @@
+// Attention of many new rows over a paged key-value cache on the
+// 5th-generation tensor cores: prompts and chunks of prompts, causal, with an
+// optional sliding window and sinks.
+//
+// The mathematics is attention_rows.cuh's: per row a running maximum m, l =
+// sum 2^(x - m) and o = sum 2^(x - m) v over the tiles that the row sees, with
+// x the score in powers of two. The rows of one kv head share its keys and
+// values, so a 128-row tile packs (token, query head) pairs: 128 / G tokens of
+// all G heads. The running maximum that o is kept relative to moves only when
+// it would grow by more than 2^8 (p stays below 2^8, far inside bf16 and
+// fp32), so o is rescaled in tensor memory a few times per row, not per tile.
+//
+// What bounds it: 4 * 128 * 128 * D flops per (row tile, 128 positions); K and
+// V come from L2 mostly. Per SM 1024 tensor clocks a tile at D = 128, against
+// 16384 exponentials. So two row tiles (A, B) share every K and V tile and
+// take turns: while one warpgroup turns S_A into P_A the tensor cores do
+// O_B += P_B V and the next S_B = Q_B K^T.
+//   warps 0..3, 4..7  softmax of row tile A, B: a thread owns a row (a
+//                     tensor-memory lane), reads S, writes P over it (bf16
+//                     pairs), and at the end reads O, divides and writes out
+//   warp 8            producer: hands out work items, loads Q, K and V (a box
+//                     per page and 64 d's) by TMA
+//   warp 9            tensor-memory allocation; lane 0 issues the MMAs
+//   warp 10           zeroes value rows no row of the item sees (they may hold
+//                     anything, and 0 * NaN is not 0)
+// S and P of a tile share 128 columns: S(j + 1) is issued after O += P(j) V(j),
+// and the tensor cores run one thread's MMAs in order. For the same reason a
+// finished S(j + 1) says that O += P(j) V(j) is finished, so the softmax warps
+// may rescale O before they publish P(j + 1).
+//
+// Roundings: q, k, v as they are, products exact, sums fp32; p is rounded to
+// one bf16 (2^-9) for the second product, as the tensor cores take it. Two
+// halves would cost a third more tensor time and halve an error that is that
+// of the output's own rounding.
+//
+// Few items (a short chunk on a long context) are split over the positions:
+// each part leaves (m, l, o) in the workspace and the last part of a row tile
+// to arrive joins them in order.
+//
+// Every wait is bounded; one that gives up raises the CTA's abort flag, every
+// role leaves its loop, and nothing more is written.
+#pragma once
+
+#include "kv.cuh"
+#include "tcgen05.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int AT_ROWS = 128;                 // rows of a row tile
+constexpr int AT_TILE = 128;                 // positions of a key tile
+constexpr int AT_K = 3, AT_V = 2;            // rings of K and V tiles
+constexpr int AT_SLOTS = AT_K + AT_V;        // ring slots: K's, then V's
+constexpr int AT_ITEMS = 2;                  // items announced ahead
+constexpr int AT_OKS = 8;                    // announced page masks of tiles
+constexpr int AT_SOFTMAX_WARPS = 8;
+constexpr int AT_PROD_WARP = 8, AT_MMA_WARP = 9, AT_CLEAN_WARP = 10;
+constexpr int AT_THREADS = 12 * 32;          // warp 11 only gives its registers away
+// registers a thread: the launch's 168 for 384 threads (64512 in all), moved
+// from the third warpgroup to the softmax ones (256 x 208 + 128 x 80 = 63488)
+constexpr int AT_REGS_SOFTMAX = 208, AT_REGS_OTHER = 80;
+static_assert(256 * AT_REGS_SOFTMAX + 128 * AT_REGS_OTHER <= AT_THREADS * 168, "register split");
+constexpr float AT_SLACK = 8.0f;             // powers of two that p may exceed 1 by
+// slot full / empty / clean, item full / empty, q full / empty, s full, p full, o full, join (each for A and B), drain
+constexpr int AT_BARS = 3 * AT_SLOTS + 2 * AT_ITEMS + 2 + 8 + 1;
+
+struct AtItem {
+  int done;
+  int h;                 // kv head
+  int row0, n_tok;       // first new-token row, tokens
+  int p0;                // first position
+  int key_end;           // positions at or past it hold nothing
+  int st, w0, i0, i1;    // tiles (KvTiles) and the part of them that is this item's
+  int item, part;        // index of the unsplit item, part of it
+};
+
+struct AtParams {
+  KvSeqs s;
+  uint16_t* out;
+  int64_t pages;
+  int heads, group;
+  int page_size, page_log2;
+  int window, sinks;
+  float scale;           // softmax scale * log2 e, > 0
+  int parts;             // parts of an item (1: no split)
+  unsigned* arrived;     // [items][2], zero between calls (split only)
+  float* part;           // [items][parts][2][128][D + 2]
+  int* status;
+};
+
+template <int D>
+struct AtShape {
+  static constexpr int HALVES = D / 64;
+  static constexpr int MAT_BYTES = AT_TILE * D * 2;       // Q row tile, K tile or V tile
+  static constexpr int SMEM = (2 + AT_SLOTS) * MAT_BYTES + AT_ITEMS * static_cast<int>(sizeof(AtItem)) + AT_OKS * 4 +
+                              AT_BARS * 8 + 64 + 1024;
+  static constexpr int O_COL0 = 256;                       // tensor memory: S_A, S_B, O_A, O_B
+};
+
+NVFP4_DEV void tc_mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+NVFP4_DEV void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+NVFP4_DEV void tc_st_32cols(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+NVFP4_DEV void fma2(float& a, float& b, float c, float d) {   // (a, b) = (a, b) * c + d
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+NVFP4_DEV void add2(float& a, float& b, float c, float d) {   // (a, b) += (c, d)
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
+// A word with its lowest n bits set (none for n <= 0).
+NVFP4_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// Whether the tile at position j0 has positions that no row of p0..p1 sees.
+NVFP4_DEV bool at_unclean(int j0, int p0, int p1, int window, int sinks) {
+  if (j0 + AT_TILE - 1 > p1) return true;
+  return window > 0 && p0 - window >= max(j0, sinks) && sinks < j0 + AT_TILE;
+}
+
+template <int D>
+__global__ void __launch_bounds__(AT_THREADS, 1)
+    attention_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                           const __grid_constant__ CUtensorMap map_v, const AtParams p) {
+  using S = AtShape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* at = smem_raw + (base - raw) + (2 + AT_SLOTS) * S::MAT_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(at);
+  AtItem* items = reinterpret_cast<AtItem*>(bars + AT_BARS);
+  unsigned* oks = reinterpret_cast<unsigned*>(items + AT_ITEMS);
+  uint32_t* tmem_slot = oks + AT_OKS;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  unsigned* last_flag = tmem_slot + 2;   // [2]
+  const uint32_t bar0 = smem_addr(bars);
+  auto kv_full = [&](int s) { return bar0 + 8u * s; };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (AT_SLOTS + s); };
+  auto kv_clean = [&](int s) { return bar0 + 8u * (2 * AT_SLOTS + s); };
+  auto item_full = [&](int s) { return bar0 + 8u * (3 * AT_SLOTS + s); };
+  auto item_empty = [&](int s) { return bar0 + 8u * (3 * AT_SLOTS + AT_ITEMS + s); };
+  constexpr int B1 = 3 * AT_SLOTS + 2 * AT_ITEMS;
+  const uint32_t q_full = bar0 + 8u * B1, q_empty = bar0 + 8u * (B1 + 1);
+  auto s_full = [&](int x) { return bar0 + 8u * (B1 + 2 + x); };
+  auto p_full = [&](int x) { return bar0 + 8u * (B1 + 4 + x); };
+  auto o_full = [&](int x) { return bar0 + 8u * (B1 + 6 + x); };
+  auto join_bar = [&](int x) { return bar0 + 8u * (B1 + 8 + x); };
+  const uint32_t drain_bar = bar0 + 8u * (B1 + 10);
+  auto q_tile = [&](int x) { return base + x * S::MAT_BYTES; };
+  auto slot = [&](int s) { return base + (2 + s) * S::MAT_BYTES; };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < AT_SLOTS; ++s) {
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_empty(s), 1);
+      mbar_init(kv_clean(s), 1);
+    }
+    for (int s = 0; s < AT_ITEMS; ++s) {
+      mbar_init(item_full(s), 1);
+      mbar_init(item_empty(s), AT_SOFTMAX_WARPS + 2);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full(x), 1);
+      mbar_init(p_full(x), AT_SOFTMAX_WARPS / 2);
+      mbar_init(o_full(x), 1);
+      mbar_init(join_bar(x), AT_SOFTMAX_WARPS / 2);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+  }
+  if (warp == AT_MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "n"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const int tile_tok = AT_ROWS / p.group;      // tokens of a row tile
+  const int item_tok = 2 * tile_tok;
+  const int box = p.page_size < AT_TILE ? p.page_size : AT_TILE;
+  const int boxes = AT_TILE / box;
+
+  // waits of a whole warp
+  auto wait = [&](uint32_t bar, int parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, static_cast<uint32_t>(parity), abort_flag, p.status)) != 0;
+  };
+  // the k-th announced item, for the roles that read it; false: no more
+  auto get_item = [&](int k, AtItem& g) {
+    const int s = k % AT_ITEMS;
+    if (!wait(item_full(s), (k / AT_ITEMS) & 1)) return false;
+    g = items[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_empty(s));
+    return g.done == 0;
+  };
+  // the ring slot of the n-th K (or V) tile and the parity of that use
+  auto k_slot = [&](int n) { return n % AT_K; };
+  auto v_slot = [&](int n) { return AT_K + n % AT_V; };
+  auto k_par = [&](int n) { return (n / AT_K) & 1; };
+  auto v_par = [&](int n) { return (n / AT_V) & 1; };
+  auto tile_pos = [&](const AtItem& g, int i) { return (i < g.st ? i : g.w0 + (i - g.st)) * AT_TILE; };
+
+  if (warp < AT_SOFTMAX_WARPS) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AT_REGS_SOFTMAX));
+    // ----------------------------------------------------------------- softmax
+    const int x = warp >> 2;                                       // row tile
+    const int r = (warp & 3) * 32 + lane;                          // row: tensor-memory lane
+    const int my_tok = r / p.group, my_head = r - my_tok * p.group;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_cols = lane_base + AT_TILE * x, o_cols = lane_base + S::O_COL0 + D * x;
+    const unsigned all_boxes = (1u << boxes) - 1u;
+    const float c = p.scale;
+    int tiles = 0, used = 0, outs = 0, joins = 0;   // tiles of the CTA, of this row tile, finished items, meetings
+    auto meet = [&]() {   // of the row tile's four warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(join_bar(x));
+      return wait(join_bar(x), joins++ & 1);
+    };
+    AtItem g;
+    for (int k = 0; get_item(k, g); ++k) {
+      const int nt = g.i1 - g.i0;
+      const bool active = x == 0 || g.n_tok > tile_tok;
+      if (!active) {
+        tiles += max(nt, 0);
+        continue;
+      }
+      const int tok = x * tile_tok + my_tok;                       // token of the item
+      const bool live = my_tok < tile_tok && tok < g.n_tok;
+      const int pos = g.p0 + min(tok, g.n_tok - 1);
+      float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      bool ok = true;
+      for (int i = g.i0; i < g.i1; ++i, ++tiles, ++used) {
+        ok = wait(s_full(x), used & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tc_ld_32cols(s_cols + 32 * q, v[q]);
+        const int j0 = tile_pos(g, i);
+        const unsigned there = oks[tiles % AT_OKS];
+        // this row sees columns 0..hi of the tile but for sk..lo - 1
+        const int hi = min(pos, g.key_end - 1) - j0;
+        const int lo = p.window > 0 ? pos - p.window + 1 - j0 : 0, sk = p.window > 0 ? p.sinks - j0 : 0;
+        const bool whole = hi >= AT_TILE - 1 && (lo <= 0 || sk >= AT_TILE) && there == all_boxes;
+        tc_wait_ld();
+        if (!__all_sync(0xffffffffu, whole)) {
+          const int box_log2 = 31 - __clz(box);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            // bit e: this row sees column 32 q + e
+            const uint32_t page_bits = (((there >> ((32 * q) >> box_log2)) & 1u) ? 0x0000FFFFu : 0u) |
+                                       (((there >> ((32 * q + 16) >> box_log2)) & 1u) ? 0xFFFF0000u : 0u);
+            const uint32_t sees = low_bits(hi + 1 - 32 * q) & (~low_bits(lo - 32 * q) | low_bits(sk - 32 * q)) & page_bits;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(sees & (1u << e))) v[q][e] = 0xFF800000u;   // -inf
+          }
+        }
+        // the row's maximum, four chains
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = __uint_as_float(v[q][0]);
+#pragma unroll
+          for (int e = 1; e < 31; e += 2)
+            mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(v[q][e])), __uint_as_float(v[q][e + 1]));
+          mx[q] = fmaxf(mx[q], __uint_as_float(v[q][31]));
+        }
+        const float mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+        const bool grows = (mn - m) * c > AT_SLACK;
+        if (__any_sync(0xffffffffu, grows)) {
+          const float alpha = grows ? exp2_approx((m - mn) * c) : 1.0f;
+          if (grows) m = mn;
+          l0 *= alpha;
+          l1 *= alpha;
+          if (i > g.i0) {
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tc_ld_16cols(o_cols + 16 * q, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tc_st_16cols(o_cols + 16 * q, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.0f : -m * c;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a = __uint_as_float(v[q][2 * e]), b = __uint_as_float(v[q][2 * e + 1]);
+            fma2(a, b, c, neg);
+            a = exp2_approx(a);
+            b = exp2_approx(b);
+            add2(l0, l1, a, b);
+            w[e] = f32x2_to_bf16x2(a, b);
+          }
+          tc_st_16cols(s_cols + 16 * q, w);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(x));
+      }
+      if (!ok) break;
+      float l = l0 + l1;
+      if (nt > 0) {
+        ok = wait(o_full(x), outs & 1);
+        if (!ok) break;
+        ++outs;
+        tc_fence_after();
+      }
+      uint16_t* dst = p.out + (static_cast<int64_t>(g.row0 + tok) * p.heads * p.group + static_cast<int64_t>(g.h) * p.group + my_head) * D;
+      if (p.parts == 1) {
+        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // a NaN stays one
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          if (nt > 0) {
+            tc_ld_32cols(o_cols + 32 * q, o);
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                y[z] = f32x2_to_bf16x2(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + 32 * q + e) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+        }
+        tc_fence_before();
+        continue;
+      }
+      // this part's (m, l, o); the last part of the row tile to arrive joins them in order
+      auto part = [&](int i) {
+        return p.part + ((static_cast<int64_t>(g.item) * p.parts + i) * 2 + x) * (AT_ROWS * (D + 2));
+      };
+      {
+        float* mine = part(g.part);
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          if (nt > 0) {
+            tc_ld_32cols(o_cols + 32 * q, o);
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            __stcg(reinterpret_cast<float4*>(mine + r * D + 32 * q + e),
+                   make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                               __uint_as_float(o[e + 3])));
+        }
+        __stcg(reinterpret_cast<float2*>(mine + AT_ROWS * D + 2 * r), make_float2(m * c, l));
+        tc_fence_before();
+      }
+      fence_acq_rel_gpu();
+      if (!meet()) break;
+      if ((threadIdx.x & 127) == 0) {
+        unsigned* counter = p.arrived + g.item * 2 + x;
+        const unsigned before = atomicAdd(counter, 1u);
+        last_flag[x] = before + 1 == static_cast<unsigned>(p.parts);
+        if (before + 1 == static_cast<unsigned>(p.parts)) *counter = 0;   // ready for the next call
+        fence_acq_rel_gpu();
+      }
+      if (!meet()) break;
+      if (last_flag[x] && live) {
+        fence_acq_rel_gpu();
+        float mx = -INFINITY;
+        for (int i = 0; i < p.parts; ++i) mx = fmaxf(mx, __ldcg(part(i) + AT_ROWS * D + 2 * r));
+        const float use = mx == -INFINITY ? 0.0f : mx;
+        float sum = 0.0f;
+        for (int i = 0; i < p.parts; ++i) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + AT_ROWS * D + 2 * r));
+          sum += ml.y * exp2_approx(ml.x - use);
+        }
+        const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+#pragma unroll 1
+        for (int q = 0; q < D / 16; ++q) {
+          float acc[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+#pragma unroll 2
+          for (int i = 0; i < p.parts; ++i) {
+            const float f = exp2_approx(__ldcg(part(i) + AT_ROWS * D + 2 * r) - use) * inv;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(part(i) + r * D + 16 * q + e));
+              acc[e] += y.x * f;
+              acc[e + 1] += y.y * f;
+              acc[e + 2] += y.z * f;
+              acc[e + 3] += y.w * f;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            *reinterpret_cast<uint4*>(dst + 16 * q + e) =
+                make_uint4(f32x2_to_bf16x2(acc[e], acc[e + 1]), f32x2_to_bf16x2(acc[e + 2], acc[e + 3]),
+                           f32x2_to_bf16x2(acc[e + 4], acc[e + 5]), f32x2_to_bf16x2(acc[e + 6], acc[e + 7]));
+        }
+      }
+      if (!meet()) break;   // the flag may be written again
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AT_REGS_OTHER));
+    if (warp == AT_PROD_WARP) {
+      // ---------------------------------------------------------------- producer
+      const int64_t table_end = static_cast<int64_t>(p.s.max_pages) * p.page_size;
+      int tiles = 0, asked[2] = {0, 0}, q_used = 0;   // tiles done, K and V tiles requested, items whose Q was
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        // work item w: (sequence, block of its rows, kv head, part), the parts of
+        // a block next to each other, then its heads; late blocks, which see
+        // more, come first
+        const int64_t w = blockIdx.x + static_cast<int64_t>(k) * gridDim.x;
+        const int64_t flat = w / (p.parts * p.heads);
+        const int rest = static_cast<int>(w - flat * (p.parts * p.heads));
+        AtItem g = {};
+        g.done = 1;
+        g.h = rest / p.parts;
+        g.part = rest - g.h * p.parts;
+        g.item = static_cast<int>(w / p.parts);
+        const int32_t* row = p.s.table;
+        int64_t run = 0;
+        for (int b0 = 0; b0 < p.s.batch && g.done; b0 += 32) {
+          const int b = b0 + lane;
+          const int r0 = b < p.s.batch ? kv_row0(p.s, b) : 0;
+          const int n = b < p.s.batch ? max(kv_row0(p.s, b + 1) - r0, 0) : 0;
+          const int blocks = (n + item_tok - 1) / item_tok;
+          int x = blocks;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, run + x > flat);
+          if (hit) {
+            const int src = __ffs(hit) - 1;
+            const int n_b = __shfl_sync(0xffffffffu, n, src), r0_b = __shfl_sync(0xffffffffu, r0, src);
+            const int nb = __shfl_sync(0xffffffffu, blocks, src), before = __shfl_sync(0xffffffffu, x, src) - nb;
+            const int blk = nb - 1 - static_cast<int>(flat - run - before);
+            const int len = kv_len(p.s, b0 + src);
+            g.done = 0;
+            g.row0 = r0_b + blk * item_tok;
+            g.n_tok = min(item_tok, n_b - blk * item_tok);
+            g.p0 = len - n_b + blk * item_tok;
+            g.key_end = static_cast<int>(min(table_end, static_cast<int64_t>(len)));
+            const KvTiles tl = kv_tiles<AT_TILE>(g.p0, g.p0 + g.n_tok - 1, p.window, p.sinks, g.key_end);
+            g.st = tl.st;
+            g.w0 = tl.w0;
+            g.i0 = static_cast<int>(static_cast<int64_t>(tl.count) * g.part / p.parts);
+            g.i1 = static_cast<int>(static_cast<int64_t>(tl.count) * (g.part + 1) / p.parts);
+            row = p.s.table + static_cast<int64_t>(b0 + src) * p.s.table_stride;
+          }
+          run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        const int slot_i = k % AT_ITEMS;
+        if (k >= AT_ITEMS && !(ok = wait(item_empty(slot_i), ((k / AT_ITEMS) - 1) & 1))) break;
+        if (lane == 0) {
+          items[slot_i] = g;
+          mbar_arrive(item_full(slot_i));
+        }
+        if (g.done) break;
+        if (g.i1 <= g.i0) continue;
+        auto page_of = [&](int i) {   // lane's box of tile i: its page, -1 where there is none
+          const int j = tile_pos(g, i) + (lane & (boxes - 1)) * box;
+          const int e = j >> p.page_log2;
+          const int page = j < g.key_end && e < p.s.max_pages ? row[e] : -1;
+          return page >= 0 && page < p.pages ? page : -1;
+        };
+        int page = page_of(g.i0);
+        // both row tiles of Q, once the last item's MMAs have read theirs
+        if (q_used > 0 && !(ok = wait(q_empty, (q_used - 1) & 1))) break;
+        if (lane == 0) {
+          const int n_x = g.n_tok > tile_tok ? 2 : 1;
+          mbar_arrive_expect_tx(q_full, n_x * S::HALVES * tile_tok * p.group * 128);
+          for (int x = 0; x < n_x; ++x)
+            for (int hf = 0; hf < S::HALVES; ++hf)
+              tma_load_4d(q_tile(x) + hf * (AT_ROWS * 128), &map_q, 0, g.h * p.group, g.row0 + x * tile_tok, hf, q_full);
+        }
+        ++q_used;
+        for (int i = g.i0; i < g.i1 && ok; ++i, ++tiles) {
+          const unsigned there = __ballot_sync(0xffffffffu, lane < boxes && page >= 0);
+          // a page that is not there: a box past the pool's end, which the copy fills with zeros
+          const int64_t block = page >= 0 ? static_cast<int64_t>(page) * p.heads + g.h : p.pages * p.heads;
+          const int y = (tile_pos(g, i) + (lane & (boxes - 1)) * box) & (p.page_size - 1);
+          if (i + 1 < g.i1) page = page_of(i + 1);
+          for (int kv = 0; kv < 2; ++kv) {
+            const int s = kv ? v_slot(tiles) : k_slot(tiles);
+            if (tiles >= (kv ? AT_V : AT_K) &&
+                !(ok = wait(kv_empty(s), kv ? v_par(tiles - AT_V) : k_par(tiles - AT_K))))
+              break;
+            if (lane == 0) {
+              if (kv == 0) oks[tiles % AT_OKS] = there;
+              mbar_arrive_expect_tx(kv_full(s), S::MAT_BYTES);
+            }
+            __syncwarp();
+            if (lane < boxes)
+              for (int hf = 0; hf < S::HALVES; ++hf)
+                tma_load_4d(slot(s) + hf * (AT_TILE * 128) + lane * box * 128, kv ? &map_v : &map_k, 0, y, hf,
+                            static_cast<int>(block), kv_full(s));
+            ++asked[kv];
+          }
+          if (!ok) break;
+        }
+      }
+      if (!ok) {
+        // the copies in flight land before this CTA's shared memory goes
+        for (int n = max(asked[0] - AT_K, 0); n < asked[0]; ++n)
+          mbar_wait_bounded(kv_full(k_slot(n)), k_par(n), nullptr, p.status);
+        for (int n = max(asked[1] - AT_V, 0); n < asked[1]; ++n)
+          mbar_wait_bounded(kv_full(v_slot(n)), v_par(n), nullptr, p.status);
+        if (q_used > 0) mbar_wait_bounded(q_full, (q_used - 1) & 1, nullptr, p.status);
+      }
+    } else if (warp == AT_MMA_WARP) {
+      // -------------------------------------------------------------- MMA issue
+      // kind::f16, bf16 A and B, fp32 D, M = 128; S = Q K^T: both K-major, N =
+      // 128; O = P V: V's d's are contiguous, so B is N-major (bit 16), N = D
+      constexpr uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((AT_TILE >> 3) << 17) | ((AT_ROWS >> 4) << 24);
+      constexpr uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((D >> 3) << 17) | ((AT_ROWS >> 4) << 24);
+      int tiles = 0, q_used = 0;   // tiles begun, items begun
+      int p_used[2] = {0, 0};
+      bool ok = true;
+      AtItem g;
+      for (int k = 0; ok && get_item(k, g); ++k) {
+        const int nt = g.i1 - g.i0;
+        if (nt <= 0) continue;
+        const int n_x = g.n_tok > tile_tok ? 2 : 1;
+        auto issue_s = [&](int x, int s) {   // S_x = Q_x K^T, K in ring slot s
+          if (lane == 0) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks >> 2) * (AT_TILE * 128) + (ks & 3) * 32;
+              tc_mma_bf16_ss(tmem + AT_TILE * x, smem_desc(q_tile(x) + off, 16, 1024, 2), smem_desc(slot(s) + off, 16, 1024, 2),
+                             idesc_s, ks > 0);
+            }
+            tc_commit(s_full(x));
+          }
+          __syncwarp();
+        };
+        ok = wait(q_full, q_used & 1) && wait(kv_full(k_slot(tiles)), k_par(tiles));
+        if (!ok) break;
+        ++q_used;
+        tc_fence_after();
+        for (int x = 0; x < n_x; ++x) issue_s(x, k_slot(tiles));
+        if (lane == 0) {
+          tc_commit(kv_empty(k_slot(tiles)));
+          if (nt == 1) tc_commit(q_empty);
+        }
+        __syncwarp();
+        for (int i = g.i0; i < g.i1 && ok; ++i, ++tiles) {
+          const int sv = v_slot(tiles), sk = k_slot(tiles + 1);
+          const bool more = i + 1 < g.i1;
+          ok = wait(kv_full(sv), v_par(tiles)) && wait(kv_clean(sv), v_par(tiles));
+          if (ok && more) ok = wait(kv_full(sk), k_par(tiles + 1));
+          for (int x = 0; x < n_x && ok; ++x) {
+            ok = wait(p_full(x), p_used[x] & 1);
+            if (!ok) break;
+            ++p_used[x];
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int ks = 0; ks < AT_TILE / 16; ++ks)
+                tc_mma_bf16_ts(tmem + S::O_COL0 + D * x, tmem + AT_TILE * x + 8 * ks,
+                               smem_desc(slot(sv) + ks * (16 * 128), AT_TILE * 128, 1024, 2), idesc_o, i > g.i0 || ks > 0);
+              if (!more) tc_commit(o_full(x));
+            }
+            __syncwarp();
+            if (more) issue_s(x, sk);
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            tc_commit(kv_empty(sv));
+            if (more) {
+              tc_commit(kv_empty(sk));
+              if (i + 2 == g.i1) tc_commit(q_empty);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      // every MMA issued so far has completed before the CTA's memory goes
+      if (lane == 0) {
+        tc_commit(drain_bar);
+        mbar_wait_bounded(drain_bar, 0, nullptr, p.status);
+      }
+      __syncwarp();
+    } else if (warp == AT_CLEAN_WARP) {
+      // --------------------------------------- value rows that no row may take in
+      // every V tile passes here, so this warp and the rings stay in step
+      int tiles = 0;
+      bool ok = true;
+      AtItem g;
+      for (int k = 0; ok && get_item(k, g); ++k) {
+        const int p1 = g.p0 + g.n_tok - 1;
+        for (int i = g.i0; i < g.i1; ++i, ++tiles) {
+          const int j0 = tile_pos(g, i), s = v_slot(tiles);
+          ok = wait(kv_full(s), v_par(tiles));
+          if (!ok) break;
+          const bool unclean = at_unclean(j0, g.p0, p1, p.window, p.sinks);
+          for (int c = 0; unclean && c < AT_TILE; ++c) {
+            const int j = j0 + c;
+            if (j <= p1 && !(p.window > 0 && j >= p.sinks && g.p0 - j >= p.window)) continue;
+            if (lane < 8 * S::HALVES)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot(s) + (lane >> 3) * (AT_TILE * 128) + c * 128 +
+                                                                            (lane & 7) * 16),
+                           "r"(0)
+                           : "memory");
+          }
+          if (unclean) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv_clean(s));
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == AT_MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+}
+
+}  // namespace
+}  // namespace nvfp4
