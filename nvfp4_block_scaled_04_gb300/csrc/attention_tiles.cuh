@@ -20,7 +20,7 @@
 //                     pairs), and at the end reads O, divides and writes out
 //   warp 8            producer: hands out work items, loads Q, K and V (a box
 //                     per page and 64 d's) by TMA
-//   warp 9            tensor-memory allocation; lane 0 issues the MMAs
+//   warp 9            tensor-memory allocation; issues the MMAs
 //   warp 10           zeroes value rows no row of the item sees (they may hold
 //                     anything, and 0 * NaN is not 0)
 // S and P of a tile share 128 columns: S(j + 1) is issued after O += P(j) V(j),
@@ -97,20 +97,29 @@ struct AtShape {
   static constexpr int O_COL0 = 256;                       // tensor memory: S_A, S_B, O_A, O_B
 };
 
-NVFP4_DEV void tc_mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// 1 in one lane of the (converged) warp, 0 in the others.
+NVFP4_DEV uint32_t elect_one() {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+  return x;
+}
+
+// D (+)= A * B, both from shared memory, by the lane whose `lead` is set.
+NVFP4_DEV void tc_mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
-NVFP4_DEV void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The same with A from tensor memory.
+NVFP4_DEV void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
 NVFP4_DEV void tc_st_32cols(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -138,6 +147,12 @@ NVFP4_DEV void add2(float& a, float& b, float c, float d) {   // (a, b) += (c, d
       "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "+f"(a), "+f"(b)
       : "f"(c), "f"(d));
+}
+
+NVFP4_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // A word with its lowest n bits set (none for n <= 0).
@@ -269,26 +284,34 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       const int tok = x * tile_tok + my_tok;                       // token of the item
       const bool live = my_tok < tile_tok && tok < g.n_tok;
       const int pos = g.p0 + min(tok, g.n_tok - 1);
-      float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      float m = -INFINITY, l[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // l in four chains
       bool ok = true;
       for (int i = g.i0; i < g.i1; ++i, ++tiles, ++used) {
         ok = wait(s_full(x), used & 1);
         if (!ok) break;
         tc_fence_after();
         uint32_t v[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tc_ld_32cols(s_cols + 32 * q, v[q]);
+        tc_ld_32cols(s_cols, v[0]);
+        tc_ld_32cols(s_cols + 32, v[1]);
         const int j0 = tile_pos(g, i);
         const unsigned there = oks[tiles % AT_OKS];
         // this row sees columns 0..hi of the tile but for sk..lo - 1
         const int hi = min(pos, g.key_end - 1) - j0;
         const int lo = p.window > 0 ? pos - p.window + 1 - j0 : 0, sk = p.window > 0 ? p.sinks - j0 : 0;
         const bool whole = hi >= AT_TILE - 1 && (lo <= 0 || sk >= AT_TILE) && there == all_boxes;
-        tc_wait_ld();
-        if (!__all_sync(0xffffffffu, whole)) {
-          const int box_log2 = 31 - __clz(box);
+        const bool masked = !__all_sync(0xffffffffu, whole);
+        const int box_log2 = 31 - __clz(box);
+        // scores of a row that are masked, and its maximum in four chains; the
+        // second half arrives meanwhile
+        float mx[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 4; ++q) {
+          if ((q & 1) == 0) tc_wait_ld();
+          if (q == 0) {
+            tc_ld_32cols(s_cols + 64, v[2]);
+            tc_ld_32cols(s_cols + 96, v[3]);
+          }
+          if (masked) {
             // bit e: this row sees column 32 q + e
             const uint32_t page_bits = (((there >> ((32 * q) >> box_log2)) & 1u) ? 0x0000FFFFu : 0u) |
                                        (((there >> ((32 * q + 16) >> box_log2)) & 1u) ? 0xFFFF0000u : 0u);
@@ -297,24 +320,17 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             for (int e = 0; e < 32; ++e)
               if (!(sees & (1u << e))) v[q][e] = 0xFF800000u;   // -inf
           }
-        }
-        // the row's maximum, four chains
-        float mx[4];
+          mx[q] = fmaxf(__uint_as_float(v[q][0]), __uint_as_float(v[q][1]));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mx[q] = __uint_as_float(v[q][0]);
-#pragma unroll
-          for (int e = 1; e < 31; e += 2)
-            mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(v[q][e])), __uint_as_float(v[q][e + 1]));
-          mx[q] = fmaxf(mx[q], __uint_as_float(v[q][31]));
+          for (int e = 2; e < 32; e += 2) mx[q] = max3(mx[q], __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
         }
         const float mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
         const bool grows = (mn - m) * c > AT_SLACK;
         if (__any_sync(0xffffffffu, grows)) {
           const float alpha = grows ? exp2_approx((m - mn) * c) : 1.0f;
           if (grows) m = mn;
-          l0 *= alpha;
-          l1 *= alpha;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) l[e] *= alpha;
           if (i > g.i0) {
 #pragma unroll
             for (int q = 0; q < D / 16; ++q) {
@@ -337,7 +353,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             fma2(a, b, c, neg);
             a = exp2_approx(a);
             b = exp2_approx(b);
-            add2(l0, l1, a, b);
+            add2(l[2 * (e & 1)], l[2 * (e & 1) + 1], a, b);
             w[e] = f32x2_to_bf16x2(a, b);
           }
           tc_st_16cols(s_cols + 16 * q, w);
@@ -348,7 +364,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         if (lane == 0) mbar_arrive(p_full(x));
       }
       if (!ok) break;
-      float l = l0 + l1;
+      const float sum_l = (l[0] + l[1]) + (l[2] + l[3]);
       if (nt > 0) {
         ok = wait(o_full(x), outs & 1);
         if (!ok) break;
@@ -357,7 +373,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       }
       uint16_t* dst = p.out + (static_cast<int64_t>(g.row0 + tok) * p.heads * p.group + static_cast<int64_t>(g.h) * p.group + my_head) * D;
       if (p.parts == 1) {
-        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // a NaN stays one
+        const float inv = sum_l > 0.0f ? 1.0f / sum_l : (sum_l == 0.0f ? 0.0f : sum_l);   // a NaN stays one
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
@@ -404,7 +420,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                    make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                                __uint_as_float(o[e + 3])));
         }
-        __stcg(reinterpret_cast<float2*>(mine + AT_ROWS * D + 2 * r), make_float2(m * c, l));
+        __stcg(reinterpret_cast<float2*>(mine + AT_ROWS * D + 2 * r), make_float2(m * c, sum_l));
         tc_fence_before();
       }
       fence_acq_rel_gpu();
@@ -568,75 +584,80 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     } else if (warp == AT_MMA_WARP) {
       // -------------------------------------------------------------- MMA issue
       // kind::f16, bf16 A and B, fp32 D, M = 128; S = Q K^T: both K-major, N =
-      // 128; O = P V: V's d's are contiguous, so B is N-major (bit 16), N = D
+      // 128; O = P V: V's d's are contiguous, so B is N-major (bit 16), N = D.
+      // The whole warp walks the loops and one lane's MMAs take effect, by a
+      // predicate and not a branch, with loop bounds from warp reductions: so
+      // descriptors stay in uniform registers. Issued from a one-lane branch a
+      // MMA took about 100 clocks to issue, more than its 64 on the tensor
+      // cores (2k rows on 8k positions: 231 -> 188 us). One warp for each row
+      // tile was slower (267 us): their MMAs interleave, so both tiles' scores
+      // come late together instead of in turns.
       constexpr uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((AT_TILE >> 3) << 17) | ((AT_ROWS >> 4) << 24);
       constexpr uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((D >> 3) << 17) | ((AT_ROWS >> 4) << 24);
-      int tiles = 0, q_used = 0;   // tiles begun, items begun
+      const uint64_t desc_q = smem_desc(q_tile(0), 16, 1024, 2), desc_k = smem_desc(slot(0), 16, 1024, 2);
+      const uint64_t desc_v = smem_desc(slot(AT_K), AT_TILE * 128, 1024, 2);
+      const uint32_t lead = elect_one();
+      int tiles = 0, q_used = 0;   // tiles done, items with tiles
       int p_used[2] = {0, 0};
       bool ok = true;
       AtItem g;
       for (int k = 0; ok && get_item(k, g); ++k) {
-        const int nt = g.i1 - g.i0;
+        const int nt = __reduce_max_sync(0xffffffffu, g.i1 - g.i0);
         if (nt <= 0) continue;
-        const int n_x = g.n_tok > tile_tok ? 2 : 1;
-        auto issue_s = [&](int x, int s) {   // S_x = Q_x K^T, K in ring slot s
-          if (lane == 0) {
+        const int n_x = __reduce_max_sync(0xffffffffu, g.n_tok > tile_tok ? 2 : 1);
+        auto issue_s = [&](int x, int n) {   // S_x = Q_x K^T with the n-th K tile
+          const uint64_t q0 = desc_q + static_cast<uint64_t>(x) * (S::MAT_BYTES >> 4);
+          const uint64_t k0 = desc_k + static_cast<uint64_t>(k_slot(n)) * (S::MAT_BYTES >> 4);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = (ks >> 2) * (AT_TILE * 128) + (ks & 3) * 32;
-              tc_mma_bf16_ss(tmem + AT_TILE * x, smem_desc(q_tile(x) + off, 16, 1024, 2), smem_desc(slot(s) + off, 16, 1024, 2),
-                             idesc_s, ks > 0);
-            }
+          for (int ks = 0; ks < D / 16; ++ks) {
+            // the descriptors' address field counts 16 bytes
+            const uint64_t off = ((ks >> 2) * (AT_TILE * 128) + (ks & 3) * 32) >> 4;
+            tc_mma_bf16_ss(tmem + AT_TILE * x, q0 + off, k0 + off, idesc_s, ks > 0, lead);
+          }
+          if (lead) {
             tc_commit(s_full(x));
+            if (x + 1 == n_x) tc_commit(kv_empty(k_slot(n)));
           }
           __syncwarp();
         };
-        ok = wait(q_full, q_used & 1) && wait(kv_full(k_slot(tiles)), k_par(tiles));
-        if (!ok) break;
+        if (!(ok = wait(q_full, q_used & 1) && wait(kv_full(k_slot(tiles)), k_par(tiles)))) break;
         ++q_used;
         tc_fence_after();
-        for (int x = 0; x < n_x; ++x) issue_s(x, k_slot(tiles));
-        if (lane == 0) {
-          tc_commit(kv_empty(k_slot(tiles)));
-          if (nt == 1) tc_commit(q_empty);
-        }
+        for (int x = 0; x < n_x; ++x) issue_s(x, tiles);
+        if (nt == 1 && lead) tc_commit(q_empty);
         __syncwarp();
-        for (int i = g.i0; i < g.i1 && ok; ++i, ++tiles) {
-          const int sv = v_slot(tiles), sk = k_slot(tiles + 1);
-          const bool more = i + 1 < g.i1;
-          ok = wait(kv_full(sv), v_par(tiles)) && wait(kv_clean(sv), v_par(tiles));
-          if (ok && more) ok = wait(kv_full(sk), k_par(tiles + 1));
-          for (int x = 0; x < n_x && ok; ++x) {
-            ok = wait(p_full(x), p_used[x] & 1);
-            if (!ok) break;
+        for (int i = 0; i < nt && ok; ++i, ++tiles) {
+          const int sv = v_slot(tiles);
+          const bool more = i + 1 < nt;
+          if (!(ok = wait(kv_clean(sv), v_par(tiles)))) break;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (x >= n_x) break;
+            if (!(ok = wait(p_full(x), p_used[x] & 1))) break;
             ++p_used[x];
             tc_fence_after();
-            if (lane == 0) {
+            const uint32_t d = tmem + S::O_COL0 + D * x, a = tmem + AT_TILE * x;
+            const uint64_t v0 = desc_v + static_cast<uint64_t>(sv - AT_K) * (S::MAT_BYTES >> 4);
+            tc_mma_bf16_ts(d, a, v0, idesc_o, i > 0, lead);
 #pragma unroll
-              for (int ks = 0; ks < AT_TILE / 16; ++ks)
-                tc_mma_bf16_ts(tmem + S::O_COL0 + D * x, tmem + AT_TILE * x + 8 * ks,
-                               smem_desc(slot(sv) + ks * (16 * 128), AT_TILE * 128, 1024, 2), idesc_o, i > g.i0 || ks > 0);
+            for (int ks = 1; ks < AT_TILE / 16; ++ks)   // 16 positions of V, 8 columns of P
+              tc_mma_bf16_ts(d, a + 8 * ks, v0 + ((ks * 16 * 128) >> 4), idesc_o, 1, lead);
+            if (lead) {
+              if (x + 1 == n_x) tc_commit(kv_empty(sv));
               if (!more) tc_commit(o_full(x));
             }
             __syncwarp();
-            if (more) issue_s(x, sk);
+            if (!more) continue;
+            if (x == 0 && !(ok = wait(kv_full(k_slot(tiles + 1)), k_par(tiles + 1)))) break;
+            issue_s(x, tiles + 1);
           }
-          if (!ok) break;
-          if (lane == 0) {
-            tc_commit(kv_empty(sv));
-            if (more) {
-              tc_commit(kv_empty(sk));
-              if (i + 2 == g.i1) tc_commit(q_empty);
-            }
-          }
+          if (ok && lead && i + 2 == nt) tc_commit(q_empty);
           __syncwarp();
         }
       }
       // every MMA issued so far has completed before the CTA's memory goes
-      if (lane == 0) {
-        tc_commit(drain_bar);
-        mbar_wait_bounded(drain_bar, 0, nullptr, p.status);
-      }
+      if (lead) tc_commit(drain_bar);
+      mbar_wait_bounded(drain_bar, 0, nullptr, p.status);
       __syncwarp();
     } else if (warp == AT_CLEAN_WARP) {
       // --------------------------------------- value rows that no row may take in
@@ -651,14 +672,17 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           ok = wait(kv_full(s), v_par(tiles));
           if (!ok) break;
           const bool unclean = at_unclean(j0, g.p0, p1, p.window, p.sinks);
-          for (int c = 0; unclean && c < AT_TILE; ++c) {
-            const int j = j0 + c;
-            if (j <= p1 && !(p.window > 0 && j >= p.sinks && g.p0 - j >= p.window)) continue;
-            if (lane < 8 * S::HALVES)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot(s) + (lane >> 3) * (AT_TILE * 128) + c * 128 +
-                                                                            (lane & 7) * 16),
-                           "r"(0)
-                           : "memory");
+          if (unclean) {
+            // rows past the item's last position, and rows between the sinks and its first window
+            auto zero = [&](int c0, int c1) {
+              for (int e = c0 * 8 + lane; e < c1 * 8; e += 32)
+#pragma unroll
+                for (int hf = 0; hf < S::HALVES; ++hf)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot(s) + hf * (AT_TILE * 128) + e * 16), "r"(0)
+                               : "memory");
+            };
+            zero(max(p1 + 1 - j0, 0), AT_TILE);
+            if (p.window > 0) zero(max(p.sinks - j0, 0), min(g.p0 - p.window + 1 - j0, AT_TILE));
           }
           if (unclean) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
