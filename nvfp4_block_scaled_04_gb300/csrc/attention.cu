@@ -21,29 +21,11 @@ int log2_of(int x) {
 // Eight-row tiles of a call of the split kernel.
 int rows_nt(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
 
-// CTAs of the split kernel: two per SM while the accumulators leave room.
-int rows_grid(int nt) { return (nt <= 2 ? 2 : 1) * sm_count(); }
+// CTAs of the split kernel: two per SM for one eight-row tile, else one of more warps.
+int rows_grid(int nt) { return (nt == 1 ? 2 : 1) * sm_count(); }
 
 constexpr int64_t COUNTER_BYTES = 4096;   // arrival counters at the front of the workspace
-
-template <bool E4M3, int D, int NT>
-int launch_rows(const ArParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
-  const int smem = ar_smem_bytes<E4M3, D, NT>(p.s.batch);
-  const int rc = ensure_smem(attention_rows_kernel<E4M3, D, NT>, smem);
-  if (rc) return rc;
-  return launch_ex(attention_rows_kernel<E4M3, D, NT>, dim3(rows_grid(NT)), dim3(AR_THREADS), smem, 1, true, stream, mk, mv,
-                   p);
-}
-
-template <bool E4M3, int D>
-int launch_rows_nt(int nt, const ArParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
-  switch (nt) {
-    case 1: return launch_rows<E4M3, D, 1>(p, mk, mv, stream);
-    case 2: return launch_rows<E4M3, D, 2>(p, mk, mv, stream);
-    case 3: return launch_rows<E4M3, D, 3>(p, mk, mv, stream);
-    default: return launch_rows<E4M3, D, 4>(p, mk, mv, stream);
-  }
-}
+constexpr int SMEM_SM = 227 * 1024;       // dynamic shared memory of the CTAs of an SM (1 KB each is reserved beside it)
 
 // One page of one head as [halves][rows][seg bytes], a copy box of `box` rows of `box_halves` halves.
 int kv_map(CUtensorMap* map, const void* pool, const nvfp4_kv_cache_t& c, int box, int box_halves) {
@@ -54,6 +36,33 @@ int kv_map(CUtensorMap* map, const void* pool, const nvfp4_kv_cache_t& c, int bo
   const int boxes[4] = {static_cast<int>(seg), box, box_halves, 1};
   return make_tmap_4d_u8(map, pool, dims, strides, boxes,
                          seg == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <bool E4M3, int D, int WARPS, int NT>
+int launch_rows(ArParams p, const nvfp4_kv_cache_t& c, cudaStream_t stream) {
+  using S = ArShape<E4M3, D, WARPS, NT>;
+  CUtensorMap mk, mv;
+  const int box = c.page_size < S::TILE ? c.page_size : S::TILE;
+  if (int rc = kv_map(&mk, c.k, c, box, S::HALVES)) return rc;
+  if (int rc = kv_map(&mv, c.v, c, box, S::HALVES)) return rc;
+  const int fixed = S::FIXED_BYTES + 4 * (p.s.batch + 2);
+  const int room = (SMEM_SM - (S::CTAS - 1) * 1024) / S::CTAS - fixed;
+  p.stages = std::max(2, std::min(AR_MAX_STAGES, room / S::STAGE_BYTES));
+  const int smem = fixed + p.stages * S::STAGE_BYTES;
+  const int rc = ensure_smem(attention_rows_kernel<E4M3, D, WARPS, NT>, smem);
+  if (rc) return rc;
+  return launch_ex(attention_rows_kernel<E4M3, D, WARPS, NT>, dim3(rows_grid(NT)), dim3(S::THREADS), smem, 1, true, stream,
+                   mk, mv, p);
+}
+
+template <bool E4M3, int D>
+int launch_rows_nt(int nt, const ArParams& p, const nvfp4_kv_cache_t& c, cudaStream_t stream) {
+  switch (nt) {
+    case 1: return launch_rows<E4M3, D, 4, 1>(p, c, stream);
+    case 2: return launch_rows<E4M3, D, 8, 2>(p, c, stream);
+    case 3: return launch_rows<E4M3, D, 8, 3>(p, c, stream);
+    default: return launch_rows<E4M3, D, 8, 4>(p, c, stream);
+  }
 }
 
 // Blocks of rows (256 at most, whole tokens) and kv heads of a call of the tile kernel, at most.
@@ -124,11 +133,6 @@ int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, con
   }
   const int nt = rows_nt(rows);
   if (4 * rows_grid(nt) > COUNTER_BYTES) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-  CUtensorMap mk, mv;
-  const int box = c.page_size < AR_TILE ? c.page_size : AR_TILE;
-  const int halves = c.head_dim == 128 && c.dtype == NVFP4_DTYPE_BF16 ? 2 : 1;
-  if (int rc = kv_map(&mk, c.k, c, box, halves)) return rc;
-  if (int rc = kv_map(&mv, c.v, c, box, halves)) return rc;
   ArParams p;
   p.s = s;
   p.q = Q;
@@ -150,8 +154,8 @@ int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, con
   p.status = status;
   const bool e4m3 = c.dtype == NVFP4_DTYPE_E4M3;
   if (c.head_dim == 128)
-    return e4m3 ? launch_rows_nt<true, 128>(nt, p, mk, mv, stream) : launch_rows_nt<false, 128>(nt, p, mk, mv, stream);
-  return e4m3 ? launch_rows_nt<true, 64>(nt, p, mk, mv, stream) : launch_rows_nt<false, 64>(nt, p, mk, mv, stream);
+    return e4m3 ? launch_rows_nt<true, 128>(nt, p, c, stream) : launch_rows_nt<false, 128>(nt, p, c, stream);
+  return e4m3 ? launch_rows_nt<true, 64>(nt, p, c, stream) : launch_rows_nt<false, 64>(nt, p, c, stream);
 }
 
 }  // namespace nvfp4

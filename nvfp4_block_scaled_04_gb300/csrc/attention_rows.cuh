@@ -22,9 +22,12 @@
 // joins them in CTA order, so results do not depend on which one it is.
 //
 // One producer warp keeps a ring of tiles full (a page's rows are one 4-D box;
-// pages shorter than 64 tokens give several boxes), four consumer warps take
-// 16 tokens each with an online softmax of their own and meet at the end of an
-// item.
+// pages shorter than 64 tokens give several boxes), another one brings the next
+// item and its query rows as fragments. Consumer warps take 16 tokens of a tile
+// each, with an online softmax of their own, and meet at the end of an item.
+// Up to 8 rows: four of them and two CTAs per SM; more rows (up to 32): eight
+// and one CTA, so that a key or value fragment is loaded (and from E4M3
+// converted) once for all rows.
 //
 // Roundings. Products are exact in fp32 sums. bf16 caches: q and k as they
 // are; p is split into two bf16 halves (p = hi + lo to 2^-17), since one bf16
@@ -44,24 +47,11 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int AR_TILE = 64;                  // tokens of one tile
-constexpr int AR_WARPS = 4;                  // consumer warps, 16 tokens of a tile each
-constexpr int AR_THREADS = (AR_WARPS + 1) * 32;
-constexpr int AR_RING_BYTES = 96 * 1024;     // two CTAs per SM
+constexpr int AR_MAX_STAGES = 8;
+constexpr int AR_ITEMS = 2;                  // items announced ahead
 constexpr int AR_MAX_BATCH = 4096;
 constexpr int AR_PAD = 4;                    // fp32 words between rows of the merge buffer: no bank conflicts
 constexpr unsigned AR_ALL = 0xffffffffu;
-
-template <bool E4M3, int D>
-struct ArShape {
-  static constexpr int ROW_BYTES = D * (E4M3 ? 1 : 2);
-  static constexpr int SEG = ROW_BYTES >= 128 ? 128 : 64;       // bytes of a swizzled row of a box
-  static constexpr int HALVES = ROW_BYTES / SEG;
-  static constexpr int MAT_BYTES = AR_TILE * ROW_BYTES;          // K or V of a tile
-  static constexpr int STAGE_BYTES = 2 * MAT_BYTES;
-  static constexpr int STAGES = AR_RING_BYTES / STAGE_BYTES < 8 ? AR_RING_BYTES / STAGE_BYTES : 8;
-  static constexpr int KS = D / 16;                              // 16-d steps
-};
 
 struct ArParams {
   KvSeqs s;
@@ -76,20 +66,35 @@ struct ArParams {
   int window, sinks;
   float scale;            // softmax scale * log2 e
   unsigned* arrived;      // [CTAs], zero between calls
-  float* part;            // [CTAs][2][8 NT][D + 2]
+  float* part;            // [CTAs][2][rows of an item][D + 2]
   int min_tiles;          // least tiles of a CTA's piece
+  int stages;             // of the ring
   int* status;
 };
 
-template <bool E4M3, int D, int NT>
-constexpr int ar_smem_bytes(int batch) {
-  using S = ArShape<E4M3, D>;
-  const int merge = (NT <= 2 ? 2 : 1) * 8 * NT * (D + AR_PAD) * 4;
-  const int qfrag = S::KS * NT * 32 * 8;
-  const int small = 8 * NT * 4 * (2 + 2 * AR_WARPS);             // row positions, multipliers, each warp's m and l
-  return 1024 + S::STAGES * S::STAGE_BYTES + merge + qfrag + small + 8 * (2 * S::STAGES + 1) + 4 * S::STAGES + 64 +
-         4 * (batch + 2);
-}
+// A shape of the kernel: WARPS consumer warps take 16 tokens each of a tile,
+// and NT eight-row tiles of queries.
+template <bool E4M3, int D, int WARPS, int NT>
+struct ArShape {
+  static constexpr int TILE = 16 * WARPS;                        // tokens of a tile
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int THREADS = (WARPS + 2) * 32;               // consumers, the producer, the item warp
+  static constexpr int CTAS = WARPS == 4 ? 2 : 1;                // per SM
+  static constexpr int BUFS = ROWS <= 16 && WARPS == 8 ? 4 : 2;  // merge buffers
+  static constexpr bool Q_REGS = NT <= 2;                        // query fragments in registers, else read per tile
+  static constexpr int ROW_BYTES = D * (E4M3 ? 1 : 2);
+  static constexpr int SEG = ROW_BYTES >= 128 ? 128 : 64;        // bytes of a swizzled row of a box
+  static constexpr int HALVES = ROW_BYTES / SEG;
+  static constexpr int MAT_BYTES = TILE * ROW_BYTES;             // K or V of a tile
+  static constexpr int STAGE_BYTES = 2 * MAT_BYTES;
+  static constexpr int KS = D / 16;                              // 16-d steps
+  static constexpr int OSTR = D + AR_PAD;
+  static constexpr int QFRAGS = KS * NT * 32;
+  // shared memory without the ring: merge buffers, fragments, multipliers and
+  // positions of the announced items, each warp's m and l, barriers
+  static constexpr int FIXED_BYTES = 1024 + BUFS * ROWS * OSTR * 4 + AR_ITEMS * (QFRAGS * 8 + ROWS * 8) + 2 * WARPS * ROWS * 4 +
+                                     8 * (2 * AR_MAX_STAGES + 2 * AR_ITEMS) + 4 * AR_MAX_STAGES + AR_ITEMS * 64 + 64;
+};
 
 NVFP4_DEV void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -117,7 +122,8 @@ NVFP4_DEV void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// AND of `pred` over the consumer warps.
+// AND of `pred` over the N consumer threads.
+template <int N>
 NVFP4_DEV bool ar_all(bool pred) {
   uint32_t out;
   asm volatile(
@@ -126,28 +132,38 @@ NVFP4_DEV bool ar_all(bool pred) {
       "bar.red.and.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(out)
-      : "r"(static_cast<uint32_t>(pred)), "n"(AR_WARPS * 32)
+      : "r"(static_cast<uint32_t>(pred)), "n"(N)
       : "memory");
   return out != 0;
 }
-NVFP4_DEV void ar_consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(AR_WARPS * 32) : "memory"); }
+template <int N>
+NVFP4_DEV void ar_consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
 
-// A piece of the line of tiles that lies inside one item.
-struct ArSeg {
-  int b, h, rb;          // sequence, kv head, block of rows
-  int n, len, row0;      // new tokens, length, first new-token row
-  int i0, i1;            // its tiles
-  int per_item;          // tiles of the whole item
-  unsigned item_u0;      // where the item starts on the line
+// A piece of the line of tiles that lies inside one item, as the item warp
+// hands it to the consumers.
+struct ArItem {
+  int done;
+  int h;                  // kv head
+  int r0, n_rows;         // rows of the sequence's (token, head) pairs
+  int row0;               // the sequence's first new-token row
+  int p0, p1;             // positions of the first and the last row
+  int key_end;            // positions at or past it hold nothing
+  KvTiles tiles;
+  int i0, i1;             // the piece's tiles
+  unsigned first_cta, last_cta;   // CTAs that share the item
 };
+static_assert(sizeof(ArItem) <= 64, "announced items");
 
-template <int NT>
+template <class S>
 struct ArWalk {
   const ArParams& p;
   const unsigned* pre;   // tiles of the sequences before (shared memory)
-  unsigned u, end;
+  unsigned per, u, end;
+  int b;                 // the sequence
 
-  NVFP4_DEV bool next(ArSeg& g) {
+  NVFP4_DEV bool next(ArItem& g) {
     if (u >= end) return false;
     int lo = 0, hi = p.s.batch;             // last b with pre[b] <= u
     while (hi - lo > 1) {
@@ -157,84 +173,98 @@ struct ArWalk {
       else
         hi = mid;
     }
-    g.b = lo;
+    b = lo;
+    g.done = 0;
     g.row0 = kv_row0(p.s, lo);
-    g.n = kv_row0(p.s, lo + 1) - g.row0;
-    g.len = kv_len(p.s, lo);
-    const int blocks = (g.n * p.group + 8 * NT - 1) / (8 * NT);
-    g.per_item = static_cast<int>((pre[lo + 1] - pre[lo]) / static_cast<unsigned>(blocks * p.heads));
-    const unsigned in = u - pre[lo], item = in / static_cast<unsigned>(g.per_item);
-    g.h = static_cast<int>(item) % p.heads;
-    g.rb = static_cast<int>(item) / p.heads;
-    g.i0 = static_cast<int>(in - item * static_cast<unsigned>(g.per_item));
-    g.item_u0 = u - static_cast<unsigned>(g.i0);
-    const unsigned left = end - u;
-    g.i1 = left < static_cast<unsigned>(g.per_item - g.i0) ? g.i0 + static_cast<int>(left) : g.per_item;
-    u += static_cast<unsigned>(g.i1 - g.i0);
+    const int n = kv_row0(p.s, lo + 1) - g.row0, len = kv_len(p.s, lo);
+    const unsigned blocks = static_cast<unsigned>((n * p.group + S::ROWS - 1) / S::ROWS);
+    const unsigned per_item = (pre[lo + 1] - pre[lo]) / (blocks * static_cast<unsigned>(p.heads));
+    const unsigned in = u - pre[lo], item = in / per_item;
+    const int rb = static_cast<int>(item / static_cast<unsigned>(p.heads));
+    g.h = static_cast<int>(item) - rb * p.heads;
+    g.i0 = static_cast<int>(in - item * per_item);
+    const unsigned u0 = u - static_cast<unsigned>(g.i0), left = end - u;
+    int i1 = left < per_item - static_cast<unsigned>(g.i0) ? g.i0 + static_cast<int>(left) : static_cast<int>(per_item);
+    u += static_cast<unsigned>(i1 - g.i0);
+    g.first_cta = u0 / per;
+    g.last_cta = (u0 + per_item - 1u) / per;
+    g.r0 = rb * S::ROWS;
+    g.n_rows = min(S::ROWS, n * p.group - g.r0);
+    g.p0 = len - n + g.r0 / p.group;
+    g.p1 = len - n + (g.r0 + g.n_rows - 1) / p.group;
+    const int64_t cap = static_cast<int64_t>(p.s.max_pages) * p.page_size;
+    g.key_end = static_cast<int>(cap < len ? cap : len);
+    g.tiles = kv_tiles<S::TILE>(g.p0, g.p1, p.window, p.sinks, g.key_end);
+    g.i1 = min(i1, g.tiles.count);
     return true;
   }
 };
 
 // Tiles that each block of sequence b's rows is given (the most any sees, at least one).
-template <int NT>
+template <class S>
 NVFP4_DEV unsigned ar_seq_tiles(const ArParams& p, int b) {
   const int n = kv_row0(p.s, b + 1) - kv_row0(p.s, b);
   if (n <= 0) return 0;
   const int len = kv_len(p.s, b);
   const int64_t cap = static_cast<int64_t>(p.s.max_pages) * p.page_size;
   const int key_end = static_cast<int>(cap < len ? cap : len);
-  const int blocks = (n * p.group + 8 * NT - 1) / (8 * NT);
-  const int span = (8 * NT - 1 + p.group - 1) / p.group;   // positions between a block's first and last row, at most
+  const int blocks = (n * p.group + S::ROWS - 1) / S::ROWS;
+  const int span = (S::ROWS - 1 + p.group - 1) / p.group;   // positions between a block's first and last row, at most
   int most;
   if (p.window > 0 && blocks > 1) {
     // a block whose rows lie as late as any: two more tiles than its widest range of positions can touch
-    const int64_t st = (min(p.sinks, max(key_end, 0)) + AR_TILE - 1) / AR_TILE;
-    const int64_t w = (static_cast<int64_t>(p.window) + span) / AR_TILE + 2;
-    const int64_t all = (max(key_end, 0) + AR_TILE - 1) / AR_TILE;
+    const int64_t st = (min(p.sinks, key_end) + S::TILE - 1) / S::TILE;
+    const int64_t w = (static_cast<int64_t>(p.window) + span) / S::TILE + 2;
+    const int64_t all = (key_end + S::TILE - 1) / S::TILE;
     most = static_cast<int>(st + w < all ? st + w : all);
   } else {
-    most = kv_tiles<AR_TILE>(len - n, len - 1, p.window, p.sinks, key_end).count;
+    most = kv_tiles<S::TILE>(len - n, len - 1, p.window, p.sinks, key_end).count;
   }
   return static_cast<unsigned>(max(most, 1)) * static_cast<unsigned>(blocks * p.heads);
 }
 
-template <bool E4M3, int D, int NT>
-__global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
+template <bool E4M3, int D, int WARPS, int NT>
+__global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<E4M3, D, WARPS, NT>::CTAS)
     attention_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                           const ArParams p) {
-  using S = ArShape<E4M3, D>;
-  constexpr int ROWS = 8 * NT;
-  constexpr int MERGE_BUFS = NT <= 2 ? 2 : 1;
-  constexpr int OSTR = D + AR_PAD;
+  using S = ArShape<E4M3, D, WARPS, NT>;
+  constexpr int ROWS = S::ROWS, KS = S::KS, BUFS = S::BUFS, OSTR = S::OSTR, TILE = S::TILE, CONSUMERS = WARPS * 32;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* at = smem_raw + (base - raw) + S::STAGES * S::STAGE_BYTES;
-  float* merge = reinterpret_cast<float*>(at);                     // [bufs][ROWS][OSTR]
-  at += MERGE_BUFS * ROWS * OSTR * 4;
-  uint2* qfrag = reinterpret_cast<uint2*>(at);                     // [KS][NT][32]
-  at += S::KS * NT * 32 * 8;
-  float* row_mult = reinterpret_cast<float*>(at);                  // [ROWS]
-  int* row_pos = reinterpret_cast<int*>(row_mult + ROWS);          // [ROWS]
-  float* warp_m = reinterpret_cast<float*>(row_pos + ROWS);        // [AR_WARPS][ROWS]
-  float* warp_l = warp_m + AR_WARPS * ROWS;
-  at = reinterpret_cast<uint8_t*>(warp_l + AR_WARPS * ROWS);
-  at = smem_raw + ((at - smem_raw + 7) & ~7);
+  const int stages = p.stages;
+  uint8_t* at = smem_raw + (base - raw) + stages * S::STAGE_BYTES;
+  float* merge = reinterpret_cast<float*>(at);                     // [BUFS][ROWS][OSTR]
+  at += BUFS * ROWS * OSTR * 4;
+  uint2* qfrag = reinterpret_cast<uint2*>(at);                     // [AR_ITEMS][KS][NT][32]
+  at += AR_ITEMS * S::QFRAGS * 8;
+  ArItem* items = reinterpret_cast<ArItem*>(at);                   // [AR_ITEMS]
+  at += AR_ITEMS * 64;
   uint64_t* bars = reinterpret_cast<uint64_t*>(at);
-  unsigned* stage_ok = reinterpret_cast<unsigned*>(bars + 2 * S::STAGES);   // which boxes hold pages
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(stage_ok + S::STAGES);
-  unsigned* last_flag = stage_ok + S::STAGES + 1;
-  unsigned* pre = last_flag + 1;                                   // [batch + 1]
+  float* row_mult = reinterpret_cast<float*>(bars + 2 * AR_MAX_STAGES + 2 * AR_ITEMS);   // [AR_ITEMS][ROWS]
+  int* row_pos = reinterpret_cast<int*>(row_mult + AR_ITEMS * ROWS);                     // [AR_ITEMS][ROWS]
+  float* warp_m = reinterpret_cast<float*>(row_pos + AR_ITEMS * ROWS);                   // [WARPS][ROWS]
+  float* warp_l = warp_m + WARPS * ROWS;
+  unsigned* stage_ok = reinterpret_cast<unsigned*>(warp_l + WARPS * ROWS);               // which boxes hold pages
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(stage_ok + AR_MAX_STAGES);
+  unsigned* last_flag = stage_ok + AR_MAX_STAGES + 1;
+  unsigned* pre = last_flag + 1;                                                         // [batch + 1]
   const uint32_t bar0 = smem_addr(bars);
   auto full_bar = [&](int st) { return bar0 + 8u * st; };
-  auto empty_bar = [&](int st) { return bar0 + 8u * (S::STAGES + st); };
+  auto empty_bar = [&](int st) { return bar0 + 8u * (AR_MAX_STAGES + st); };
+  auto item_full = [&](int i) { return bar0 + 8u * (2 * AR_MAX_STAGES + i); };
+  auto item_empty = [&](int i) { return bar0 + 8u * (2 * AR_MAX_STAGES + AR_ITEMS + i); };
   auto stage_k = [&](int st) { return base + st * S::STAGE_BYTES; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int st = 0; st < S::STAGES; ++st) {
+    for (int st = 0; st < stages; ++st) {
       mbar_init(full_bar(st), 1);
-      mbar_init(empty_bar(st), AR_WARPS);
+      mbar_init(empty_bar(st), WARPS);
+    }
+    for (int i = 0; i < AR_ITEMS; ++i) {
+      mbar_init(item_full(i), 1);
+      mbar_init(item_empty(i), WARPS);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -243,8 +273,8 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
   }
   pdl_launch_dependents();
   pdl_wait();
-  // the line of tiles: prefix sums over the sequences, by the first warp
-  for (int b = threadIdx.x; b < p.s.batch; b += AR_THREADS) pre[b + 1] = ar_seq_tiles<NT>(p, b);
+  // the line of tiles: prefix sums over the sequences
+  for (int b = threadIdx.x; b < p.s.batch; b += S::THREADS) pre[b + 1] = ar_seq_tiles<S>(p, b);
   __syncthreads();
   if (warp == 0) {
     unsigned run = 0;
@@ -266,36 +296,28 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
   if (per < static_cast<unsigned>(p.min_tiles)) per = static_cast<unsigned>(p.min_tiles);
   const uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * per;
   if (u0 >= total) return;
-  ArWalk<NT> walk{p, pre, static_cast<unsigned>(u0), static_cast<unsigned>(u0 + per < total ? u0 + per : total)};
-  ArSeg g;
-  const int box = p.page_size < AR_TILE ? p.page_size : AR_TILE;   // tokens of one copied box
-  const int boxes = AR_TILE / box;
-  const int64_t cap = static_cast<int64_t>(p.s.max_pages) * p.page_size;
+  ArWalk<S> walk{p, pre, per, static_cast<unsigned>(u0), static_cast<unsigned>(u0 + per < total ? u0 + per : total), 0};
+  ArItem g;
+  const int box = p.page_size < TILE ? p.page_size : TILE;   // tokens of one copied box
+  const int box_log2 = 31 - __clz(box), boxes = TILE >> box_log2, boxes_log2 = 31 - __clz(boxes);
 
-  if (warp == AR_WARPS) {
+  if (warp == WARPS) {
     // ------------------------------------------------------------ producer
-    int it = 0;
+    int st = 0, par = 1, used = 0;   // ring slot, parity of its last release, slots used
     bool ok = true;
     while (ok && walk.next(g)) {
-      const int key_end = static_cast<int>(cap < g.len ? cap : g.len);
-      const int r0 = g.rb * ROWS, r1 = min(r0 + ROWS, g.n * p.group) - 1;
-      const KvTiles tl = kv_tiles<AR_TILE>(g.len - g.n + r0 / p.group, g.len - g.n + r1 / p.group, p.window, p.sinks, key_end);
-      const int i1 = min(g.i1, tl.count);
-      const int32_t* row = p.s.table + static_cast<int64_t>(g.b) * p.s.table_stride;
+      const int32_t* row = p.s.table + static_cast<int64_t>(walk.b) * p.s.table_stride;
       // page ids of 32 boxes at a time, one per lane
-      const int boxes_log2 = boxes == 4 ? 2 : boxes - 1;
       int page = -1;
-      for (int i = g.i0; i < i1; ++i, ++it) {
+      for (int i = g.i0; i < g.i1; ++i) {
         const int k = (i - g.i0) << boxes_log2;   // this tile's first box since the piece began
         if ((k & 31) == 0) {
-          const int j = tl.tile(min(i + (lane >> boxes_log2), i1 - 1)) * AR_TILE + (lane & (boxes - 1)) * box;
+          const int j = g.tiles.tile(min(i + (lane >> boxes_log2), g.i1 - 1)) * TILE + ((lane & (boxes - 1)) << box_log2);
           const int e = j >> p.page_log2;
-          page = j < key_end && e < p.s.max_pages ? row[e] : -1;
+          page = j < g.key_end && e < p.s.max_pages ? row[e] : -1;
           if (page < 0 || page >= p.pages) page = -1;
         }
-        const int st = it % S::STAGES;
-        if (it >= S::STAGES)
-          ok = __all_sync(AR_ALL, mbar_wait_bounded(empty_bar(st), ((it / S::STAGES) - 1) & 1, abort_flag, p.status));
+        if (used >= stages) ok = __all_sync(AR_ALL, mbar_wait_bounded(empty_bar(st), par, abort_flag, p.status));
         if (!ok) break;
         const int mine = __shfl_sync(AR_ALL, page, (k & 31) + (lane & (boxes - 1)));
         const unsigned there = __ballot_sync(AR_ALL, lane < boxes && mine >= 0);
@@ -305,128 +327,168 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
         }
         __syncwarp();
         if (lane < boxes) {
-          const int j = tl.tile(i) * AR_TILE + lane * box;
+          const int j = g.tiles.tile(i) * TILE + (lane << box_log2);
           // a page that is not there: a box past the pool's end, which the copy fills with zeros
           const int64_t block = mine >= 0 ? static_cast<int64_t>(mine) * p.heads + g.h : p.pages * p.heads;
           const int y = j & (p.page_size - 1);
-          const uint32_t dst = stage_k(st) + lane * box * S::ROW_BYTES;
+          const uint32_t dst = stage_k(st) + (lane << box_log2) * S::ROW_BYTES;
           tma_load_4d(dst, &map_k, 0, y, 0, static_cast<int>(block), full_bar(st));
           tma_load_4d(dst + S::MAT_BYTES, &map_v, 0, y, 0, static_cast<int>(block), full_bar(st));
+        }
+        ++used;
+        if (++st == stages) {
+          st = 0;
+          par ^= 1;
         }
       }
     }
     if (!ok) {
       // the copies in flight land before this CTA's shared memory goes
-      for (int k = it > S::STAGES ? it - S::STAGES : 0; k < it; ++k)
-        mbar_wait_bounded(full_bar(k % S::STAGES), (k / S::STAGES) & 1, nullptr, p.status);
+      for (int k = used > stages ? used - stages : 0; k < used; ++k)
+        mbar_wait_bounded(full_bar(k % stages), (k / stages) & 1, nullptr, p.status);
     }
     return;
+  }
+
+  if (warp == WARPS + 1) {
+    // ------------------------------------------ items and their query rows
+    const int quad = lane & 3, oct = lane >> 2;
+    for (int k = 0;; ++k) {
+      const int buf = k % AR_ITEMS;
+      const bool more = walk.next(g);
+      uint32_t w[NT][KS][2];
+      int tok[NT];
+      if (more) {
+        // fragments (B of m16n8k16: k = d, n = row), requested before the wait
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = g.r0 + nt * 8 + oct;
+          const bool live = nt * 8 + oct < g.n_rows;
+          const int i = r / p.group;
+          tok[nt] = live ? i : -1;
+          const uint16_t* src = p.q + static_cast<int64_t>(g.row0 + i) * p.q_stride +
+                                (static_cast<int64_t>(g.h) * p.group + (r - i * p.group)) * D;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            if (E4M3) {
+              // an 8-bit ldmatrix hands a lane four consecutive d's: the same order here
+              const uint2 x = live ? *reinterpret_cast<const uint2*>(src + 16 * ks + 4 * quad) : make_uint2(0u, 0u);
+              w[nt][ks][0] = x.x;
+              w[nt][ks][1] = x.y;
+            } else {
+              w[nt][ks][0] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * quad) : 0u;
+              w[nt][ks][1] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 + 2 * quad) : 0u;
+            }
+          }
+        }
+      }
+      if (k >= AR_ITEMS &&
+          !__all_sync(AR_ALL, mbar_wait_bounded(item_empty(buf), ((k / AR_ITEMS) - 1) & 1, abort_flag, p.status)))
+        return;
+      if (more) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float mult = p.scale;
+          if (E4M3) {
+            float amax = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(w[nt][ks][c] & 0xFFFFu)), fabsf(bf16_bits_to_f32(w[nt][ks][c] >> 16))));
+            amax = fmaxf(amax, __shfl_xor_sync(AR_ALL, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(AR_ALL, amax, 2));
+            // 2^-e brings amax into [2^14, 2^15)
+            const int e = amax > 0.0f && amax < INFINITY ? ilogbf(amax) - 14 : 0;
+            // in two factors: 2^-e alone may lie outside fp32
+            const int e1 = min(max(-e, -100), 100);
+            const float down = scalbnf(1.0f, e1), rest = scalbnf(1.0f, -e - e1);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                w[nt][ks][c] = f32x2_to_f16x2(bf16_bits_to_f32(w[nt][ks][c] & 0xFFFFu) * down * rest,
+                                              bf16_bits_to_f32(w[nt][ks][c] >> 16) * down * rest);
+            mult = p.scale * p.k_scale[g.h] * scalbnf(1.0f, e);
+          }
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            qfrag[buf * S::QFRAGS + (ks * NT + nt) * 32 + lane] = make_uint2(w[nt][ks][0], w[nt][ks][1]);
+          if (quad == 0) {
+            row_mult[buf * ROWS + nt * 8 + oct] = mult;
+            // the position, from the item's first row's
+            row_pos[buf * ROWS + nt * 8 + oct] = tok[nt] >= 0 ? g.p0 + (tok[nt] - g.r0 / p.group) : -1;
+          }
+        }
+      } else {
+        g.done = 1;
+      }
+      if (lane == 0) items[buf] = g;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_full(buf));
+      if (!more) return;
+    }
   }
 
   // -------------------------------------------------------------- consumers
   const int quad = lane & 3, oct = lane >> 2;
   const int tok0 = warp * 16;                                  // this warp's tokens of a tile
-  const int my_box = tok0 / box;
+  const int my_box = tok0 >> box_log2;
   // byte offsets of this lane's ldmatrix rows inside a tile
   const int k_row = (tok0 & (box - 1)) + (lane & 15);
   const int v_row = (tok0 & (box - 1)) + (lane & 7) +
                     (E4M3 ? ((lane >> 3) & 1) * 8 : ((lane >> 4) & 1) * 8);
-  const uint32_t box_off = static_cast<uint32_t>(my_box * box * S::ROW_BYTES);
+  const uint32_t box_off = static_cast<uint32_t>((my_box << box_log2) * S::ROW_BYTES);
   auto swz = [&](int row, int chunk) {                         // 16-byte chunk of a box row
     const int half = S::SEG == 128 ? chunk >> 3 : 0;
     const int c = S::SEG == 128 ? (chunk & 7) ^ (row & 7) : chunk ^ ((row >> 1) & 3);
-    return static_cast<uint32_t>(half * box * S::SEG + row * S::SEG + (c << 4));
+    return static_cast<uint32_t>(((half << box_log2) + row) * S::SEG + (c << 4));
   };
 
-  int it = 0;
+  int st = 0, par = 0;                                         // ring slot, parity of its next filling
   bool ok = true;
-  float o[S::KS][NT][4];
+  float o[KS][NT][4];
   float m[NT][2], l[NT][2];
-  while (walk.next(g)) {
-    const int key_end = static_cast<int>(cap < g.len ? cap : g.len);
-    const int r0 = g.rb * ROWS, n_rows = min(ROWS, g.n * p.group - r0);
-    const int p0 = g.len - g.n + r0 / p.group, p1 = g.len - g.n + (r0 + n_rows - 1) / p.group;
-    const KvTiles tl = kv_tiles<AR_TILE>(p0, p1, p.window, p.sinks, key_end);
-    const int i1 = min(g.i1, tl.count);
-    // query fragments (B of m16n8k16: k = d, n = row), one eight-row tile per warp
-    if (warp < NT) {
-      const int r = r0 + warp * 8 + oct;
-      const bool live = warp * 8 + oct < n_rows;
-      const int i = r / p.group;
-      const uint16_t* src = p.q + static_cast<int64_t>(g.row0 + i) * p.q_stride +
-                            (static_cast<int64_t>(g.h) * p.group + (r - i * p.group)) * D;
-      uint32_t w[S::KS][2];
+  for (int k = 0;; ++k) {
+    const int buf = k % AR_ITEMS;
+    // a wait that gives up ends every consumer here: they agree on `ok` at the end of each item
+    if (!ar_all<CONSUMERS>(ok && mbar_wait_bounded(item_full(buf), (k / AR_ITEMS) & 1, abort_flag, p.status))) return;
+    g = items[buf];
+    if (g.done) return;
+    const uint2* qf = qfrag + buf * S::QFRAGS + lane;
+    uint2 qreg[S::Q_REGS ? KS : 1][S::Q_REGS ? NT : 1];
+    if constexpr (S::Q_REGS) {
 #pragma unroll
-      for (int ks = 0; ks < S::KS; ++ks) {
-        if (E4M3) {
-          // an 8-bit ldmatrix hands a lane four consecutive d's: the same order here
-          const uint2 x = live ? *reinterpret_cast<const uint2*>(src + 16 * ks + 4 * quad) : make_uint2(0u, 0u);
-          w[ks][0] = x.x;
-          w[ks][1] = x.y;
-        } else {
-          w[ks][0] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * quad) : 0u;
-          w[ks][1] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 + 2 * quad) : 0u;
-        }
-      }
-      float mult = p.scale;
-      if (E4M3) {
-        float amax = 0.0f;
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < S::KS; ++ks)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(w[ks][c] & 0xFFFFu)), fabsf(bf16_bits_to_f32(w[ks][c] >> 16))));
-        amax = fmaxf(amax, __shfl_xor_sync(AR_ALL, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(AR_ALL, amax, 2));
-        // 2^-e brings amax into [2^14, 2^15)
-        const int e = amax > 0.0f && amax < INFINITY ? ilogbf(amax) - 14 : 0;
-        // in two factors: 2^-e alone may lie outside fp32
-        const int e1 = min(max(-e, -100), 100);
-        const float down = scalbnf(1.0f, e1), rest = scalbnf(1.0f, -e - e1);
-#pragma unroll
-        for (int ks = 0; ks < S::KS; ++ks)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            w[ks][c] = f32x2_to_f16x2(bf16_bits_to_f32(w[ks][c] & 0xFFFFu) * down * rest,
-                                      bf16_bits_to_f32(w[ks][c] >> 16) * down * rest);
-        mult = p.scale * p.k_scale[g.h] * scalbnf(1.0f, e);
-      }
-#pragma unroll
-      for (int ks = 0; ks < S::KS; ++ks) qfrag[(ks * NT + warp) * 32 + lane] = make_uint2(w[ks][0], w[ks][1]);
-      if (quad == 0) {
-        row_mult[warp * 8 + oct] = mult;
-        row_pos[warp * 8 + oct] = live ? g.len - g.n + i : -1;
-      }
+        for (int nt = 0; nt < NT; ++nt) qreg[ks][nt] = qf[(ks * NT + nt) * 32];
     }
-    ar_consumer_sync();
-    uint2 qreg[NT <= 2 ? S::KS : 1][NT <= 2 ? NT : 1];
-    if constexpr (NT <= 2) {
-#pragma unroll
-      for (int ks = 0; ks < S::KS; ++ks)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) qreg[ks][nt] = qfrag[(ks * NT + nt) * 32 + lane];
-    }
+    auto q_at = [&](int ks, int nt) {
+      if constexpr (S::Q_REGS)
+        return qreg[ks][nt];
+      else
+        return qf[(ks * NT + nt) * 32];
+    };
     float mult[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        mult[nt][c] = row_mult[nt * 8 + 2 * quad + c];
+        mult[nt][c] = row_mult[buf * ROWS + nt * 8 + 2 * quad + c];
         m[nt][c] = -INFINITY;
         l[nt][c] = 0.0f;
       }
 #pragma unroll
-    for (int mt = 0; mt < S::KS; ++mt)
+    for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[mt][nt][c] = 0.0f;
 
-    for (int i = g.i0; i < i1; ++i, ++it) {
-      const int st = it % S::STAGES;
-      if (ok) ok = __all_sync(AR_ALL, mbar_wait_bounded(full_bar(st), (it / S::STAGES) & 1, abort_flag, p.status));
-      if (!ok) continue;
-      const int j0 = tl.tile(i) * AR_TILE;                     // the tile's first position
+    for (int i = g.i0; i < g.i1; ++i) {
+      if (ok) ok = __all_sync(AR_ALL, mbar_wait_bounded(full_bar(st), par, abort_flag, p.status));
+      if (!ok) break;
+      const int j0 = g.tiles.tile(i) * TILE;                     // the tile's first position
       const bool box_ok = (stage_ok[st] >> my_box) & 1u;
       const uint32_t kb = stage_k(st) + box_off, vb = kb + S::MAT_BYTES;
       // S^T = K Q^T
@@ -437,7 +499,7 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
         for (int c = 0; c < 4; ++c) s[nt][c] = 0.0f;
       if constexpr (E4M3) {
 #pragma unroll
-        for (int k2 = 0; k2 < S::KS / 2; ++k2) {
+        for (int k2 = 0; k2 < KS / 2; ++k2) {
           uint32_t r[4];
           ldsm_x4(kb + swz(k_row, 2 * k2 + (lane >> 4)), r);
 #pragma unroll
@@ -445,29 +507,22 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
             const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * hf] & 0xFFFFu), e4m3x2_to_f16x2(r[2 * hf + 1] & 0xFFFFu),
                                    e4m3x2_to_f16x2(r[2 * hf] >> 16), e4m3x2_to_f16x2(r[2 * hf + 1] >> 16)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 qb = NT <= 2 ? qreg[NT <= 2 ? 2 * k2 + hf : 0][NT <= 2 ? nt : 0]
-                                       : qfrag[((2 * k2 + hf) * NT + nt) * 32 + lane];
-              mma_f16_16816(s[nt], a, qb.x, qb.y);
-            }
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a, q_at(2 * k2 + hf, nt).x, q_at(2 * k2 + hf, nt).y);
           }
         }
       } else {
 #pragma unroll
-        for (int ks = 0; ks < S::KS; ++ks) {
+        for (int ks = 0; ks < KS; ++ks) {
           uint32_t a[4];
           ldsm_x4(kb + swz(k_row, 2 * ks + (lane >> 4)), a);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 qb = NT <= 2 ? qreg[NT <= 2 ? ks : 0][NT <= 2 ? nt : 0] : qfrag[(ks * NT + nt) * 32 + lane];
-            mma_bf16_16816(s[nt], a, qb.x, qb.y);
-          }
+          for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(s[nt], a, q_at(ks, nt).x, q_at(ks, nt).y);
         }
       }
       // scores in powers of two; masked ones replaced
-      const bool all_seen = stage_ok[st] == (1u << boxes) - 1u && j0 + AR_TILE - 1 <= p0 &&
-                            j0 + AR_TILE <= key_end &&
-                            (p.window <= 0 || p1 - j0 < p.window || j0 + AR_TILE <= p.sinks);
+      const bool all_seen = stage_ok[st] == (1u << boxes) - 1u && j0 + TILE - 1 <= g.p0 &&
+                            j0 + TILE <= g.key_end &&
+                            (p.window <= 0 || g.p1 - j0 < p.window || j0 + TILE <= p.sinks);
       uint32_t keep[2] = {AR_ALL, AR_ALL};                     // value rows of tokens 2 quad, +1 (and + 8)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -475,16 +530,16 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
         for (int c = 0; c < 4; ++c) s[nt][c] *= mult[nt][c & 1];
       if (!all_seen) {
         auto none_sees = [&](int j) {
-          return !box_ok || j > p1 || j >= key_end || (p.window > 0 && j >= p.sinks && p0 - j >= p.window);
+          return !box_ok || j > g.p1 || j >= g.key_end || (p.window > 0 && j >= p.sinks && g.p0 - j >= p.window);
         };
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int j = j0 + tok0 + oct + (c >> 1) * 8;
-            const int pos = row_pos[nt * 8 + 2 * quad + (c & 1)];
-            const bool sees = box_ok && j <= pos && j < key_end &&
-                              (p.window <= 0 || pos - j < p.window || j < p.sinks);
+            const int at_pos = row_pos[buf * ROWS + nt * 8 + 2 * quad + (c & 1)];
+            const bool sees = box_ok && j <= at_pos && j < g.key_end &&
+                              (p.window <= 0 || at_pos - j < p.window || j < p.sinks);
             if (!sees) s[nt][c] = -INFINITY;
           }
 #pragma unroll
@@ -528,7 +583,7 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
       }
       if (__any_sync(AR_ALL, moved)) {
 #pragma unroll
-        for (int mt = 0; mt < S::KS; ++mt)
+        for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -537,7 +592,7 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
       // O^T += V^T P^T
       if constexpr (E4M3) {
 #pragma unroll
-        for (int m2 = 0; m2 < S::KS / 2; ++m2) {
+        for (int m2 = 0; m2 < KS / 2; ++m2) {
           uint32_t r[4];
           ldsm_x4_t(vb + swz(v_row, 2 * m2 + (lane >> 4)), r);
 #pragma unroll
@@ -551,7 +606,7 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
         }
       } else {
 #pragma unroll
-        for (int mt = 0; mt < S::KS; ++mt) {
+        for (int mt = 0; mt < KS; ++mt) {
           uint32_t a[4];
           ldsm_x4_t(vb + swz(v_row, 2 * mt + ((lane >> 3) & 1)), a);
           a[0] &= keep[0];
@@ -567,9 +622,15 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty_bar(st));
+      if (++st == stages) {
+        st = 0;
+        par ^= 1;
+      }
     }
 
-    // the four warps' parts meet
+    // the item's rows and fragments have been read; the warps' parts meet
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_empty(buf));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -582,11 +643,11 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
           warp_l[warp * ROWS + nt * 8 + 2 * quad + c] = l[nt][c];
         }
       }
-    ar_consumer_sync();
+    ar_consumer_sync<CONSUMERS>();
     auto row_max = [&](int r) {
       float x = warp_m[r];
 #pragma unroll
-      for (int w = 1; w < AR_WARPS; ++w) x = fmaxf(x, warp_m[w * ROWS + r]);
+      for (int w = 1; w < WARPS; ++w) x = fmaxf(x, warp_m[w * ROWS + r]);
       return x;
     };
     float f[NT][2];
@@ -597,29 +658,30 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
         const float x = row_max(nt * 8 + 2 * quad + c);
         f[nt][c] = exp2_approx(m[nt][c] - (x == -INFINITY ? 0.0f : x));
       }
-    constexpr int TURNS = AR_WARPS / MERGE_BUFS;
+    constexpr int TURNS = WARPS / BUFS;
 #pragma unroll 1
     for (int turn = 0; turn < TURNS; ++turn) {
-      if (warp / MERGE_BUFS == turn) {
-        float* buf = merge + (warp % MERGE_BUFS) * ROWS * OSTR;
+      if (warp / BUFS == turn) {
+        float* mbuf = merge + (warp % BUFS) * ROWS * OSTR;
 #pragma unroll
-        for (int mt = 0; mt < S::KS; ++mt)
+        for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int d = 16 * mt + (E4M3 ? 2 * oct + (c >> 1) : oct + 8 * (c >> 1));
-              float* x = buf + (nt * 8 + 2 * quad + (c & 1)) * OSTR + d;
+              float* x = mbuf + (nt * 8 + 2 * quad + (c & 1)) * OSTR + d;
               const float y = o[mt][nt][c] * f[nt][c & 1];
               *x = turn == 0 ? y : *x + y;
             }
       }
-      ar_consumer_sync();
+      ar_consumer_sync<CONSUMERS>();
     }
     auto merged = [&](int r, int d) {
       float4 x = *reinterpret_cast<const float4*>(merge + r * OSTR + d);
-      if constexpr (MERGE_BUFS == 2) {
-        const float4 y = *reinterpret_cast<const float4*>(merge + (ROWS + r) * OSTR + d);
+#pragma unroll
+      for (int w = 1; w < BUFS; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(merge + (w * ROWS + r) * OSTR + d);
         x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
       }
       return x;
@@ -628,26 +690,25 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
       const float use = mx == -INFINITY ? 0.0f : mx;
       float x = 0.0f;
 #pragma unroll
-      for (int w = 0; w < AR_WARPS; ++w) x += warp_l[w * ROWS + r] * exp2_approx(warp_m[w * ROWS + r] - use);
+      for (int w = 0; w < WARPS; ++w) x += warp_l[w * ROWS + r] * exp2_approx(warp_m[w * ROWS + r] - use);
       return x;
     };
     const float v_mult = E4M3 ? p.v_scale[g.h] : 1.0f;
     auto store = [&](int r, int d, float4 x, float sum) {
       const float inv = sum > 0.0f ? v_mult / sum : (sum == 0.0f ? 0.0f : sum);   // a NaN stays one
-      const int i = (r0 + r) / p.group;
-      const int64_t head = static_cast<int64_t>(g.h) * p.group + (r0 + r - i * p.group);
+      const int i = (g.r0 + r) / p.group;
+      const int64_t head = static_cast<int64_t>(g.h) * p.group + (g.r0 + r - i * p.group);
       uint16_t* dst = p.out + (static_cast<int64_t>(g.row0 + i) * p.heads * p.group + head) * D + d;
       *reinterpret_cast<uint2*>(dst) = make_uint2(f32x2_to_bf16x2(x.x * inv, x.y * inv), f32x2_to_bf16x2(x.z * inv, x.w * inv));
     };
-    const unsigned first_cta = g.item_u0 / per, last_cta = (g.item_u0 + static_cast<unsigned>(g.per_item) - 1u) / per;
-    ok = ar_all(ok);
+    ok = ar_all<CONSUMERS>(ok);
     if (!ok) continue;   // a wait gave up: nothing more is written
+    const unsigned first_cta = g.first_cta, last_cta = g.last_cta;
     if (first_cta == last_cta) {
-      for (int x = threadIdx.x; x < n_rows * (D / 4); x += AR_WARPS * 32) {
+      for (int x = threadIdx.x; x < g.n_rows * (D / 4); x += CONSUMERS) {
         const int r = x / (D / 4), d = (x % (D / 4)) * 4;
         store(r, d, merged(r, d), row_sum(r, row_max(r)));
       }
-      ar_consumer_sync();   // the merge buffers may be written again
       continue;
     }
     // this CTA's part, then the join by the last one to arrive
@@ -655,16 +716,16 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
       return p.part + (static_cast<int64_t>(cta) * 2 + (cta == first_cta ? 1 : 0)) * (ROWS * (D + 2));
     };
     float* mine = part(blockIdx.x);
-    for (int x = threadIdx.x; x < n_rows * (D / 4); x += AR_WARPS * 32) {
+    for (int x = threadIdx.x; x < g.n_rows * (D / 4); x += CONSUMERS) {
       const int r = x / (D / 4), d = (x % (D / 4)) * 4;
       __stcg(reinterpret_cast<float4*>(mine + r * D + d), merged(r, d));
     }
-    for (int r = threadIdx.x; r < n_rows; r += AR_WARPS * 32) {
+    for (int r = threadIdx.x; r < g.n_rows; r += CONSUMERS) {
       const float mx = row_max(r);
       __stcg(reinterpret_cast<float2*>(mine + ROWS * D + 2 * r), make_float2(mx, row_sum(r, mx)));
     }
     fence_acq_rel_gpu();
-    ar_consumer_sync();
+    ar_consumer_sync<CONSUMERS>();
     if (threadIdx.x == 0) {
       const unsigned n_parts = last_cta - first_cta + 1;
       const unsigned before = atomicAdd(p.arrived + first_cta, 1u);
@@ -672,18 +733,18 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
       if (before + 1 == n_parts) p.arrived[first_cta] = 0;    // ready for the next call
       fence_acq_rel_gpu();
     }
-    ar_consumer_sync();
+    ar_consumer_sync<CONSUMERS>();
     if (*last_flag) {
       fence_acq_rel_gpu();
-      for (int x = threadIdx.x; x < n_rows * (D / 4); x += AR_WARPS * 32) {
+      for (int x = threadIdx.x; x < g.n_rows * (D / 4); x += CONSUMERS) {
         const int r = x / (D / 4), d = (x % (D / 4)) * 4;
         float mx = -INFINITY;
-        for (unsigned c = first_cta; c <= last_cta; ++c)
-          mx = fmaxf(mx, __ldcg(part(c) + ROWS * D + 2 * r));
+#pragma unroll 8
+        for (unsigned c = first_cta; c <= last_cta; ++c) mx = fmaxf(mx, __ldcg(part(c) + ROWS * D + 2 * r));
         const float use = mx == -INFINITY ? 0.0f : mx;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float sum = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
         for (unsigned c = first_cta; c <= last_cta; ++c) {
           const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(c) + ROWS * D + 2 * r));
           const float4 y = __ldcg(reinterpret_cast<const float4*>(part(c) + r * D + d));
@@ -697,7 +758,6 @@ __global__ void __launch_bounds__(AR_THREADS, NT <= 2 ? 2 : 1)
         store(r, d, acc, sum);
       }
     }
-    ar_consumer_sync();   // the merge buffers and the flag may be written again
   }
 }
 
