@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from functools import lru_cache
 from pathlib import Path
 
 import torch
@@ -115,7 +116,8 @@ def _ptr(t):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the raw handle: torch.cuda.current_stream() takes about 3 us to build its object
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _require_cuda(*ts):
@@ -145,6 +147,7 @@ def scales_bytes(rows: int, K: int, layout: int) -> int:
     return int(lib().nvfp4_scales_bytes(rows, K, layout))
 
 
+@lru_cache(maxsize=1024)
 def workspace_size(op: int, a=0, b=0, c=0, e=0, topk=0) -> int:
     return int(lib().nvfp4_workspace_size(op, a, b, c, e, topk))
 
@@ -395,33 +398,37 @@ def kv_cache(pages: int, heads: int, page_size: int, head_dim: int, dtype: torch
 
 
 def _int32(t, name, dim=1):
-    if t.dtype != torch.int32 or t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    """Shape of an int32 tensor on the device whose last dimension is contiguous."""
+    shape = t.shape
+    if not t.is_cuda:
+        _require_cuda(t)
+    if t.dtype != torch.int32 or len(shape) != dim or (shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name}: an int32 tensor of {dim} dimension(s), the last one contiguous, is needed")
+    return shape
 
 
-def _table_stride(table):
-    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+def _table_stride(table, shape):
+    return table.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _seqs(table, lens, start, max_new) -> CKVSeqs:
-    _require_cuda(table, lens, start)
-    _int32(table, "table", 2)
-    _int32(lens, "lens")
-    batch = lens.shape[0]
-    if table.shape[0] != batch:
+    shape = _int32(table, "table", 2)
+    batch, = _int32(lens, "lens")
+    if shape[0] != batch:
         raise ValueError("table: one row for each entry of lens is needed")
-    if start is not None:
-        _int32(start, "start")
-        if start.shape[0] != batch + 1:
-            raise ValueError("start: batch + 1 offsets are needed")
-    return CKVSeqs(table.data_ptr(), lens.data_ptr(), None if start is None else start.data_ptr(), _table_stride(table),
-                   batch, table.shape[1], max_new, 0)
+    if start is not None and _int32(start, "start")[0] != batch + 1:
+        raise ValueError("start: batch + 1 offsets are needed")
+    return CKVSeqs(table.data_ptr(), lens.data_ptr(), None if start is None else start.data_ptr(),
+                   _table_stride(table, shape), batch, shape[1], max_new, 0)
 
 
 def _token_rows(x, heads, dim, name):
     """x bf16 [T][heads][dim] with a token stride the kernels take (a copy if it has another layout)."""
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+    _, h, d = x.shape if x.dim() == 3 else (0, -1, -1)
+    if x.dtype != torch.bfloat16 or h != heads or d != dim:
         raise ValueError(f"{name}: bf16 [tokens][{heads}][{dim}] is needed")
+    if not x.is_cuda:
+        _require_cuda(x)
     s = x.stride()
     if s[2] != 1 or (s[1] != dim and heads > 1) or s[0] % 8 or s[0] < heads * dim or x.data_ptr() % 16:
         x = x.contiguous()
@@ -436,8 +443,7 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Ten
     fused projection) to their positions, the last ones of each sequence.
     lens counts the new tokens; sequence b's are rows start[b] .. start[b + 1] - 1
     (start None: max_new for every sequence)."""
-    _require_cuda(k, v)
-    c = cache.c()
+    c = cache._c
     k, v = _token_rows(k, c.heads, c.head_dim, "k"), _token_rows(v, c.heads, c.head_dim, "v")
     if k.shape != v.shape:
         raise ValueError("kv_append: k and v need the same shape")
@@ -463,16 +469,15 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     window > 0 a position sees the last `window` positions and the first
     `sinks`. scale defaults to head_dim ** -0.5. A row that sees nothing gives
     zeros. `workspace`: attention_workspace(...), kept between calls of one stream."""
-    _require_cuda(q)
-    c = cache.c()
-    if q.dim() != 3:
-        raise ValueError("q: bf16 [tokens][q_heads][head_dim] is needed")
-    T, heads, D = q.shape
+    c = cache._c
+    T, heads, D = q.shape if q.dim() == 3 else (0, -1, -1)
     q = _token_rows(q, heads, c.head_dim, "q")
     if out is None:
-        o = torch.empty(T, heads, D, dtype=torch.bfloat16, device=q.device)
+        # (empty_like is the cheapest allocation to ask for)
+        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(T, heads, D, dtype=q.dtype, device=q.device)
     else:
         o = out
+        _require_cuda(o)
         if o.shape != (T, heads, D) or o.dtype != torch.bfloat16 or not o.is_contiguous():
             raise ValueError("out: contiguous bf16 of q's shape is needed")
     seqs = _seqs(table, lens, start, max_new)
@@ -491,26 +496,22 @@ def kv_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page
                start: torch.Tensor | None = None, max_new: int = 1, workspace: torch.Tensor | None = None) -> None:
     """Pages (lowest free ids first) for the positions of the new tokens whose
     table entry holds none; refs int32 [pages] counts a page's users."""
-    _require_cuda(refs)
-    _int32(refs, "refs")
+    pages, = _int32(refs, "refs")
     seqs = _seqs(table, lens, start, max_new)
     tokens = seqs.batch * max_new if start is None else (1 << 30) - 1   # start says how many
-    ws = _pages_ws(workspace, refs.shape[0], seqs.batch, refs.device)
-    _check(lib().nvfp4_kv_reserve(seqs, tokens, page_size, table.data_ptr(), refs.data_ptr(), refs.shape[0],
+    ws = _pages_ws(workspace, pages, seqs.batch, refs.device)
+    _check(lib().nvfp4_kv_reserve(seqs, tokens, page_size, table.data_ptr(), refs.data_ptr(), pages,
                                   ws.data_ptr(), ws.numel(), _stream()), "nvfp4_kv_reserve")
 
 
 def _pool_args(table, lens, refs, pages=None):
-    _require_cuda(table, lens, refs)
-    _int32(table, "table", 2)
-    _int32(refs, "refs")
-    if pages is not None and refs.shape[0] != pages:
+    shape = _int32(table, "table", 2)
+    n, = _int32(refs, "refs")
+    if pages is not None and n != pages:
         raise ValueError("refs: one count for each page is needed")
-    if lens is not None:
-        _int32(lens, "lens")
-        if lens.shape[0] != table.shape[0]:
-            raise ValueError("lens: one length for each row of the table is needed")
-    return table.data_ptr(), _table_stride(table), table.shape[1]
+    if lens is not None and _int32(lens, "lens")[0] != shape[0]:
+        raise ValueError("lens: one length for each row of the table is needed")
+    return table.data_ptr(), _table_stride(table, shape), shape[1]
 
 
 def kv_fork(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, src: torch.Tensor,
@@ -518,14 +519,11 @@ def kv_fork(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, refs: torch
     """Rows dst[f] of the table become forks of rows src[f]: full pages are
     shared, the positions in use of a partly filled last page are copied to a
     fresh page. dst rows must be empty, distinct and not in src."""
-    _require_cuda(src, dst)
-    _int32(src, "src")
-    _int32(dst, "dst")
-    if src.shape != dst.shape:
+    n, = _int32(src, "src")
+    if _int32(dst, "dst")[0] != n:
         raise ValueError("kv_fork: src and dst need the same length")
-    c = cache.c()
+    c = cache._c
     args = _pool_args(table, lens, refs, c.pages)
-    n = src.shape[0]
     ws = _pages_ws(workspace, c.pages, n, refs.device)
     _check(lib().nvfp4_kv_fork(c, *args, lens.data_ptr(), table.shape[0], refs.data_ptr(), src.data_ptr(),
                                dst.data_ptr(), n, ws.data_ptr(), ws.numel(), _stream()), "nvfp4_kv_fork")
@@ -534,18 +532,17 @@ def kv_fork(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, refs: torch
 def kv_release(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seqs: torch.Tensor) -> None:
     """Give up the sequences of rows seqs (distinct): their pages' counts go
     down, their entries to -1 and their lengths to 0."""
-    _require_cuda(seqs)
-    _int32(seqs, "seqs")
+    n, = _int32(seqs, "seqs")
     args = _pool_args(table, lens, refs)
     _check(lib().nvfp4_kv_release(*args, lens.data_ptr(), table.shape[0], refs.data_ptr(), refs.shape[0],
-                                  seqs.data_ptr(), seqs.shape[0], _stream()), "nvfp4_kv_release")
+                                  seqs.data_ptr(), n, _stream()), "nvfp4_kv_release")
 
 
 def kv_compact(cache: KVCache, table: torch.Tensor, refs: torch.Tensor,
                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Move the live pages to the ids below their number (pages already there
     stay); returns that number, int32 on the device."""
-    c = cache.c()
+    c = cache._c
     args = _pool_args(table, None, refs, c.pages)
     live = torch.empty((), dtype=torch.int32, device=refs.device)
     ws = _pages_ws(workspace, c.pages, 0, refs.device)

@@ -18,8 +18,10 @@ int log2_of(int x) {
   return n;
 }
 
-// Eight-row tiles of a call of the split kernel.
-int rows_nt(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
+// Eight-row tiles of an item of the split kernel. An E4M3 cache with more than
+// 24 rows takes two items of 16: the fragments of four tiles beside the
+// conversions' do not fit the registers.
+int rows_nt(int64_t rows, bool e4m3) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : e4m3 ? 2 : 4; }
 
 // CTAs of the split kernel: two per SM for one eight-row tile, else one of more warps.
 int rows_grid(int nt) { return (nt == 1 ? 2 : 1) * sm_count(); }
@@ -28,14 +30,14 @@ constexpr int64_t COUNTER_BYTES = 4096;   // arrival counters at the front of th
 constexpr int SMEM_SM = 227 * 1024;       // dynamic shared memory of the CTAs of an SM (1 KB each is reserved beside it)
 
 // One page of one head as [halves][rows][seg bytes], a copy box of `box` rows of `box_halves` halves.
-int kv_map(CUtensorMap* map, const void* pool, const nvfp4_kv_cache_t& c, int box, int box_halves) {
+int kv_map(CUtensorMap* map, const void* pool, const nvfp4_kv_cache_t& c, int box, int box_halves, bool swizzled = true) {
   const int64_t row = static_cast<int64_t>(c.head_dim) * (c.dtype == NVFP4_DTYPE_BF16 ? 2 : 1);
   const int64_t seg = row >= 128 ? 128 : 64, halves = row / seg;
   const int64_t dims[4] = {seg, c.page_size, halves, c.pages * c.heads};
   const int64_t strides[3] = {row, halves > 1 ? seg : row * c.page_size, row * c.page_size};
   const int boxes[4] = {static_cast<int>(seg), box, box_halves, 1};
   return make_tmap_4d_u8(map, pool, dims, strides, boxes,
-                         seg == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                         !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : seg == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 template <bool E4M3, int D, int WARPS, int NT>
@@ -45,7 +47,7 @@ int launch_rows(ArParams p, const nvfp4_kv_cache_t& c, cudaStream_t stream) {
   const int box = c.page_size < S::TILE ? c.page_size : S::TILE;
   if (int rc = kv_map(&mk, c.k, c, box, S::HALVES)) return rc;
   if (int rc = kv_map(&mv, c.v, c, box, S::HALVES)) return rc;
-  const int fixed = S::FIXED_BYTES + 4 * (p.s.batch + 2);
+  const int fixed = S::FIXED_BYTES + 4 * (p.s.batch + 2) + (p.s.batch <= AR_KEPT ? 4 * (2 * p.s.batch + 2) : 0);
   const int room = (SMEM_SM - (S::CTAS - 1) * 1024) / S::CTAS - fixed;
   p.stages = std::max(2, std::min(AR_MAX_STAGES, room / S::STAGE_BYTES));
   const int smem = fixed + p.stages * S::STAGE_BYTES;
@@ -61,7 +63,9 @@ int launch_rows_nt(int nt, const ArParams& p, const nvfp4_kv_cache_t& c, cudaStr
     case 1: return launch_rows<E4M3, D, 4, 1>(p, c, stream);
     case 2: return launch_rows<E4M3, D, 8, 2>(p, c, stream);
     case 3: return launch_rows<E4M3, D, 8, 3>(p, c, stream);
-    default: return launch_rows<E4M3, D, 8, 4>(p, c, stream);
+    default:
+      if constexpr (E4M3) return NVFP4_ERR_UNSUPPORTED_SHAPE;   // not chosen (rows_nt)
+      else return launch_rows<E4M3, D, 8, 4>(p, c, stream);
   }
 }
 
@@ -70,7 +74,7 @@ int64_t tiles_items(int64_t tokens, int64_t batch, int64_t heads, int group) {
   return heads * (tokens / (2 * (AT_ROWS / group)) + batch);
 }
 
-template <int D>
+template <bool E4M3, int D>
 int launch_tiles(const uint16_t* Q, int64_t q_stride, int q_heads, const nvfp4_kv_cache_t& c, AtParams& p,
                  cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
@@ -78,18 +82,20 @@ int launch_tiles(const uint16_t* Q, int64_t q_stride, int q_heads, const nvfp4_k
   const int64_t q_strides[3] = {D * 2, q_stride * 2, 128};
   const int q_box[4] = {128, p.group, AT_ROWS / p.group, 1};
   if (int rc = make_tmap_4d_u8(&mq, Q, q_dims, q_strides, q_box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
-  const int box = c.page_size < AT_TILE ? c.page_size : AT_TILE;
-  if (int rc = kv_map(&mk, c.k, c, box, 1)) return rc;
-  if (int rc = kv_map(&mv, c.v, c, box, 1)) return rc;
+  // E4M3 codes are copied as they lie, in boxes of up to a chunk's rows
+  constexpr int most = E4M3 ? AT_CHUNK : AT_TILE;
+  const int box = c.page_size < most ? c.page_size : most;
+  if (int rc = kv_map(&mk, c.k, c, box, 1, !E4M3)) return rc;
+  if (int rc = kv_map(&mv, c.v, c, box, 1, !E4M3)) return rc;
   const int64_t items = tiles_items(p.s.tokens, p.s.batch, c.heads, p.group);
   const int ctas = sm_count();
   // fewer items than half the SMs: each is split over its positions
   p.parts = items < ctas ? static_cast<int>(ctas / items) : 1;
   const int64_t units = items * p.parts;
-  const int rc = ensure_smem(attention_tiles_kernel<D>, AtShape<D>::SMEM);
+  const int rc = ensure_smem(attention_tiles_kernel<E4M3, D>, AtShape<E4M3, D>::SMEM);
   if (rc) return rc;
-  return launch_ex(attention_tiles_kernel<D>, dim3(static_cast<unsigned>(units < ctas ? units : ctas)), dim3(AT_THREADS),
-                   AtShape<D>::SMEM, 1, true, stream, mq, mk, mv, p);
+  return launch_ex(attention_tiles_kernel<E4M3, D>, dim3(static_cast<unsigned>(units < ctas ? units : ctas)), dim3(AT_THREADS),
+                   AtShape<E4M3, D>::SMEM, 1, true, stream, mq, mk, mv, p);
 }
 
 // Rows of a kv head from which the tile kernel takes a call.
@@ -100,8 +106,11 @@ bool takes_tiles(int64_t rows) { return rows > 32; }
 size_t attention_workspace_bytes(int64_t batch, int64_t max_new, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
   if (batch <= 0 || max_new <= 0 || kv_heads <= 0 || q_heads <= 0 || head_dim <= 0) return 0;
   const int64_t rows = max_new * (q_heads / kv_heads);
-  const int nt = rows_nt(rows);
-  int64_t parts = static_cast<int64_t>(rows_grid(nt)) * 2 * 8 * nt;               // rows of partial sums
+  int64_t parts = 0;                                                              // rows of partial sums
+  for (bool e4m3 : {false, true}) {
+    const int nt = rows_nt(rows, e4m3);
+    parts = std::max(parts, static_cast<int64_t>(rows_grid(nt)) * 2 * 8 * nt);
+  }
   if (takes_tiles(rows)) parts = std::max(parts, static_cast<int64_t>(sm_count()) * 2 * AT_ROWS);
   return static_cast<size_t>(COUNTER_BYTES + parts * (head_dim + 2) * 4);
 }
@@ -113,7 +122,8 @@ int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, con
   if (!status) return NVFP4_ERR_CUDA;
   const int group = q_heads / c.heads;
   const int64_t rows = static_cast<int64_t>(s.max_new) * group;
-  if (takes_tiles(rows) && c.dtype == NVFP4_DTYPE_BF16 && group <= AT_ROWS / 2 && scale > 0.0f) {
+  const bool e4m3 = c.dtype == NVFP4_DTYPE_E4M3;
+  if (takes_tiles(rows) && group <= AT_ROWS / 2 && scale > 0.0f) {
     AtParams p;
     p.s = s;
     p.out = out;
@@ -128,10 +138,15 @@ int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, con
     p.arrived = static_cast<unsigned*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + COUNTER_BYTES);
     p.status = status;
-    return c.head_dim == 128 ? launch_tiles<128>(Q, q_stride, q_heads, c, p, stream)
-                             : launch_tiles<64>(Q, q_stride, q_heads, c, p, stream);
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
+    if (c.head_dim == 128)
+      return e4m3 ? launch_tiles<true, 128>(Q, q_stride, q_heads, c, p, stream)
+                  : launch_tiles<false, 128>(Q, q_stride, q_heads, c, p, stream);
+    return e4m3 ? launch_tiles<true, 64>(Q, q_stride, q_heads, c, p, stream)
+                : launch_tiles<false, 64>(Q, q_stride, q_heads, c, p, stream);
   }
-  const int nt = rows_nt(rows);
+  const int nt = rows_nt(rows, e4m3);
   if (4 * rows_grid(nt) > COUNTER_BYTES) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   ArParams p;
   p.s = s;
@@ -150,9 +165,7 @@ int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, con
   p.scale = scale * LOG2_E;
   p.arrived = static_cast<unsigned*>(ws);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + COUNTER_BYTES);
-  p.min_tiles = 1;
   p.status = status;
-  const bool e4m3 = c.dtype == NVFP4_DTYPE_E4M3;
   if (c.head_dim == 128)
     return e4m3 ? launch_rows_nt<true, 128>(nt, p, c, stream) : launch_rows_nt<false, 128>(nt, p, c, stream);
   return e4m3 ? launch_rows_nt<true, 64>(nt, p, c, stream) : launch_rows_nt<false, 64>(nt, p, c, stream);

@@ -49,7 +49,7 @@ namespace {
 
 constexpr int AR_MAX_STAGES = 8;
 constexpr int AR_ITEMS = 2;                  // items announced ahead
-constexpr int AR_MAX_BATCH = 4096;
+constexpr int AR_KEPT = 128;                 // sequences whose lengths are kept in shared memory
 constexpr int AR_PAD = 4;                    // fp32 words between rows of the merge buffer: no bank conflicts
 constexpr unsigned AR_ALL = 0xffffffffu;
 
@@ -67,7 +67,6 @@ struct ArParams {
   float scale;            // softmax scale * log2 e
   unsigned* arrived;      // [CTAs], zero between calls
   float* part;            // [CTAs][2][rows of an item][D + 2]
-  int min_tiles;          // least tiles of a CTA's piece
   int stages;             // of the ring
   int* status;
 };
@@ -160,6 +159,7 @@ template <class S>
 struct ArWalk {
   const ArParams& p;
   const unsigned* pre;   // tiles of the sequences before (shared memory)
+  const int* rows;       // first new-token rows [batch + 1] and lengths [batch], for batches up to AR_KEPT
   unsigned per, u, end;
   int b;                 // the sequence
 
@@ -175,8 +175,10 @@ struct ArWalk {
     }
     b = lo;
     g.done = 0;
-    g.row0 = kv_row0(p.s, lo);
-    const int n = kv_row0(p.s, lo + 1) - g.row0, len = kv_len(p.s, lo);
+    const bool kept = p.s.batch <= AR_KEPT;
+    g.row0 = kept ? rows[lo] : kv_row0(p.s, lo);
+    const int n = (kept ? rows[lo + 1] : kv_row0(p.s, lo + 1)) - g.row0;
+    const int len = kept ? rows[p.s.batch + 1 + lo] : kv_len(p.s, lo);
     const unsigned blocks = static_cast<unsigned>((n * p.group + S::ROWS - 1) / S::ROWS);
     const unsigned per_item = (pre[lo + 1] - pre[lo]) / (blocks * static_cast<unsigned>(p.heads));
     const unsigned in = u - pre[lo], item = in / per_item;
@@ -200,12 +202,11 @@ struct ArWalk {
   }
 };
 
-// Tiles that each block of sequence b's rows is given (the most any sees, at least one).
+// Tiles of all items of a sequence of n new tokens: each block of rows is given
+// the most that any sees, at least one.
 template <class S>
-NVFP4_DEV unsigned ar_seq_tiles(const ArParams& p, int b) {
-  const int n = kv_row0(p.s, b + 1) - kv_row0(p.s, b);
+NVFP4_DEV unsigned ar_seq_tiles(const ArParams& p, int n, int len) {
   if (n <= 0) return 0;
-  const int len = kv_len(p.s, b);
   const int64_t cap = static_cast<int64_t>(p.s.max_pages) * p.page_size;
   const int key_end = static_cast<int>(cap < len ? cap : len);
   const int blocks = (n * p.group + S::ROWS - 1) / S::ROWS;
@@ -249,6 +250,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
   volatile int* abort_flag = reinterpret_cast<volatile int*>(stage_ok + AR_MAX_STAGES);
   unsigned* last_flag = stage_ok + AR_MAX_STAGES + 1;
   unsigned* pre = last_flag + 1;                                                         // [batch + 1]
+  int* rows = reinterpret_cast<int*>(pre + p.s.batch + 1);                               // [2 batch + 1]
   const uint32_t bar0 = smem_addr(bars);
   auto full_bar = [&](int st) { return bar0 + 8u * st; };
   auto empty_bar = [&](int st) { return bar0 + 8u * (AR_MAX_STAGES + st); };
@@ -274,7 +276,15 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
   pdl_launch_dependents();
   pdl_wait();
   // the line of tiles: prefix sums over the sequences
-  for (int b = threadIdx.x; b < p.s.batch; b += S::THREADS) pre[b + 1] = ar_seq_tiles<S>(p, b);
+  for (int b = threadIdx.x; b < p.s.batch; b += S::THREADS) {
+    const int r0 = kv_row0(p.s, b), r1 = kv_row0(p.s, b + 1), len = kv_len(p.s, b);
+    pre[b + 1] = ar_seq_tiles<S>(p, r1 - r0, len);
+    if (p.s.batch <= AR_KEPT) {
+      rows[b] = r0;
+      rows[b + 1] = r1;   // the next thread writes the same
+      rows[p.s.batch + 1 + b] = len;
+    }
+  }
   __syncthreads();
   if (warp == 0) {
     unsigned run = 0;
@@ -293,10 +303,12 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
   __syncthreads();
   const unsigned total = pre[p.s.batch];
   unsigned per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < static_cast<unsigned>(p.min_tiles)) per = static_cast<unsigned>(p.min_tiles);
+  // where a CTA's piece would be one tile of long items, two: half the parts to
+  // join (one sequence of 2,000 positions: 8.8 -> 8.0 us)
+  if (per == 1 && total >= 16u * static_cast<unsigned>(p.s.batch * p.heads)) per = 2;
   const uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * per;
   if (u0 >= total) return;
-  ArWalk<S> walk{p, pre, per, static_cast<unsigned>(u0), static_cast<unsigned>(u0 + per < total ? u0 + per : total), 0};
+  ArWalk<S> walk{p, pre, rows, per, static_cast<unsigned>(u0), static_cast<unsigned>(u0 + per < total ? u0 + per : total), 0};
   ArItem g;
   const int box = p.page_size < TILE ? p.page_size : TILE;   // tokens of one copied box
   const int box_log2 = 31 - __clz(box), boxes = TILE >> box_log2, boxes_log2 = 31 - __clz(boxes);
@@ -724,36 +736,58 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
       const float mx = row_max(r);
       __stcg(reinterpret_cast<float2*>(mine + ROWS * D + 2 * r), make_float2(mx, row_sum(r, mx)));
     }
-    fence_acq_rel_gpu();
-    ar_consumer_sync<CONSUMERS>();
+    ar_consumer_sync<CONSUMERS>();   // every warp's share is written: thread 0's release below covers it
     if (threadIdx.x == 0) {
-      const unsigned n_parts = last_cta - first_cta + 1;
-      const unsigned before = atomicAdd(p.arrived + first_cta, 1u);
-      *last_flag = before + 1 == n_parts;
-      if (before + 1 == n_parts) p.arrived[first_cta] = 0;    // ready for the next call
-      fence_acq_rel_gpu();
+      unsigned before;
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.arrived + first_cta) : "memory");
+      const bool last = before == last_cta - first_cta;
+      if (last) p.arrived[first_cta] = 0;    // ready for the next call
+      *last_flag = last;
     }
     ar_consumer_sync<CONSUMERS>();
     if (*last_flag) {
-      fence_acq_rel_gpu();
+      // each row's maximum over the parts: a thread takes every STEP-th part of
+      // a row, then the row's threads meet in shared memory
+      constexpr int STEP = CONSUMERS / ROWS;
+      const int n_parts = static_cast<int>(last_cta - first_cta) + 1;
+      {
+        const int r = threadIdx.x % ROWS;
+        float mx = -INFINITY;
+        if (r < g.n_rows)
+#pragma unroll 4
+          for (int c = threadIdx.x / ROWS; c < n_parts; c += STEP)
+            mx = fmaxf(mx, __ldcg(part(first_cta + c) + ROWS * D + 2 * r));
+        merge[threadIdx.x] = mx;
+      }
+      ar_consumer_sync<CONSUMERS>();
       for (int x = threadIdx.x; x < g.n_rows * (D / 4); x += CONSUMERS) {
         const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-        float mx = -INFINITY;
-#pragma unroll 8
-        for (unsigned c = first_cta; c <= last_cta; ++c) mx = fmaxf(mx, __ldcg(part(c) + ROWS * D + 2 * r));
+        float mx = merge[r];
+#pragma unroll
+        for (int c = 1; c < STEP; ++c) mx = fmaxf(mx, merge[c * ROWS + r]);
         const float use = mx == -INFINITY ? 0.0f : mx;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float sum = 0.0f;
-#pragma unroll 8
-        for (unsigned c = first_cta; c <= last_cta; ++c) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(c) + ROWS * D + 2 * r));
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(part(c) + r * D + d));
-          const float w = exp2_approx(ml.x - use);
-          sum += ml.y * w;
-          acc.x += y.x * w;
-          acc.y += y.y * w;
-          acc.z += y.z * w;
-          acc.w += y.w * w;
+        // sixteen parts' loads in flight
+        for (int c0 = 0; c0 < n_parts; c0 += 16) {
+          float2 ml[16];
+          float4 y[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float* src = part(first_cta + min(c0 + c, n_parts - 1));
+            ml[c] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * D + 2 * r));
+            y[c] = __ldcg(reinterpret_cast<const float4*>(src + r * D + d));
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            if (c0 + c >= n_parts) continue;
+            const float w = exp2_approx(ml[c].x - use);
+            sum += ml[c].y * w;
+            acc.x += y[c].x * w;
+            acc.y += y[c].y * w;
+            acc.z += y[c].z * w;
+            acc.w += y[c].w * w;
+          }
         }
         store(r, d, acc, sum);
       }

@@ -49,8 +49,9 @@ namespace {
 
 constexpr int AT_ROWS = 128;                 // rows of a row tile
 constexpr int AT_TILE = 128;                 // positions of a key tile
-constexpr int AT_K = 3, AT_V = 2;            // rings of K and V tiles
-constexpr int AT_SLOTS = AT_K + AT_V;        // ring slots: K's, then V's
+constexpr int AT_SLOTS = 5;                  // ring slots of K and V tiles, at most
+constexpr int AT_CHUNK = 32;                 // rows of a chunk of 8-bit codes
+constexpr int AT_CHUNKS = 4;                 // chunks of K, and of V, in flight: a tile's
 constexpr int AT_ITEMS = 2;                  // items announced ahead
 constexpr int AT_OKS = 8;                    // announced page masks of tiles
 constexpr int AT_SOFTMAX_WARPS = 8;
@@ -61,8 +62,9 @@ constexpr int AT_THREADS = 12 * 32;          // warp 11 only gives its registers
 constexpr int AT_REGS_SOFTMAX = 208, AT_REGS_OTHER = 80;
 static_assert(256 * AT_REGS_SOFTMAX + 128 * AT_REGS_OTHER <= AT_THREADS * 168, "register split");
 constexpr float AT_SLACK = 8.0f;             // powers of two that p may exceed 1 by
-// slot full / empty / clean, item full / empty, q full / empty, s full, p full, o full, join (each for A and B), drain
-constexpr int AT_BARS = 3 * AT_SLOTS + 2 * AT_ITEMS + 2 + 8 + 1;
+// slot full / empty / clean, item full / empty, q full / empty, s full, p full,
+// o full, join, q ready (each for A and B), chunk full / empty (K's, V's), drain
+constexpr int AT_BARS = 3 * AT_SLOTS + 2 * AT_ITEMS + 2 + 10 + 4 * AT_CHUNKS + 1;
 
 struct AtItem {
   int done;
@@ -83,19 +85,24 @@ struct AtParams {
   int window, sinks;
   float scale;           // softmax scale * log2 e, > 0
   int parts;             // parts of an item (1: no split)
+  const float* k_scale;  // E4M3 only
+  const float* v_scale;
   unsigned* arrived;     // [items][2], zero between calls (split only)
   float* part;           // [items][parts][2][128][D + 2]
   int* status;
 };
 
-template <int D>
+template <bool E4M3, int D>
 struct AtShape {
   static constexpr int HALVES = D / 64;
   static constexpr int MAT_BYTES = AT_TILE * D * 2;       // Q row tile, K tile or V tile
-  static constexpr int SMEM = (2 + AT_SLOTS) * MAT_BYTES + AT_ITEMS * static_cast<int>(sizeof(AtItem)) + AT_OKS * 4 +
-                              AT_BARS * 8 + 64 + 1024;
+  static constexpr int K_SLOTS = E4M3 ? 2 : 3, V_SLOTS = 2;   // rings: K's slots, then V's
+  static constexpr int CHUNK_BYTES = E4M3 ? AT_CHUNK * D : 0;
+  static constexpr int DATA = (2 + K_SLOTS + V_SLOTS) * MAT_BYTES + 2 * AT_CHUNKS * CHUNK_BYTES;
+  static constexpr int SMEM = DATA + AT_ITEMS * static_cast<int>(sizeof(AtItem)) + AT_OKS * 4 + AT_BARS * 8 + 64 + 1024;
   static constexpr int O_COL0 = 256;                       // tensor memory: S_A, S_B, O_A, O_B
 };
+static_assert(AtShape<false, 128>::SMEM <= 227 * 1024 && AtShape<true, 128>::SMEM <= 227 * 1024, "shared memory");
 
 // 1 in one lane of the (converged) warp, 0 in the others.
 NVFP4_DEV uint32_t elect_one() {
@@ -155,6 +162,10 @@ NVFP4_DEV float max3(float a, float b, float c) {
   return d;
 }
 
+NVFP4_DEV void sts128(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
 // A word with its lowest n bits set (none for n <= 0).
 NVFP4_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
@@ -164,15 +175,15 @@ NVFP4_DEV bool at_unclean(int j0, int p0, int p1, int window, int sinks) {
   return window > 0 && p0 - window >= max(j0, sinks) && sinks < j0 + AT_TILE;
 }
 
-template <int D>
+template <bool E4M3, int D>
 __global__ void __launch_bounds__(AT_THREADS, 1)
     attention_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                            const __grid_constant__ CUtensorMap map_v, const AtParams p) {
-  using S = AtShape<D>;
+  using S = AtShape<E4M3, D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* at = smem_raw + (base - raw) + (2 + AT_SLOTS) * S::MAT_BYTES;
+  uint8_t* at = smem_raw + (base - raw) + S::DATA;
   uint64_t* bars = reinterpret_cast<uint64_t*>(at);
   AtItem* items = reinterpret_cast<AtItem*>(bars + AT_BARS);
   unsigned* oks = reinterpret_cast<unsigned*>(items + AT_ITEMS);
@@ -191,9 +202,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   auto p_full = [&](int x) { return bar0 + 8u * (B1 + 4 + x); };
   auto o_full = [&](int x) { return bar0 + 8u * (B1 + 6 + x); };
   auto join_bar = [&](int x) { return bar0 + 8u * (B1 + 8 + x); };
-  const uint32_t drain_bar = bar0 + 8u * (B1 + 10);
+  auto q_ready = [&](int x) { return bar0 + 8u * (B1 + 10 + x); };
+  auto chunk_full = [&](int kv, int s) { return bar0 + 8u * (B1 + 12 + 2 * AT_CHUNKS * kv + s); };
+  auto chunk_empty = [&](int kv, int s) { return bar0 + 8u * (B1 + 12 + 2 * AT_CHUNKS * kv + AT_CHUNKS + s); };
+  const uint32_t drain_bar = bar0 + 8u * (B1 + 12 + 4 * AT_CHUNKS);
   auto q_tile = [&](int x) { return base + x * S::MAT_BYTES; };
   auto slot = [&](int s) { return base + (2 + s) * S::MAT_BYTES; };
+  auto chunk = [&](int kv, int s) { return base + (2 + S::K_SLOTS + S::V_SLOTS) * S::MAT_BYTES + (kv * AT_CHUNKS + s) * S::CHUNK_BYTES; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -204,7 +219,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     }
     for (int s = 0; s < AT_ITEMS; ++s) {
       mbar_init(item_full(s), 1);
-      mbar_init(item_empty(s), AT_SOFTMAX_WARPS + 2);
+      mbar_init(item_empty(s), AT_SOFTMAX_WARPS + (E4M3 ? 3 : 2));
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -213,6 +228,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       mbar_init(p_full(x), AT_SOFTMAX_WARPS / 2);
       mbar_init(o_full(x), 1);
       mbar_init(join_bar(x), AT_SOFTMAX_WARPS / 2);
+      mbar_init(q_ready(x), AT_SOFTMAX_WARPS / 2);
+      for (int s = 0; s < AT_CHUNKS; ++s) {
+        mbar_init(chunk_full(x, s), 1);
+        mbar_init(chunk_empty(x, s), 1);
+      }
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -234,7 +254,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const int tile_tok = AT_ROWS / p.group;      // tokens of a row tile
   const int item_tok = 2 * tile_tok;
-  const int box = p.page_size < AT_TILE ? p.page_size : AT_TILE;
+  constexpr int BOX = E4M3 ? AT_CHUNK : AT_TILE;   // most rows of a copied box
+  const int box = p.page_size < BOX ? p.page_size : BOX;
   const int boxes = AT_TILE / box;
 
   // waits of a whole warp
@@ -251,10 +272,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     return g.done == 0;
   };
   // the ring slot of the n-th K (or V) tile and the parity of that use
-  auto k_slot = [&](int n) { return n % AT_K; };
-  auto v_slot = [&](int n) { return AT_K + n % AT_V; };
-  auto k_par = [&](int n) { return (n / AT_K) & 1; };
-  auto v_par = [&](int n) { return (n / AT_V) & 1; };
+  auto k_slot = [&](int n) { return n % S::K_SLOTS; };
+  auto v_slot = [&](int n) { return S::K_SLOTS + n % S::V_SLOTS; };
+  auto k_par = [&](int n) { return (n / S::K_SLOTS) & 1; };
+  auto v_par = [&](int n) { return (n / S::V_SLOTS) & 1; };
   auto tile_pos = [&](const AtItem& g, int i) { return (i < g.st ? i : g.w0 + (i - g.st)) * AT_TILE; };
 
   if (warp < AT_SOFTMAX_WARPS) {
@@ -266,8 +287,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_cols = lane_base + AT_TILE * x, o_cols = lane_base + S::O_COL0 + D * x;
     const unsigned all_boxes = (1u << boxes) - 1u;
-    const float c = p.scale;
-    int tiles = 0, used = 0, outs = 0, joins = 0;   // tiles of the CTA, of this row tile, finished items, meetings
+    float c = p.scale;                                             // of this row, with E4M3 its powers of two
+    int tiles = 0, used = 0, outs = 0, joins = 0, q_seen = 0;   // tiles of the CTA, of this row tile, finished items, meetings
     auto meet = [&]() {   // of the row tile's four warps
       __syncwarp();
       if (lane == 0) mbar_arrive(join_bar(x));
@@ -279,6 +300,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       const bool active = x == 0 || g.n_tok > tile_tok;
       if (!active) {
         tiles += max(nt, 0);
+        if constexpr (E4M3) {
+          // in step with the other row tile, whether it has rows or not
+          if (nt > 0) {
+            if (!wait(q_full, q_seen++ & 1)) break;
+            if (lane == 0) mbar_arrive(q_ready(x));
+          }
+        }
         continue;
       }
       const int tok = x * tile_tok + my_tok;                       // token of the item
@@ -286,6 +314,46 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       const int pos = g.p0 + min(tok, g.n_tok - 1);
       float m = -INFINITY, l[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // l in four chains
       bool ok = true;
+      if constexpr (E4M3) {
+        if (nt > 0) {
+          // this thread's row of Q to f16 in place, scaled by a power of two that
+          // brings its largest element into [2^14, 2^15): exact for elements above
+          // 2^-29 of it. c takes the power back.
+          ok = wait(q_full, q_seen++ & 1);
+          if (!ok) break;
+          auto at_chunk = [&](int e) {   // 16-byte chunk e of the row, 128B swizzle
+            return q_tile(x) + (e >> 3) * (AT_ROWS * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
+          };
+          uint32_t top = 0;              // largest magnitude, bf16 bits of either half
+#pragma unroll
+          for (int e = 0; e < D / 8; ++e) {
+            const uint4 w = lds128(at_chunk(e));
+            top = __vmaxu2(top, w.x & 0x7FFF7FFFu);
+            top = __vmaxu2(top, w.y & 0x7FFF7FFFu);
+            top = __vmaxu2(top, w.z & 0x7FFF7FFFu);
+            top = __vmaxu2(top, w.w & 0x7FFF7FFFu);
+          }
+          const float amax = bf16_bits_to_f32(max(top & 0xFFFFu, top >> 16));
+          const int e2 = amax > 0.0f && amax < INFINITY ? ilogbf(amax) - 14 : 0;
+          // in two factors: 2^-e2 alone may lie outside fp32
+          const int e1 = min(max(-e2, -100), 100);
+          const float down = scalbnf(1.0f, e1), rest = scalbnf(1.0f, -e2 - e1);
+#pragma unroll
+          for (int e = 0; e < D / 8; ++e) {
+            const uint4 w = lds128(at_chunk(e));
+            const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+            uint32_t h[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              h[z] = f32x2_to_f16x2(bf16_bits_to_f32(y[z] & 0xFFFFu) * down * rest, bf16_bits_to_f32(y[z] >> 16) * down * rest);
+            sts128(at_chunk(e), h);
+          }
+          c = fmaxf(p.scale * p.k_scale[g.h] * scalbnf(1.0f, e2), 1e-44f);   // not zero: a masked score times it is -inf
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_ready(x));
+        }
+      }
       for (int i = g.i0; i < g.i1; ++i, ++tiles, ++used) {
         ok = wait(s_full(x), used & 1);
         if (!ok) break;
@@ -354,7 +422,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             a = exp2_approx(a);
             b = exp2_approx(b);
             add2(l[2 * (e & 1)], l[2 * (e & 1) + 1], a, b);
-            w[e] = f32x2_to_bf16x2(a, b);
+            w[e] = E4M3 ? f32x2_to_f16x2(a, b) : f32x2_to_bf16x2(a, b);
           }
           tc_st_16cols(s_cols + 16 * q, w);
         }
@@ -365,6 +433,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       }
       if (!ok) break;
       const float sum_l = (l[0] + l[1]) + (l[2] + l[3]);
+      const float v_mult = E4M3 ? p.v_scale[g.h] : 1.0f;
       if (nt > 0) {
         ok = wait(o_full(x), outs & 1);
         if (!ok) break;
@@ -373,7 +442,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       }
       uint16_t* dst = p.out + (static_cast<int64_t>(g.row0 + tok) * p.heads * p.group + static_cast<int64_t>(g.h) * p.group + my_head) * D;
       if (p.parts == 1) {
-        const float inv = sum_l > 0.0f ? 1.0f / sum_l : (sum_l == 0.0f ? 0.0f : sum_l);   // a NaN stays one
+        const float inv = sum_l > 0.0f ? v_mult / sum_l : (sum_l == 0.0f ? 0.0f : sum_l);   // a NaN stays one
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
@@ -443,7 +512,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + AT_ROWS * D + 2 * r));
           sum += ml.y * exp2_approx(ml.x - use);
         }
-        const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+        const float inv = sum > 0.0f ? v_mult / sum : (sum == 0.0f ? 0.0f : sum);
 #pragma unroll 1
         for (int q = 0; q < D / 16; ++q) {
           float acc[16];
@@ -554,36 +623,54 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           const int64_t block = page >= 0 ? static_cast<int64_t>(page) * p.heads + g.h : p.pages * p.heads;
           const int y = (tile_pos(g, i) + (lane & (boxes - 1)) * box) & (p.page_size - 1);
           if (i + 1 < g.i1) page = page_of(i + 1);
-          for (int kv = 0; kv < 2; ++kv) {
-            const int s = kv ? v_slot(tiles) : k_slot(tiles);
-            if (tiles >= (kv ? AT_V : AT_K) &&
-                !(ok = wait(kv_empty(s), kv ? v_par(tiles - AT_V) : k_par(tiles - AT_K))))
-              break;
-            if (lane == 0) {
-              if (kv == 0) oks[tiles % AT_OKS] = there;
-              mbar_arrive_expect_tx(kv_full(s), S::MAT_BYTES);
+          if constexpr (E4M3) {
+            // codes in chunks of 32 rows, K and V in turn; the converters read them
+            if (lane == 0) oks[tiles % AT_OKS] = there;
+            for (int u = 0; u < 2 * AT_CHUNKS; ++u) {
+              const int kv = u & 1, cu = u >> 1;
+              if (tiles > 0 && !(ok = wait(chunk_empty(kv, cu), (tiles - 1) & 1))) break;
+              if (lane == 0) mbar_arrive_expect_tx(chunk_full(kv, cu), S::CHUNK_BYTES);
+              __syncwarp();
+              // this chunk's boxes are those of lanes cu * per .. + per - 1
+              const int per = boxes / AT_CHUNKS;
+              if (lane < boxes && lane / per == cu)
+                tma_load_4d(chunk(kv, cu) + (lane - cu * per) * box * D, kv ? &map_v : &map_k, 0, y, 0, static_cast<int>(block),
+                            chunk_full(kv, cu));
+              asked[kv] = tiles * AT_CHUNKS + cu + 1;
             }
-            __syncwarp();
-            if (lane < boxes)
-              for (int hf = 0; hf < S::HALVES; ++hf)
-                tma_load_4d(slot(s) + hf * (AT_TILE * 128) + lane * box * 128, kv ? &map_v : &map_k, 0, y, hf,
-                            static_cast<int>(block), kv_full(s));
-            ++asked[kv];
+          } else {
+            for (int kv = 0; kv < 2; ++kv) {
+              const int s = kv ? v_slot(tiles) : k_slot(tiles);
+              if (tiles >= (kv ? S::V_SLOTS : S::K_SLOTS) &&
+                  !(ok = wait(kv_empty(s), kv ? v_par(tiles - S::V_SLOTS) : k_par(tiles - S::K_SLOTS))))
+                break;
+              if (lane == 0) {
+                if (kv == 0) oks[tiles % AT_OKS] = there;
+                mbar_arrive_expect_tx(kv_full(s), S::MAT_BYTES);
+              }
+              __syncwarp();
+              if (lane < boxes)
+                for (int hf = 0; hf < S::HALVES; ++hf)
+                  tma_load_4d(slot(s) + hf * (AT_TILE * 128) + lane * box * 128, kv ? &map_v : &map_k, 0, y, hf,
+                              static_cast<int>(block), kv_full(s));
+              ++asked[kv];
+            }
           }
           if (!ok) break;
         }
       }
       if (!ok) {
         // the copies in flight land before this CTA's shared memory goes
-        for (int n = max(asked[0] - AT_K, 0); n < asked[0]; ++n)
-          mbar_wait_bounded(kv_full(k_slot(n)), k_par(n), nullptr, p.status);
-        for (int n = max(asked[1] - AT_V, 0); n < asked[1]; ++n)
-          mbar_wait_bounded(kv_full(v_slot(n)), v_par(n), nullptr, p.status);
+        for (int kv = 0; kv < 2; ++kv)
+          for (int n = max(asked[kv] - (E4M3 ? AT_CHUNKS : kv ? S::V_SLOTS : S::K_SLOTS), 0); n < asked[kv]; ++n) {
+            const uint32_t bar = E4M3 ? chunk_full(kv, n % AT_CHUNKS) : kv_full(kv ? v_slot(n) : k_slot(n));
+            mbar_wait_bounded(bar, E4M3 ? (n / AT_CHUNKS) & 1 : kv ? v_par(n) : k_par(n), nullptr, p.status);
+          }
         if (q_used > 0) mbar_wait_bounded(q_full, (q_used - 1) & 1, nullptr, p.status);
       }
     } else if (warp == AT_MMA_WARP) {
       // -------------------------------------------------------------- MMA issue
-      // kind::f16, bf16 A and B, fp32 D, M = 128; S = Q K^T: both K-major, N =
+      // kind::f16, bf16 (E4M3 caches: f16) A and B, fp32 D, M = 128; S = Q K^T: both K-major, N =
       // 128; O = P V: V's d's are contiguous, so B is N-major (bit 16), N = D.
       // The whole warp walks the loops and one lane's MMAs take effect, by a
       // predicate and not a branch, with loop bounds from warp reductions: so
@@ -592,10 +679,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       // cores (2k rows on 8k positions: 231 -> 188 us). One warp for each row
       // tile was slower (267 us): their MMAs interleave, so both tiles' scores
       // come late together instead of in turns.
-      constexpr uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((AT_TILE >> 3) << 17) | ((AT_ROWS >> 4) << 24);
-      constexpr uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((D >> 3) << 17) | ((AT_ROWS >> 4) << 24);
+      constexpr uint32_t ab = E4M3 ? 0u : (1u << 7) | (1u << 10);   // f16 or bf16 A and B
+      constexpr uint32_t idesc_s = (1u << 4) | ab | ((AT_TILE >> 3) << 17) | ((AT_ROWS >> 4) << 24);
+      constexpr uint32_t idesc_o = (1u << 4) | ab | (1u << 16) | ((D >> 3) << 17) | ((AT_ROWS >> 4) << 24);
       const uint64_t desc_q = smem_desc(q_tile(0), 16, 1024, 2), desc_k = smem_desc(slot(0), 16, 1024, 2);
-      const uint64_t desc_v = smem_desc(slot(AT_K), AT_TILE * 128, 1024, 2);
+      const uint64_t desc_v = smem_desc(slot(S::K_SLOTS), AT_TILE * 128, 1024, 2);
       const uint32_t lead = elect_one();
       int tiles = 0, q_used = 0;   // tiles done, items with tiles
       int p_used[2] = {0, 0};
@@ -620,7 +708,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           }
           __syncwarp();
         };
-        if (!(ok = wait(q_full, q_used & 1) && wait(kv_full(k_slot(tiles)), k_par(tiles)))) break;
+        if constexpr (E4M3) {
+          // the softmax warps convert each row tile's Q
+          ok = wait(q_ready(0), q_used & 1) && wait(q_ready(1), q_used & 1);
+        } else {
+          ok = wait(q_full, q_used & 1);
+        }
+        if (!ok || !(ok = wait(kv_full(k_slot(tiles)), k_par(tiles)))) break;
         ++q_used;
         tc_fence_after();
         for (int x = 0; x < n_x; ++x) issue_s(x, tiles);
@@ -637,7 +731,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             ++p_used[x];
             tc_fence_after();
             const uint32_t d = tmem + S::O_COL0 + D * x, a = tmem + AT_TILE * x;
-            const uint64_t v0 = desc_v + static_cast<uint64_t>(sv - AT_K) * (S::MAT_BYTES >> 4);
+            const uint64_t v0 = desc_v + static_cast<uint64_t>(sv - S::K_SLOTS) * (S::MAT_BYTES >> 4);
             tc_mma_bf16_ts(d, a, v0, idesc_o, i > 0, lead);
 #pragma unroll
             for (int ks = 1; ks < AT_TILE / 16; ++ks)   // 16 positions of V, 8 columns of P
@@ -659,6 +753,55 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       if (lead) tc_commit(drain_bar);
       mbar_wait_bounded(drain_bar, 0, nullptr, p.status);
       __syncwarp();
+    } else if constexpr (E4M3) {
+      // ------------------ codes to f16 tiles: V (the clean warp's work too), K
+      const int kv = warp == AT_CLEAN_WARP ? 1 : 0;
+      constexpr int UNITS = D / 16;       // 16-byte pieces of a code row; pieces of a lane in a chunk
+      int tiles = 0;
+      bool ok = true;
+      AtItem g;
+      for (int k = 0; ok && get_item(k, g); ++k) {
+        const int p1 = g.p0 + g.n_tok - 1;
+        for (int i = g.i0; i < g.i1 && ok; ++i, ++tiles) {
+          const int j0 = tile_pos(g, i), s = kv ? v_slot(tiles) : k_slot(tiles);
+          if (tiles >= (kv ? S::V_SLOTS : S::K_SLOTS) &&
+              !(ok = wait(kv_empty(s), kv ? v_par(tiles - S::V_SLOTS) : k_par(tiles - S::K_SLOTS))))
+            break;
+          const bool unclean = kv && at_unclean(j0, g.p0, p1, p.window, p.sinks);
+          for (int cu = 0; cu < AT_CHUNKS; ++cu) {
+            if (!(ok = wait(chunk_full(kv, cu), tiles & 1))) break;
+            uint4 w[UNITS];
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) w[u] = lds128(chunk(kv, cu) + (u * 32 + lane) * 16);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(chunk_empty(kv, cu));
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+              const int row = cu * AT_CHUNK + (u * 32 + lane) / UNITS, piece = (u * 32 + lane) % UNITS;
+              const int j = j0 + row;
+              // value rows no row of the item sees become zeros: they may hold anything, and 0 * NaN is not 0
+              const bool keep = !unclean || (j <= p1 && !(p.window > 0 && j >= p.sinks && g.p0 - j >= p.window));
+              const uint32_t y[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                uint32_t h[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  const uint32_t v = y[2 * hf + (z >> 1)];
+                  h[z] = e4m3x2_to_f16x2((z & 1) ? v >> 16 : v & 0xFFFFu);
+                  if (!keep) h[z] = 0u;
+                }
+                const int c8 = 2 * piece + hf;   // 16-byte chunk of the f16 row
+                sts128(slot(s) + (c8 >> 3) * (AT_TILE * 128) + row * 128 + (((c8 & 7) ^ (row & 7)) << 4), h);
+              }
+            }
+          }
+          if (!ok) break;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv ? kv_clean(s) : kv_full(s));
+        }
+      }
     } else if (warp == AT_CLEAN_WARP) {
       // --------------------------------------- value rows that no row may take in
       // every V tile passes here, so this warp and the rings stay in step
