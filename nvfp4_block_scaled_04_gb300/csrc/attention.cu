@@ -69,9 +69,10 @@ int launch_rows_nt(int nt, const ArParams& p, const nvfp4_kv_cache_t& c, cudaStr
   }
 }
 
-// Blocks of rows (256 at most, whole tokens) and kv heads of a call of the tile kernel, at most.
+// Blocks of rows (256 at most, whole tokens) times kv heads of a call of the tile kernel, at most.
 int64_t tiles_items(int64_t tokens, int64_t batch, int64_t heads, int group) {
-  return heads * (tokens / (2 * (AT_ROWS / group)) + batch);
+  const int64_t block = 2 * (AT_ROWS / group);
+  return heads * ((tokens + batch * (block - 1)) / block);
 }
 
 template <bool E4M3, int D>
@@ -94,7 +95,7 @@ int launch_tiles(const uint16_t* Q, int64_t q_stride, int q_heads, const nvfp4_k
   const int64_t units = items * p.parts;
   const int rc = ensure_smem(attention_tiles_kernel<E4M3, D>, AtShape<E4M3, D>::SMEM);
   if (rc) return rc;
-  return launch_ex(attention_tiles_kernel<E4M3, D>, dim3(static_cast<unsigned>(units < ctas ? units : ctas)), dim3(AT_THREADS),
+  return launch_ex(attention_tiles_kernel<E4M3, D>, dim3(static_cast<unsigned>(units < ctas ? units : ctas)), dim3(AtShape<E4M3, D>::THREADS),
                    AtShape<E4M3, D>::SMEM, 1, true, stream, mq, mk, mv, p);
 }
 

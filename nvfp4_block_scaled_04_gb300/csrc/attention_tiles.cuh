@@ -23,6 +23,10 @@
 //   warp 9            tensor-memory allocation; issues the MMAs
 //   warp 10           zeroes value rows no row of the item sees (they may hold
 //                     anything, and 0 * NaN is not 0)
+//   warps 10, 12..15  with E4M3 caches: a producer of its own for V, and codes,
+//                     which the producers copy in chunks of 32 rows, to f16 tiles (two
+//                     warps for K, two for V); the MMAs are f16 then, and the
+//                     softmax warps bring each item's Q to f16
 // S and P of a tile share 128 columns: S(j + 1) is issued after O += P(j) V(j),
 // and the tensor cores run one thread's MMAs in order. For the same reason a
 // finished S(j + 1) says that O += P(j) V(j) is finished, so the softmax warps
@@ -49,18 +53,15 @@ namespace {
 
 constexpr int AT_ROWS = 128;                 // rows of a row tile
 constexpr int AT_TILE = 128;                 // positions of a key tile
-constexpr int AT_SLOTS = 5;                  // ring slots of K and V tiles, at most
+constexpr int AT_SLOTS = 4;                  // ring slots of K and V tiles
 constexpr int AT_CHUNK = 32;                 // rows of a chunk of 8-bit codes
 constexpr int AT_CHUNKS = 4;                 // chunks of K, and of V, in flight: a tile's
 constexpr int AT_ITEMS = 2;                  // items announced ahead
 constexpr int AT_OKS = 8;                    // announced page masks of tiles
 constexpr int AT_SOFTMAX_WARPS = 8;
 constexpr int AT_PROD_WARP = 8, AT_MMA_WARP = 9, AT_CLEAN_WARP = 10;
-constexpr int AT_THREADS = 12 * 32;          // warp 11 only gives its registers away
-// registers a thread: the launch's 168 for 384 threads (64512 in all), moved
-// from the third warpgroup to the softmax ones (256 x 208 + 128 x 80 = 63488)
-constexpr int AT_REGS_SOFTMAX = 208, AT_REGS_OTHER = 80;
-static_assert(256 * AT_REGS_SOFTMAX + 128 * AT_REGS_OTHER <= AT_THREADS * 168, "register split");
+constexpr int AT_V_PROD_WARP = 10;           // (E4M3 caches)
+constexpr int AT_CONVERT_WARP = 12;          // 12, 13: K's codes, 14, 15: V's (E4M3 caches)
 constexpr float AT_SLACK = 8.0f;             // powers of two that p may exceed 1 by
 // slot full / empty / clean, item full / empty, q full / empty, s full, p full,
 // o full, join, q ready (each for A and B), chunk full / empty (K's, V's), drain
@@ -88,7 +89,7 @@ struct AtParams {
   const float* k_scale;  // E4M3 only
   const float* v_scale;
   unsigned* arrived;     // [items][2], zero between calls (split only)
-  float* part;           // [items][parts][2][128][D + 2]
+  float* part;           // [items][parts][2] of o [D / 4][128] float4 (a warp's rows next to each other), (m, l) [128]
   int* status;
 };
 
@@ -96,11 +97,20 @@ template <bool E4M3, int D>
 struct AtShape {
   static constexpr int HALVES = D / 64;
   static constexpr int MAT_BYTES = AT_TILE * D * 2;       // Q row tile, K tile or V tile
-  static constexpr int K_SLOTS = E4M3 ? 2 : 3, V_SLOTS = 2;   // rings: K's slots, then V's
+  static constexpr int K_SLOTS = 2, V_SLOTS = 2;          // rings: K's slots, then V's
   static constexpr int CHUNK_BYTES = E4M3 ? AT_CHUNK * D : 0;
-  static constexpr int DATA = (2 + K_SLOTS + V_SLOTS) * MAT_BYTES + 2 * AT_CHUNKS * CHUNK_BYTES;
+  // beside the tiles: E4M3 chunks of K and V, or each softmax warp's staging of
+  // 32 output rows x 64 d's
+  static constexpr int STAGING = E4M3 ? 0 : AT_SOFTMAX_WARPS * 32 * 128;
+  static constexpr int DATA = (2 + K_SLOTS + V_SLOTS) * MAT_BYTES + 2 * AT_CHUNKS * CHUNK_BYTES + STAGING;
   static constexpr int SMEM = DATA + AT_ITEMS * static_cast<int>(sizeof(AtItem)) + AT_OKS * 4 + AT_BARS * 8 + 64 + 1024;
   static constexpr int O_COL0 = 256;                       // tensor memory: S_A, S_B, O_A, O_B
+  // Registers a thread, moved from the other warpgroups to the two softmax
+  // ones: 384 x 168 = 64512 at launch, 256 x 208 + 128 x 80 = 63488 after; with
+  // converters 512 x 128 = 65536, 256 x 192 + 256 x 64 = 65536.
+  static constexpr int THREADS = E4M3 ? 16 * 32 : 12 * 32;
+  static constexpr int REGS_SOFTMAX = E4M3 ? 192 : 208, REGS_OTHER = E4M3 ? 64 : 80;
+  static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * (E4M3 ? 128 : 168), "register split");
 };
 static_assert(AtShape<false, 128>::SMEM <= 227 * 1024 && AtShape<true, 128>::SMEM <= 227 * 1024, "shared memory");
 
@@ -176,7 +186,7 @@ NVFP4_DEV bool at_unclean(int j0, int p0, int p1, int window, int sinks) {
 }
 
 template <bool E4M3, int D>
-__global__ void __launch_bounds__(AT_THREADS, 1)
+__global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
     attention_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                            const __grid_constant__ CUtensorMap map_v, const AtParams p) {
   using S = AtShape<E4M3, D>;
@@ -213,13 +223,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < AT_SLOTS; ++s) {
-      mbar_init(kv_full(s), 1);
+      mbar_init(kv_full(s), E4M3 ? 2 : 1);
       mbar_init(kv_empty(s), 1);
-      mbar_init(kv_clean(s), 1);
+      mbar_init(kv_clean(s), E4M3 ? 2 : 1);
     }
     for (int s = 0; s < AT_ITEMS; ++s) {
       mbar_init(item_full(s), 1);
-      mbar_init(item_empty(s), AT_SOFTMAX_WARPS + (E4M3 ? 3 : 2));
+      mbar_init(item_empty(s), AT_SOFTMAX_WARPS + (E4M3 ? 5 : 2));
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -279,7 +289,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   auto tile_pos = [&](const AtItem& g, int i) { return (i < g.st ? i : g.w0 + (i - g.st)) * AT_TILE; };
 
   if (warp < AT_SOFTMAX_WARPS) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AT_REGS_SOFTMAX));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::REGS_SOFTMAX));
     // ----------------------------------------------------------------- softmax
     const int x = warp >> 2;                                       // row tile
     const int r = (warp & 3) * 32 + lane;                          // row: tensor-memory lane
@@ -443,25 +453,47 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       uint16_t* dst = p.out + (static_cast<int64_t>(g.row0 + tok) * p.heads * p.group + static_cast<int64_t>(g.h) * p.group + my_head) * D;
       if (p.parts == 1) {
         const float inv = sum_l > 0.0f ? v_mult / sum_l : (sum_l == 0.0f ? 0.0f : sum_l);   // a NaN stays one
+        // bf16 rows through shared memory, 64 d's at a time, so that a store
+        // writes four rows' 128 bytes: from one row per thread it would write 32
+        // rows' 16 (E4M3 caches leave no room for that)
+        const uint32_t my_off = live ? static_cast<uint32_t>((tok * p.heads * p.group + my_head) * D) : 0xFFFFFFFFu;
+        uint16_t* out0 = p.out + (static_cast<int64_t>(g.row0) * p.heads * p.group + static_cast<int64_t>(g.h) * p.group) * D;
+        const uint32_t stage = slot(S::K_SLOTS + S::V_SLOTS) + warp * (32 * 128);
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
+        for (int hf = 0; hf < D / 64; ++hf) {
+          uint32_t o[2][32];
           if (nt > 0) {
-            tc_ld_32cols(o_cols + 32 * q, o);
+            tc_ld_32cols(o_cols + 64 * hf, o[0]);
+            tc_ld_32cols(o_cols + 64 * hf + 32, o[1]);
             tc_wait_ld();
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
+            for (int e = 0; e < 32; ++e) o[0][e] = o[1][e] = 0u;
           }
-          if (live) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t y[4];
+          for (int e = 0; e < 8; ++e) {
+            uint32_t y[4];
 #pragma unroll
-              for (int z = 0; z < 4; ++z)
-                y[z] = f32x2_to_bf16x2(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + 32 * q + e) = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int z = 0; z < 4; ++z) {
+              const int q = 8 * (e & 3) + 2 * z;
+              y[z] = f32x2_to_bf16x2(__uint_as_float(o[e >> 2][q]) * inv, __uint_as_float(o[e >> 2][q + 1]) * inv);
             }
+            if constexpr (E4M3) {
+              if (live) *reinterpret_cast<uint4*>(out0 + my_off + 64 * hf + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
+            } else {
+              sts128(stage + lane * 128 + ((e ^ (lane & 7)) << 4), y);
+            }
+          }
+          if constexpr (!E4M3) {
+            __syncwarp();
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+              const int rr = 4 * it + (lane >> 3), e = lane & 7;
+              const uint32_t off = __shfl_sync(0xffffffffu, my_off, rr);
+              const uint4 y = lds128(stage + rr * 128 + ((e ^ (rr & 7)) << 4));
+              if (off != 0xFFFFFFFFu) *reinterpret_cast<uint4*>(out0 + off + 64 * hf + 8 * e) = y;
+            }
+            __syncwarp();
           }
         }
         tc_fence_before();
@@ -485,25 +517,23 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            __stcg(reinterpret_cast<float4*>(mine + r * D + 32 * q + e),
+            __stcg(reinterpret_cast<float4*>(mine) + (8 * q + e / 4) * AT_ROWS + r,
                    make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                                __uint_as_float(o[e + 3])));
         }
         __stcg(reinterpret_cast<float2*>(mine + AT_ROWS * D + 2 * r), make_float2(m * c, sum_l));
         tc_fence_before();
       }
-      fence_acq_rel_gpu();
-      if (!meet()) break;
+      if (!meet()) break;   // the four warps' shares are written: the release below covers them
       if ((threadIdx.x & 127) == 0) {
         unsigned* counter = p.arrived + g.item * 2 + x;
-        const unsigned before = atomicAdd(counter, 1u);
+        unsigned before;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
         last_flag[x] = before + 1 == static_cast<unsigned>(p.parts);
         if (before + 1 == static_cast<unsigned>(p.parts)) *counter = 0;   // ready for the next call
-        fence_acq_rel_gpu();
       }
       if (!meet()) break;
       if (last_flag[x] && live) {
-        fence_acq_rel_gpu();
         float mx = -INFINITY;
         for (int i = 0; i < p.parts; ++i) mx = fmaxf(mx, __ldcg(part(i) + AT_ROWS * D + 2 * r));
         const float use = mx == -INFINITY ? 0.0f : mx;
@@ -518,12 +548,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           float acc[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
           for (int i = 0; i < p.parts; ++i) {
             const float f = exp2_approx(__ldcg(part(i) + AT_ROWS * D + 2 * r) - use) * inv;
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(part(i) + r * D + 16 * q + e));
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(part(i)) + (4 * q + e / 4) * AT_ROWS + r);
               acc[e] += y.x * f;
               acc[e + 1] += y.y * f;
               acc[e + 2] += y.z * f;
@@ -540,9 +570,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       if (!meet()) break;   // the flag may be written again
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AT_REGS_OTHER));
-    if (warp == AT_PROD_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
+    if (warp == AT_PROD_WARP || (E4M3 && warp == AT_V_PROD_WARP)) {
       // ---------------------------------------------------------------- producer
+      // (with E4M3 a second one for V, so that K's codes need not wait for it)
+      const bool first = warp == AT_PROD_WARP;   // announces items, brings Q
       const int64_t table_end = static_cast<int64_t>(p.s.max_pages) * p.page_size;
       int tiles = 0, asked[2] = {0, 0}, q_used = 0;   // tiles done, K and V tiles requested, items whose Q was
       bool ok = true;
@@ -593,8 +625,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           run += __shfl_sync(0xffffffffu, x, 31);
         }
         const int slot_i = k % AT_ITEMS;
-        if (k >= AT_ITEMS && !(ok = wait(item_empty(slot_i), ((k / AT_ITEMS) - 1) & 1))) break;
-        if (lane == 0) {
+        if (first && k >= AT_ITEMS && !(ok = wait(item_empty(slot_i), ((k / AT_ITEMS) - 1) & 1))) break;
+        if (first && lane == 0) {
           items[slot_i] = g;
           mbar_arrive(item_full(slot_i));
         }
@@ -608,8 +640,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         };
         int page = page_of(g.i0);
         // both row tiles of Q, once the last item's MMAs have read theirs
-        if (q_used > 0 && !(ok = wait(q_empty, (q_used - 1) & 1))) break;
-        if (lane == 0) {
+        if (first && q_used > 0 && !(ok = wait(q_empty, (q_used - 1) & 1))) break;
+        if (first && lane == 0) {
           const int n_x = g.n_tok > tile_tok ? 2 : 1;
           mbar_arrive_expect_tx(q_full, n_x * S::HALVES * tile_tok * p.group * 128);
           for (int x = 0; x < n_x; ++x)
@@ -624,15 +656,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           const int y = (tile_pos(g, i) + (lane & (boxes - 1)) * box) & (p.page_size - 1);
           if (i + 1 < g.i1) page = page_of(i + 1);
           if constexpr (E4M3) {
-            // codes in chunks of 32 rows, K and V in turn; the converters read them
-            if (lane == 0) oks[tiles % AT_OKS] = there;
-            for (int u = 0; u < 2 * AT_CHUNKS; ++u) {
-              const int kv = u & 1, cu = u >> 1;
+            // codes in chunks of 32 rows; the converters read them
+            const int kv = first ? 0 : 1;
+            if (first && lane == 0) oks[tiles % AT_OKS] = there;
+            const int per = boxes / AT_CHUNKS;   // boxes of a chunk: those of lanes cu * per .. + per - 1
+            for (int cu = 0; cu < AT_CHUNKS; ++cu) {
               if (tiles > 0 && !(ok = wait(chunk_empty(kv, cu), (tiles - 1) & 1))) break;
               if (lane == 0) mbar_arrive_expect_tx(chunk_full(kv, cu), S::CHUNK_BYTES);
               __syncwarp();
-              // this chunk's boxes are those of lanes cu * per .. + per - 1
-              const int per = boxes / AT_CHUNKS;
               if (lane < boxes && lane / per == cu)
                 tma_load_4d(chunk(kv, cu) + (lane - cu * per) * box * D, kv ? &map_v : &map_k, 0, y, 0, static_cast<int>(block),
                             chunk_full(kv, cu));
@@ -666,7 +697,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             const uint32_t bar = E4M3 ? chunk_full(kv, n % AT_CHUNKS) : kv_full(kv ? v_slot(n) : k_slot(n));
             mbar_wait_bounded(bar, E4M3 ? (n / AT_CHUNKS) & 1 : kv ? v_par(n) : k_par(n), nullptr, p.status);
           }
-        if (q_used > 0) mbar_wait_bounded(q_full, (q_used - 1) & 1, nullptr, p.status);
+        if (first && q_used > 0) mbar_wait_bounded(q_full, (q_used - 1) & 1, nullptr, p.status);
       }
     } else if (warp == AT_MMA_WARP) {
       // -------------------------------------------------------------- MMA issue
@@ -754,52 +785,58 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       mbar_wait_bounded(drain_bar, 0, nullptr, p.status);
       __syncwarp();
     } else if constexpr (E4M3) {
-      // ------------------ codes to f16 tiles: V (the clean warp's work too), K
-      const int kv = warp == AT_CLEAN_WARP ? 1 : 0;
-      constexpr int UNITS = D / 16;       // 16-byte pieces of a code row; pieces of a lane in a chunk
-      int tiles = 0;
-      bool ok = true;
-      AtItem g;
-      for (int k = 0; ok && get_item(k, g); ++k) {
-        const int p1 = g.p0 + g.n_tok - 1;
-        for (int i = g.i0; i < g.i1 && ok; ++i, ++tiles) {
-          const int j0 = tile_pos(g, i), s = kv ? v_slot(tiles) : k_slot(tiles);
-          if (tiles >= (kv ? S::V_SLOTS : S::K_SLOTS) &&
-              !(ok = wait(kv_empty(s), kv ? v_par(tiles - S::V_SLOTS) : k_par(tiles - S::K_SLOTS))))
-            break;
-          const bool unclean = kv && at_unclean(j0, g.p0, p1, p.window, p.sinks);
-          for (int cu = 0; cu < AT_CHUNKS; ++cu) {
-            if (!(ok = wait(chunk_full(kv, cu), tiles & 1))) break;
-            uint4 w[UNITS];
+      if (warp >= AT_CONVERT_WARP) {
+        // ---------------- codes to f16 tiles: two warps for K, two for V, which
+        // also do the clean warp's work; each takes every second chunk
+        const int kv = (warp - AT_CONVERT_WARP) >> 1, sub = warp & 1;
+        constexpr int UNITS = D / 16;       // 16-byte pieces of a code row; pieces of a lane in a chunk
+        constexpr int BATCH = 4;            // pieces in registers at once
+        int tiles = 0;
+        bool ok = true;
+        AtItem g;
+        for (int k = 0; ok && get_item(k, g); ++k) {
+          const int p1 = g.p0 + g.n_tok - 1;
+          for (int i = g.i0; i < g.i1 && ok; ++i, ++tiles) {
+            const int j0 = tile_pos(g, i), s = kv ? v_slot(tiles) : k_slot(tiles);
+            if (tiles >= (kv ? S::V_SLOTS : S::K_SLOTS) &&
+                !(ok = wait(kv_empty(s), kv ? v_par(tiles - S::V_SLOTS) : k_par(tiles - S::K_SLOTS))))
+              break;
+            const bool unclean = kv && at_unclean(j0, g.p0, p1, p.window, p.sinks);
+            for (int cu = sub; cu < AT_CHUNKS; cu += 2) {
+              if (!(ok = wait(chunk_full(kv, cu), tiles & 1))) break;
 #pragma unroll
-            for (int u = 0; u < UNITS; ++u) w[u] = lds128(chunk(kv, cu) + (u * 32 + lane) * 16);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(chunk_empty(kv, cu));
+              for (int u0 = 0; u0 < UNITS; u0 += BATCH) {
+                uint4 w[BATCH];
 #pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
-              const int row = cu * AT_CHUNK + (u * 32 + lane) / UNITS, piece = (u * 32 + lane) % UNITS;
-              const int j = j0 + row;
-              // value rows no row of the item sees become zeros: they may hold anything, and 0 * NaN is not 0
-              const bool keep = !unclean || (j <= p1 && !(p.window > 0 && j >= p.sinks && g.p0 - j >= p.window));
-              const uint32_t y[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                uint32_t h[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  const uint32_t v = y[2 * hf + (z >> 1)];
-                  h[z] = e4m3x2_to_f16x2((z & 1) ? v >> 16 : v & 0xFFFFu);
-                  if (!keep) h[z] = 0u;
+                for (int u = 0; u < BATCH; ++u) w[u] = lds128(chunk(kv, cu) + ((u0 + u) * 32 + lane) * 16);
+                if (u0 + BATCH == UNITS) {
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(chunk_empty(kv, cu));
                 }
-                const int c8 = 2 * piece + hf;   // 16-byte chunk of the f16 row
-                sts128(slot(s) + (c8 >> 3) * (AT_TILE * 128) + row * 128 + (((c8 & 7) ^ (row & 7)) << 4), h);
+#pragma unroll
+                for (int u = 0; u < BATCH; ++u) {
+                  const int row = cu * AT_CHUNK + ((u0 + u) * 32 + lane) / UNITS, piece = lane % UNITS;
+                  if (unclean) {
+                    // value rows no row of the item sees become zeros: they may hold anything, and 0 * NaN is not 0
+                    const int j = j0 + row;
+                    if (j > p1 || (p.window > 0 && j >= p.sinks && g.p0 - j >= p.window)) w[u] = make_uint4(0u, 0u, 0u, 0u);
+                  }
+                  const uint32_t y[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf) {
+                    const uint32_t h[4] = {e4m3x2_to_f16x2(y[2 * hf] & 0xFFFFu), e4m3x2_to_f16x2(y[2 * hf] >> 16),
+                                           e4m3x2_to_f16x2(y[2 * hf + 1] & 0xFFFFu), e4m3x2_to_f16x2(y[2 * hf + 1] >> 16)};
+                    const int c8 = 2 * piece + hf;   // 16-byte chunk of the f16 row
+                    sts128(slot(s) + (c8 >> 3) * (AT_TILE * 128) + row * 128 + (((c8 & 7) ^ (row & 7)) << 4), h);
+                  }
+                }
               }
             }
+            if (!ok) break;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(kv ? kv_clean(s) : kv_full(s));
           }
-          if (!ok) break;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(kv ? kv_clean(s) : kv_full(s));
         }
       }
     } else if (warp == AT_CLEAN_WARP) {
