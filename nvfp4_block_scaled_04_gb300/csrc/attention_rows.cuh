@@ -49,6 +49,7 @@ namespace {
 
 constexpr int AR_MAX_STAGES = 8;
 constexpr int AR_ITEMS = 2;                  // items announced ahead
+constexpr float AR_SLACK = 8.0f;             // powers of two that p may exceed 1 by before sums are rescaled
 constexpr int AR_KEPT = 128;                 // sequences whose lengths are kept in shared memory
 constexpr int AR_PAD = 4;                    // fp32 words between rows of the merge buffer: no bank conflicts
 constexpr unsigned AR_ALL = 0xffffffffu;
@@ -509,6 +510,11 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[nt][c] = 0.0f;
+      float s2[NT][4];   // (two tiles leave room for a second chain of products)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s2[nt][c] = 0.0f;
       if constexpr (E4M3) {
 #pragma unroll
         for (int k2 = 0; k2 < KS / 2; ++k2) {
@@ -519,7 +525,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
             const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * hf] & 0xFFFFu), e4m3x2_to_f16x2(r[2 * hf + 1] & 0xFFFFu),
                                    e4m3x2_to_f16x2(r[2 * hf] >> 16), e4m3x2_to_f16x2(r[2 * hf + 1] >> 16)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a, q_at(2 * k2 + hf, nt).x, q_at(2 * k2 + hf, nt).y);
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(hf && NT == 2 ? s2[nt] : s[nt], a, q_at(2 * k2 + hf, nt).x, q_at(2 * k2 + hf, nt).y);
           }
         }
       } else {
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
           uint32_t a[4];
           ldsm_x4(kb + swz(k_row, 2 * ks + (lane >> 4)), a);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(s[nt], a, q_at(ks, nt).x, q_at(ks, nt).y);
+          for (int nt = 0; nt < NT; ++nt) mma_bf16_16816((ks & 1) && NT == 2 ? s2[nt] : s[nt], a, q_at(ks, nt).x, q_at(ks, nt).y);
         }
       }
       // scores in powers of two; masked ones replaced
@@ -539,7 +545,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[nt][c] *= mult[nt][c & 1];
+        for (int c = 0; c < 4; ++c) s[nt][c] = (s[nt][c] + s2[nt][c]) * mult[nt][c & 1];
       if (!all_seen) {
         auto none_sees = [&](int j) {
           return !box_ok || j > g.p1 || j >= g.key_end || (p.window > 0 && j >= p.sinks && g.p0 - j >= p.window);
@@ -572,11 +578,12 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
           mx = fmaxf(mx, __shfl_xor_sync(AR_ALL, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(AR_ALL, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(AR_ALL, mx, 16));
-          const float mn = fmaxf(m[nt][c], mx);
-          const float use = mn == -INFINITY ? 0.0f : mn;
-          alpha[nt][c] = exp2_approx(m[nt][c] - use);
-          moved = moved || mn != m[nt][c];
-          m[nt][c] = mn;
+          // m moves, and o with it, only where p would exceed 2^AR_SLACK
+          const bool grows = mx - m[nt][c] > AR_SLACK;
+          alpha[nt][c] = grows ? exp2_approx(m[nt][c] - mx) : 1.0f;
+          moved = moved || grows;
+          if (grows) m[nt][c] = mx;
+          const float use = m[nt][c] == -INFINITY ? 0.0f : m[nt][c];
           s[nt][c] = exp2_approx(s[nt][c] - use);
           s[nt][c + 2] = exp2_approx(s[nt][c + 2] - use);
           l[nt][c] = l[nt][c] * alpha[nt][c] + (s[nt][c] + s[nt][c + 2]);

@@ -74,7 +74,7 @@ struct AtItem {
   int p0;                // first position
   int key_end;           // positions at or past it hold nothing
   int st, w0, i0, i1;    // tiles (KvTiles) and the part of them that is this item's
-  int item, part;        // index of the unsplit item, part of it
+  int item, part, parts; // index of the unsplit item, part of it, its parts
 };
 
 struct AtParams {
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
         tc_fence_after();
       }
       uint16_t* dst = p.out + (static_cast<int64_t>(g.row0 + tok) * p.heads * p.group + static_cast<int64_t>(g.h) * p.group + my_head) * D;
-      if (p.parts == 1) {
+      if (g.parts == 1) {
         const float inv = sum_l > 0.0f ? v_mult / sum_l : (sum_l == 0.0f ? 0.0f : sum_l);   // a NaN stays one
         // bf16 rows through shared memory, 64 d's at a time, so that a store
         // writes four rows' 128 bytes: from one row per thread it would write 32
@@ -529,16 +529,16 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
         unsigned* counter = p.arrived + g.item * 2 + x;
         unsigned before;
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
-        last_flag[x] = before + 1 == static_cast<unsigned>(p.parts);
-        if (before + 1 == static_cast<unsigned>(p.parts)) *counter = 0;   // ready for the next call
+        last_flag[x] = before + 1 == static_cast<unsigned>(g.parts);
+        if (before + 1 == static_cast<unsigned>(g.parts)) *counter = 0;   // ready for the next call
       }
       if (!meet()) break;
       if (last_flag[x] && live) {
         float mx = -INFINITY;
-        for (int i = 0; i < p.parts; ++i) mx = fmaxf(mx, __ldcg(part(i) + AT_ROWS * D + 2 * r));
+        for (int i = 0; i < g.parts; ++i) mx = fmaxf(mx, __ldcg(part(i) + AT_ROWS * D + 2 * r));
         const float use = mx == -INFINITY ? 0.0f : mx;
         float sum = 0.0f;
-        for (int i = 0; i < p.parts; ++i) {
+        for (int i = 0; i < g.parts; ++i) {
           const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + AT_ROWS * D + 2 * r));
           sum += ml.y * exp2_approx(ml.x - use);
         }
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
 #pragma unroll 4
-          for (int i = 0; i < p.parts; ++i) {
+          for (int i = 0; i < g.parts; ++i) {
             const float f = exp2_approx(__ldcg(part(i) + AT_ROWS * D + 2 * r) - use) * inv;
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
@@ -578,11 +578,12 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
       const int64_t table_end = static_cast<int64_t>(p.s.max_pages) * p.page_size;
       int tiles = 0, asked[2] = {0, 0}, q_used = 0;   // tiles done, K and V tiles requested, items whose Q was
       bool ok = true;
-      for (int k = 0; ok; ++k) {
+      int k = -1, b_from = 0;                  // items announced
+      int64_t run_from = 0;
+      for (int64_t w = blockIdx.x; ok; w += gridDim.x) {
         // work item w: (sequence, block of its rows, kv head, part), the parts of
         // a block next to each other, then its heads; late blocks, which see
         // more, come first
-        const int64_t w = blockIdx.x + static_cast<int64_t>(k) * gridDim.x;
         const int64_t flat = w / (p.parts * p.heads);
         const int rest = static_cast<int>(w - flat * (p.parts * p.heads));
         AtItem g = {};
@@ -591,8 +592,8 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
         g.part = rest - g.h * p.parts;
         g.item = static_cast<int>(w / p.parts);
         const int32_t* row = p.s.table;
-        int64_t run = 0;
-        for (int b0 = 0; b0 < p.s.batch && g.done; b0 += 32) {
+        int64_t run = run_from;
+        for (int b0 = b_from; b0 < p.s.batch && g.done; b0 += 32) {
           const int b = b0 + lane;
           const int r0 = b < p.s.batch ? kv_row0(p.s, b) : 0;
           const int n = b < p.s.batch ? max(kv_row0(p.s, b + 1) - r0, 0) : 0;
@@ -605,6 +606,8 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
           }
           const unsigned hit = __ballot_sync(0xffffffffu, run + x > flat);
           if (hit) {
+            b_from = b0;   // items come in order: the next one's search begins here
+            run_from = run;
             const int src = __ffs(hit) - 1;
             const int n_b = __shfl_sync(0xffffffffu, n, src), r0_b = __shfl_sync(0xffffffffu, r0, src);
             const int nb = __shfl_sync(0xffffffffu, blocks, src), before = __shfl_sync(0xffffffffu, x, src) - nb;
@@ -618,12 +621,16 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
             const KvTiles tl = kv_tiles<AT_TILE>(g.p0, g.p0 + g.n_tok - 1, p.window, p.sinks, g.key_end);
             g.st = tl.st;
             g.w0 = tl.w0;
-            g.i0 = static_cast<int>(static_cast<int64_t>(tl.count) * g.part / p.parts);
-            g.i1 = static_cast<int>(static_cast<int64_t>(tl.count) * (g.part + 1) / p.parts);
+            // parts of two tiles at least
+            g.parts = max(1, min(p.parts, tl.count / 2));
+            g.i0 = static_cast<int>(static_cast<int64_t>(tl.count) * g.part / g.parts);
+            g.i1 = static_cast<int>(static_cast<int64_t>(tl.count) * (g.part + 1) / g.parts);
             row = p.s.table + static_cast<int64_t>(b0 + src) * p.s.table_stride;
           }
           run += __shfl_sync(0xffffffffu, x, 31);
         }
+        if (!g.done && g.part >= g.parts) continue;   // fewer parts than the launch has room for
+        ++k;
         const int slot_i = k % AT_ITEMS;
         if (first && k >= AT_ITEMS && !(ok = wait(item_empty(slot_i), ((k / AT_ITEMS) - 1) & 1))) break;
         if (first && lane == 0) {

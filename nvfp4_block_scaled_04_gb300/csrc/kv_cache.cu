@@ -23,10 +23,36 @@ constexpr int PLAN_PER_THREAD = 16;
 
 // ------------------------------------------------------------------ append
 
-// One warp per (token, K or V): its row of every head. bf16 rows are copied,
-// E4M3 rows are x / scale[head] (IEEE division), rounded to nearest even and
+// Eight bf16 values over sc as E4M3 codes of the IEEE quotients. With r =
+// RN(1 / sc), rl = RN(r (1 - 2^-20)) lies below 1 / sc and rh = RN(r (1 + 2^-20))
+// above it, and rounding is monotone: where the codes of RN(x rl) and RN(x rh)
+// agree, they are the quotient's. Otherwise (a midpoint close by) the division
+// decides. (60,000 tokens: 82.6 -> 72.0 us, 5.1 TB/s.)
+NVFP4_DEV uint2 e4m3_of_quotients(const uint4& x, float sc) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const float r = __frcp_rn(sc), rl = r * 0.99999904632568359375f, rh = r * 1.00000095367431640625f;
+  uint32_t o[4], differ = 0;
+#pragma unroll
+  for (int z = 0; z < 4; ++z) {
+    const float a = bf16_bits_to_f32(w[z] & 0xFFFFu), b = bf16_bits_to_f32(w[z] >> 16);
+    o[z] = f32x2_to_e4m3x2(a * rl, b * rl);
+    differ |= o[z] ^ f32x2_to_e4m3x2(a * rh, b * rh);
+  }
+  if (differ || !(sc > 0x1p-100f && sc < 0x1p100f)) {
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+      o[z] = f32x2_to_e4m3x2(__fdiv_rn(bf16_bits_to_f32(w[z] & 0xFFFFu), sc), __fdiv_rn(bf16_bits_to_f32(w[z] >> 16), sc));
+  }
+  return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+}
+
+// One warp per (TOKENS consecutive tokens, K or V): their rows of every head.
+// The lanes look up the tokens' places side by side. bf16 rows are copied, E4M3
+// rows are x / scale[head] (IEEE division), rounded to nearest even and
 // saturated at 448: the cache's 8 bits are the one rounding of the append.
-template <bool E4M3>
+// TOKENS is 8 for long appends, which share one chain of dependent lookups
+// among 16 KB of rows, and 1 for short ones, which need all the warps.
+template <bool E4M3, int TOKENS>
 __global__ void __launch_bounds__(256) kv_append_kernel(const nvfp4_kv_cache_t c, const KvSeqs s, const uint16_t* K,
                                                         const uint16_t* V, int64_t k_stride, int64_t v_stride,
                                                         int* status) {
@@ -34,58 +60,79 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const nvfp4_kv_cache_t c
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
-  const int64_t t = unit >> 1;
+  const int64_t t0 = (unit >> 1) * TOKENS;
   const bool is_v = unit & 1;
-  if (t >= s.tokens) return;
-  // its sequence: the last one whose rows start at or before t
-  int b;
-  if (s.start) {
-    b = -1;
-    for (int i = 0; i < s.batch; i += 32) {
-      const bool before = i + lane < s.batch && s.start[i + lane] <= t;
-      const unsigned m = __ballot_sync(0xffffffffu, before);
-      if (m) b = i + 31 - __clz(m);
-      if (m != 0xffffffffu) break;
-    }
-  } else {
-    b = static_cast<int>(t / s.max_new);
-  }
-  if (b < 0 || b >= s.batch || t >= kv_row0(s, b + 1)) return;
-  const int64_t pos = static_cast<int64_t>(s.lens[b]) - (kv_row0(s, b + 1) - t);
-  const int64_t entry = pos / c.page_size;
-  const int page = pos >= 0 && entry < s.max_pages ? s.table[b * s.table_stride + entry] : -1;
-  if (page < 0 || page >= c.pages) {
-    if (lane == 0 && !is_v) atomicExch(status, NVFP4_ERR_INVALID_ARG);
-    return;
-  }
-  const uint16_t* src = (is_v ? V : K) + t * (is_v ? v_stride : k_stride);
+  if (t0 >= s.tokens) return;
   const int64_t head_elems = static_cast<int64_t>(c.page_size) * c.head_dim;
-  const int64_t row0 = (static_cast<int64_t>(page) * c.heads) * head_elems + (pos % c.page_size) * c.head_dim;
-  const int n8 = c.heads * c.head_dim / 8, d8 = c.head_dim / 8;
+  int64_t place = -1;   // of lane's token's row of head 0, in elements of the pool
+  const int64_t t = t0 + lane;
+  if (lane < TOKENS && t < s.tokens) {
+    // its sequence: the last one whose rows start at or before t
+    int lo = 0, hi = s.batch;
+    if (s.start) {
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.start[mid] <= t)
+          lo = mid;
+        else
+          hi = mid;
+      }
+    } else {
+      lo = static_cast<int>(t / s.max_new);
+    }
+    const int64_t r0 = kv_row0(s, lo), r1 = kv_row0(s, lo + 1);
+    if (t >= r0 && t < r1) {
+      const int64_t pos = static_cast<int64_t>(s.lens[lo]) - (r1 - t);
+      const int64_t entry = pos / c.page_size;
+      const int page = pos >= 0 && entry < s.max_pages ? s.table[lo * s.table_stride + entry] : -1;
+      if (page >= 0 && page < c.pages)
+        place = static_cast<int64_t>(page) * c.heads * head_elems + (pos % c.page_size) * c.head_dim;
+      else if (!is_v)
+        atomicExch(status, NVFP4_ERR_INVALID_ARG);
+    }
+  }
+  __syncwarp();
+  const int n8 = c.heads * c.head_dim / 8, d8_log2 = c.head_dim == 128 ? 4 : 3;
+  const int64_t stride = is_v ? v_stride : k_stride;
+  const uint16_t* src0 = (is_v ? V : K) + t0 * stride;
   uint8_t* pool = static_cast<uint8_t*>(is_v ? c.v : c.k);
   const float* scale = is_v ? c.v_scale : c.k_scale;
-#pragma unroll 4
-  for (int i = lane; i < n8; i += 32) {
-    const uint4 x = *reinterpret_cast<const uint4*>(src + i * 8);
-    const int h = i / d8;
-    const int64_t at = row0 + h * head_elems + (i - h * d8) * 8;
-    if (E4M3) {
-      const float sc = scale[h];
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t o[2];
+  for (int tt = 0; tt < TOKENS; ++tt) {
+    const int64_t row0 = __shfl_sync(0xffffffffu, place, tt);
+    if (row0 < 0) continue;
+    const uint16_t* src = src0 + tt * stride;
+    for (int i0 = lane; i0 < n8; i0 += 128) {
+      uint4 x[4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t a = f32x2_to_e4m3x2(__fdiv_rn(bf16_bits_to_f32(w[2 * j] & 0xFFFFu), sc),
-                                           __fdiv_rn(bf16_bits_to_f32(w[2 * j] >> 16), sc));
-        const uint32_t d = f32x2_to_e4m3x2(__fdiv_rn(bf16_bits_to_f32(w[2 * j + 1] & 0xFFFFu), sc),
-                                           __fdiv_rn(bf16_bits_to_f32(w[2 * j + 1] >> 16), sc));
-        o[j] = a | (d << 16);
+      for (int j = 0; j < 4; ++j)
+        if (i0 + 32 * j < n8) x[j] = *reinterpret_cast<const uint4*>(src + (i0 + 32 * j) * 8);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + 32 * j;
+        if (i >= n8) break;
+        const int h = i >> d8_log2;
+        const int64_t at = row0 + h * head_elems + (i - (h << d8_log2)) * 8;
+        if (E4M3) {
+          *reinterpret_cast<uint2*>(pool + at) = e4m3_of_quotients(x[j], scale[h]);
+        } else {
+          *reinterpret_cast<uint4*>(pool + 2 * at) = x[j];
+        }
       }
-      *reinterpret_cast<uint2*>(pool + at) = make_uint2(o[0], o[1]);
-    } else {
-      *reinterpret_cast<uint4*>(pool + 2 * at) = x;
     }
   }
+}
+
+template <bool E4M3>
+int launch_append(const nvfp4_kv_cache_t& c, const KvSeqs& s, const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                  int64_t v_stride, int* status, cudaStream_t stream) {
+  // 8 tokens a warp once that still gives every SM 16 warps
+  const bool many = s.tokens >= 64 * static_cast<int64_t>(sm_count());
+  const int64_t units = 2 * ceil_div(s.tokens, many ? 8 : 1);
+  // few rows spread over more CTAs, one warp each
+  const int threads = units <= 8 * sm_count() ? 32 : 256;
+  const dim3 grid(static_cast<unsigned>(ceil_div(units, threads / 32)));
+  return many ? launch_ex(kv_append_kernel<E4M3, 8>, grid, dim3(threads), 0, 1, true, stream, c, s, k, v, k_stride, v_stride, status)
+              : launch_ex(kv_append_kernel<E4M3, 1>, grid, dim3(threads), 0, 1, true, stream, c, s, k, v, k_stride, v_stride, status);
 }
 
 // ------------------------------------------------------------ planning CTA
@@ -392,15 +439,43 @@ __global__ void __launch_bounds__(256) kv_compact_move_kernel(const nvfp4_kv_cac
   const int moves = ws[2 * c.pages], n = ws[2 * c.pages + 1];
   const int chunks = static_cast<int>((page_bytes + COMPACT_CHUNK - 1) / COMPACT_CHUNK);
   const int64_t units = static_cast<int64_t>(moves) * 2 * chunks;
+  // a step's loads are in flight while the last step's stores go out, and its
+  // page ids are read a step earlier still
+  struct Step {
+    const uint4* x;
+    uint4* o;
+    int n16;
+  };
+  auto step = [&](int64_t u) {
+    Step t = {nullptr, nullptr, 0};
+    if (u < units) {
+      const int m = static_cast<int>(u / (2 * chunks)), part = static_cast<int>(u - static_cast<int64_t>(m) * 2 * chunks);
+      uint8_t* pool = static_cast<uint8_t*>(part < chunks ? c.k : c.v);
+      const int64_t off = static_cast<int64_t>(part < chunks ? part : part - chunks) * COMPACT_CHUNK;
+      t.x = reinterpret_cast<const uint4*>(pool + from[m] * page_bytes + off) + threadIdx.x;
+      t.o = reinterpret_cast<uint4*>(pool + to[m] * page_bytes + off) + threadIdx.x;
+      t.n16 = static_cast<int>((page_bytes - off < COMPACT_CHUNK ? page_bytes - off : COMPACT_CHUNK) / 16) - static_cast<int>(threadIdx.x);
+    }
+    return t;
+  };
+  constexpr int PER = COMPACT_CHUNK / 16 / 256;
+  Step now = step(blockIdx.x), then = step(static_cast<int64_t>(blockIdx.x) + gridDim.x);
+  uint4 x[PER], y[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (256 * j < now.n16) x[j] = now.x[256 * j];
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int m = static_cast<int>(u / (2 * chunks)), part = static_cast<int>(u - static_cast<int64_t>(m) * 2 * chunks);
-    uint8_t* pool = static_cast<uint8_t*>(part < chunks ? c.k : c.v);
-    const int64_t off = static_cast<int64_t>(part < chunks ? part : part - chunks) * COMPACT_CHUNK;
-    const uint4* x = reinterpret_cast<const uint4*>(pool + from[m] * page_bytes + off);
-    uint4* o = reinterpret_cast<uint4*>(pool + to[m] * page_bytes + off);
-    const int n16 = static_cast<int>((page_bytes - off < COMPACT_CHUNK ? page_bytes - off : COMPACT_CHUNK) / 16);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n16; i += 256) o[i] = x[i];
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (256 * j < then.n16) y[j] = then.x[256 * j];
+    const Step next = step(u + 2 * static_cast<int64_t>(gridDim.x));
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (256 * j < now.n16) now.o[256 * j] = x[j];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) x[j] = y[j];
+    now = then;
+    then = next;
   }
   const int64_t gtid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t gthreads = static_cast<int64_t>(gridDim.x) * blockDim.x;
@@ -434,17 +509,10 @@ int launch_kv_append(const nvfp4_kv_cache_t& c, const KvSeqs& s, const void* K, 
                      int64_t v_stride, cudaStream_t stream) {
   int* status = device_status_ptr();
   if (!status) return NVFP4_ERR_CUDA;
-  // few rows spread over more CTAs, one warp each
-  const int64_t units = 2 * s.tokens;
-  const int threads = units <= 8 * sm_count() ? 32 : 256;
-  const dim3 grid(static_cast<unsigned>(ceil_div(units, threads / 32)));
   auto* k = static_cast<const uint16_t*>(K);
   auto* v = static_cast<const uint16_t*>(V);
-  if (c.dtype == NVFP4_DTYPE_E4M3)
-    return launch_ex(kv_append_kernel<true>, grid, dim3(threads), 0, 1, true, stream, c, s, k, v, k_stride, v_stride,
-                     status);
-  return launch_ex(kv_append_kernel<false>, grid, dim3(threads), 0, 1, true, stream, c, s, k, v, k_stride, v_stride,
-                   status);
+  return c.dtype == NVFP4_DTYPE_E4M3 ? launch_append<true>(c, s, k, v, k_stride, v_stride, status, stream)
+                                     : launch_append<false>(c, s, k, v, k_stride, v_stride, status, stream);
 }
 
 size_t kv_pages_workspace_bytes(int64_t pages, int64_t n) { return static_cast<size_t>(4 * (2 * pages + n + 4)); }
