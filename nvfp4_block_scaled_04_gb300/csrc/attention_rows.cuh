@@ -80,6 +80,7 @@ struct ArShape {
   static constexpr int ROWS = 8 * NT;
   static constexpr int THREADS = (WARPS + 2) * 32;               // consumers, the producer, the item warp
   static constexpr int CTAS = WARPS == 4 ? 2 : 1;                // per SM
+  static constexpr int EXTRA = 3;                                // tiles' time that an item costs beside its tiles
   static constexpr int BUFS = ROWS <= 16 && WARPS == 8 ? 4 : 2;  // merge buffers
   static constexpr bool Q_REGS = NT <= 2;                        // query fragments in registers, else read per tile
   static constexpr int ROW_BYTES = D * (E4M3 ? 1 : 2);
@@ -165,46 +166,52 @@ struct ArWalk {
   int b;                 // the sequence
 
   NVFP4_DEV bool next(ArItem& g) {
-    if (u >= end) return false;
-    int lo = 0, hi = p.s.batch;             // last b with pre[b] <= u
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= u)
-        lo = mid;
-      else
-        hi = mid;
+    while (u < end) {
+      int lo = 0, hi = p.s.batch;             // last b with pre[b] <= u
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= u)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      b = lo;
+      g.done = 0;
+      const bool kept = p.s.batch <= AR_KEPT;
+      g.row0 = kept ? rows[lo] : kv_row0(p.s, lo);
+      const int n = (kept ? rows[lo + 1] : kv_row0(p.s, lo + 1)) - g.row0;
+      const int len = kept ? rows[p.s.batch + 1 + lo] : kv_len(p.s, lo);
+      const unsigned blocks = static_cast<unsigned>((n * p.group + S::ROWS - 1) / S::ROWS);
+      const unsigned per_item = (pre[lo + 1] - pre[lo]) / (blocks * static_cast<unsigned>(p.heads));
+      const unsigned in = u - pre[lo], item = in / per_item;
+      const int rb = static_cast<int>(item / static_cast<unsigned>(p.heads));
+      g.h = static_cast<int>(item) - rb * p.heads;
+      g.i0 = static_cast<int>(in - item * per_item);
+      const unsigned u0 = u - static_cast<unsigned>(g.i0);
+      const int i1 = static_cast<int>(min(end - u0, per_item));
+      u = u0 + static_cast<unsigned>(i1);
+      g.r0 = rb * S::ROWS;
+      g.n_rows = min(S::ROWS, n * p.group - g.r0);
+      g.p0 = len - n + g.r0 / p.group;
+      g.p1 = len - n + (g.r0 + g.n_rows - 1) / p.group;
+      const int64_t cap = static_cast<int64_t>(p.s.max_pages) * p.page_size;
+      g.key_end = static_cast<int>(cap < len ? cap : len);
+      g.tiles = kv_tiles<S::TILE>(g.p0, g.p1, p.window, p.sinks, g.key_end);
+      // what follows the item's tiles on the line is nobody's work
+      const int real = max(g.tiles.count, 1);
+      if (g.i0 >= real) continue;
+      g.i1 = min(i1, g.tiles.count);
+      g.first_cta = u0 / per;
+      g.last_cta = (u0 + static_cast<unsigned>(real) - 1u) / per;
+      return true;
     }
-    b = lo;
-    g.done = 0;
-    const bool kept = p.s.batch <= AR_KEPT;
-    g.row0 = kept ? rows[lo] : kv_row0(p.s, lo);
-    const int n = (kept ? rows[lo + 1] : kv_row0(p.s, lo + 1)) - g.row0;
-    const int len = kept ? rows[p.s.batch + 1 + lo] : kv_len(p.s, lo);
-    const unsigned blocks = static_cast<unsigned>((n * p.group + S::ROWS - 1) / S::ROWS);
-    const unsigned per_item = (pre[lo + 1] - pre[lo]) / (blocks * static_cast<unsigned>(p.heads));
-    const unsigned in = u - pre[lo], item = in / per_item;
-    const int rb = static_cast<int>(item / static_cast<unsigned>(p.heads));
-    g.h = static_cast<int>(item) - rb * p.heads;
-    g.i0 = static_cast<int>(in - item * per_item);
-    const unsigned u0 = u - static_cast<unsigned>(g.i0), left = end - u;
-    int i1 = left < per_item - static_cast<unsigned>(g.i0) ? g.i0 + static_cast<int>(left) : static_cast<int>(per_item);
-    u += static_cast<unsigned>(i1 - g.i0);
-    g.first_cta = u0 / per;
-    g.last_cta = (u0 + per_item - 1u) / per;
-    g.r0 = rb * S::ROWS;
-    g.n_rows = min(S::ROWS, n * p.group - g.r0);
-    g.p0 = len - n + g.r0 / p.group;
-    g.p1 = len - n + (g.r0 + g.n_rows - 1) / p.group;
-    const int64_t cap = static_cast<int64_t>(p.s.max_pages) * p.page_size;
-    g.key_end = static_cast<int>(cap < len ? cap : len);
-    g.tiles = kv_tiles<S::TILE>(g.p0, g.p1, p.window, p.sinks, g.key_end);
-    g.i1 = min(i1, g.tiles.count);
-    return true;
+    return false;
   }
 };
 
-// Tiles of all items of a sequence of n new tokens: each block of rows is given
-// the most that any sees, at least one.
+// Length on the line of all items of a sequence of n new tokens: each block of
+// rows is given the most tiles that any sees, and EXTRA more that stand for what
+// an item costs beside them (its parts' meeting and the output).
 template <class S>
 NVFP4_DEV unsigned ar_seq_tiles(const ArParams& p, int n, int len) {
   if (n <= 0) return 0;
@@ -222,7 +229,7 @@ NVFP4_DEV unsigned ar_seq_tiles(const ArParams& p, int n, int len) {
   } else {
     most = kv_tiles<S::TILE>(len - n, len - 1, p.window, p.sinks, key_end).count;
   }
-  return static_cast<unsigned>(max(most, 1)) * static_cast<unsigned>(blocks * p.heads);
+  return static_cast<unsigned>(max(most, 1) + S::EXTRA) * static_cast<unsigned>(blocks * p.heads);
 }
 
 template <bool E4M3, int D, int WARPS, int NT>
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
   unsigned per = (total + gridDim.x - 1) / gridDim.x;
   // where a CTA's piece would be one tile of long items, two: half the parts to
   // join (one sequence of 2,000 positions: 8.8 -> 8.0 us)
-  if (per == 1 && total >= 16u * static_cast<unsigned>(p.s.batch * p.heads)) per = 2;
+  if (per == 1 && total >= (16u + S::EXTRA) * static_cast<unsigned>(p.s.batch * p.heads)) per = 2;
   const uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * per;
   if (u0 >= total) return;
   ArWalk<S> walk{p, pre, rows, per, static_cast<unsigned>(u0), static_cast<unsigned>(u0 + per < total ? u0 + per : total), 0};
