@@ -429,9 +429,9 @@ int nvfp4_paged_attention(const void* Q, int64_t q_stride, int q_heads, nvfp4_kv
  * the call's list. Where the pool runs out, entries stay without a page (-1) and
  * the device status word says NVFP4_ERR_NO_PAGES; a list entry outside the
  * table's rows is skipped (NVFP4_ERR_INVALID_ARG in the status word). Sequence
- * lists must not name a row twice. `workspace`: >= nvfp4_workspace_size(
- * NVFP4_OP_KV_PAGES, pages, entries of the list (or batch), 0, 0, 0) bytes,
- * 16-byte aligned; scratch. */
+ * lists must not name a row twice. `workspace` (reserve, compact): >=
+ * nvfp4_workspace_size(NVFP4_OP_KV_PAGES, pages, batch (compact: 0), 0, 0, 0)
+ * bytes, 16-byte aligned; scratch. */
 
 /* A page for every position of the sequences' new tokens whose table entry
  * holds none (`table` is seqs.table, written). */
@@ -444,8 +444,7 @@ int nvfp4_kv_reserve(nvfp4_kv_seqs_t seqs, int64_t tokens, int page_size, int32_
  * a src may be forked many times.
  *   table  device int32 [rows][max_pages];  lens  device int32 [rows] */
 int nvfp4_kv_fork(nvfp4_kv_cache_t cache, int32_t* table, int64_t table_stride, int max_pages, int32_t* lens, int rows,
-                  int32_t* refs, const int32_t* src, const int32_t* dst, int n, void* workspace,
-                  size_t workspace_bytes, nvfp4_stream_t stream);
+                  int32_t* refs, const int32_t* src, const int32_t* dst, int n, nvfp4_stream_t stream);
 
 /* Give up sequences: their pages' counts go down by one, their table rows to
  * -1 and their lengths to 0. */
@@ -473,7 +472,7 @@ size_t nvfp4_scales_bytes(int64_t rows, int64_t K, int scale_layout);
  *   GEMM_W4A4_QUANT: (M, N, K, -, -)
  *   GROUPED_GEMM_W4A4: (T, H, I, E, topk)
  *   PAGED_ATTENTION: (batch, max_new, q_heads, kv_heads, head_dim)
- *   KV_PAGES:      (pages, entries of the list or batch, -, -, -) */
+ *   KV_PAGES:      (pages, batch, -, -, -) */
 size_t nvfp4_workspace_size(int op, int64_t a, int64_t b, int64_t c, int64_t e, int64_t topk);
 
 /* Human-readable name of a status code (static storage). */

@@ -86,7 +86,7 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_kv_append.argtypes = [CKVCache, CKVSeqs, vp, i64, vp, i64, i64, vp]
         L.nvfp4_paged_attention.argtypes = [vp, i64, i32, CKVCache, CKVSeqs, i64, i32, i32, ctypes.c_float, vp, vp, sz, vp]
         L.nvfp4_kv_reserve.argtypes = [CKVSeqs, i64, i32, vp, vp, i64, vp, sz, vp]
-        L.nvfp4_kv_fork.argtypes = [CKVCache, vp, i64, i32, vp, i32, vp, vp, vp, i32, vp, sz, vp]
+        L.nvfp4_kv_fork.argtypes = [CKVCache, vp, i64, i32, vp, i32, vp, vp, vp, i32, vp]
         L.nvfp4_kv_release.argtypes = [vp, i64, i32, vp, i32, vp, i64, vp, i32, vp]
         L.nvfp4_kv_compact.argtypes = [CKVCache, vp, i64, i32, i32, vp, vp, vp, sz, vp]
         L.nvfp4_scales_bytes.argtypes = [i64, i64, i32]
@@ -358,29 +358,33 @@ def verify_accept(h: torch.Tensor, w: QTensor, draft_ids: torch.Tensor, workspac
     return tokens, n_acc
 
 
-@dataclass
+@dataclass(frozen=True)
 class KVCache:
     """One layer's paged key-value cache: pools k, v [pages][heads][page_size]
     [head_dim], bf16, or float8_e4m3fn with a scale for each kv head
-    (value = code * scale)."""
+    (value = code * scale). Page sizes 16, 32, 64, 128; head_dim 64 or 128."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor | None = None
     v_scale: torch.Tensor | None = None
 
     def __post_init__(self):
-        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
-        _require_cuda(k, v, ks, vs)
-        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or not k.is_contiguous() or not v.is_contiguous():
+        k, v = self.k, self.v
+        shape, dtype = k.shape, k.dtype
+        if len(shape) != 4 or shape != v.shape or dtype != v.dtype or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("KVCache: k and v are contiguous pools [pages][heads][page_size][head_dim] of one type")
-        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        _require_cuda(k, v)
+        if dtype == torch.bfloat16:
+            object.__setattr__(self, "_c", CKVCache(k.data_ptr(), v.data_ptr(), None, None, *shape, DTYPE_BF16))
+            return
+        if dtype != torch.float8_e4m3fn:
             raise ValueError("KVCache: pools are bfloat16 or float8_e4m3fn")
-        e4m3 = k.dtype == torch.float8_e4m3fn
-        for t in (ks, vs) if e4m3 else ():
-            if t is None or t.dtype != torch.float32 or t.shape != (k.shape[1],) or not t.is_contiguous():
+        for t in (self.k_scale, self.v_scale):
+            if t is None or t.dtype != torch.float32 or t.shape != shape[1:2] or not t.is_contiguous():
                 raise ValueError("KVCache: an E4M3 cache needs fp32 scales [heads]")
-        self._c = CKVCache(k.data_ptr(), v.data_ptr(), ks.data_ptr() if e4m3 else None, vs.data_ptr() if e4m3 else None,
-                           k.shape[0], k.shape[1], k.shape[2], k.shape[3], DTYPE_E4M3 if e4m3 else DTYPE_BF16)
+        _require_cuda(self.k_scale, self.v_scale)
+        object.__setattr__(self, "_c", CKVCache(k.data_ptr(), v.data_ptr(), self.k_scale.data_ptr(),
+                                                self.v_scale.data_ptr(), *shape, DTYPE_E4M3))
 
     def c(self) -> CKVCache:
         return self._c
@@ -515,7 +519,7 @@ def _pool_args(table, lens, refs, pages=None):
 
 
 def kv_fork(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, src: torch.Tensor,
-            dst: torch.Tensor, workspace: torch.Tensor | None = None) -> None:
+            dst: torch.Tensor) -> None:
     """Rows dst[f] of the table become forks of rows src[f]: full pages are
     shared, the positions in use of a partly filled last page are copied to a
     fresh page. dst rows must be empty, distinct and not in src."""
@@ -524,9 +528,8 @@ def kv_fork(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, refs: torch
         raise ValueError("kv_fork: src and dst need the same length")
     c = cache._c
     args = _pool_args(table, lens, refs, c.pages)
-    ws = _pages_ws(workspace, c.pages, n, refs.device)
     _check(lib().nvfp4_kv_fork(c, *args, lens.data_ptr(), table.shape[0], refs.data_ptr(), src.data_ptr(),
-                               dst.data_ptr(), n, ws.data_ptr(), ws.numel(), _stream()), "nvfp4_kv_fork")
+                               dst.data_ptr(), n, _stream()), "nvfp4_kv_fork")
 
 
 def kv_release(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seqs: torch.Tensor) -> None:

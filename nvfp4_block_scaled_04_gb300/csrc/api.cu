@@ -357,14 +357,12 @@ int nvfp4_kv_reserve(nvfp4_kv_seqs_t seqs, int64_t tokens, int page_size, int32_
 }
 
 int nvfp4_kv_fork(nvfp4_kv_cache_t cache, int32_t* table, int64_t table_stride, int max_pages, int32_t* lens, int rows,
-                  int32_t* refs, const int32_t* src, const int32_t* dst, int n, void* workspace,
-                  size_t workspace_bytes, nvfp4_stream_t stream) {
+                  int32_t* refs, const int32_t* src, const int32_t* dst, int n, nvfp4_stream_t stream) {
   if (int rc = cache_check(cache)) return rc;
   if (int rc = pages_check(table, table_stride, max_pages, rows, refs)) return rc;
   if (!lens || n < 0 || (n > 0 && (!src || !dst))) return NVFP4_ERR_INVALID_ARG;
   if (n == 0) return NVFP4_OK;
-  if (int rc = pages_ws_check(workspace, workspace_bytes, cache.pages, n)) return rc;
-  return launch_kv_fork(cache, table, table_stride, max_pages, lens, rows, refs, src, dst, n, workspace,
+  return launch_kv_fork(cache, table, table_stride, max_pages, lens, rows, refs, src, dst, n,
                         reinterpret_cast<cudaStream_t>(stream));
 }
 

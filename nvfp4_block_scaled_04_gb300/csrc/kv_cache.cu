@@ -264,21 +264,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(const KvSeqs s
 
 // -------------------------------------------------------------------- fork
 
-// Which fresh page each fork's partly filled last page is copied to (-1:
-// none); marks those pages taken. ws: free pages [pages], fresh page of each fork [n].
-__global__ void __launch_bounds__(PLAN_THREADS) kv_fork_plan_kernel(const int32_t* table, int64_t table_stride,
-                                                                    int max_pages, const int32_t* lens, int rows,
-                                                                    int32_t* refs, int64_t pages, int page_size,
-                                                                    const int32_t* src, const int32_t* dst, int n,
-                                                                    int32_t* ws, int* status) {
+// Gives each fork's partly filled last page a fresh page (-1 where there is
+// none left or none is needed): its id goes into the fork's table row, and the
+// page is taken. PLAN_THREADS forks at a time.
+__global__ void __launch_bounds__(PLAN_THREADS) kv_fork_plan_kernel(int32_t* table, int64_t table_stride, int max_pages,
+                                                                    const int32_t* lens, int rows, int32_t* refs,
+                                                                    int64_t pages, int page_size, const int32_t* src,
+                                                                    const int32_t* dst, int n, int* status) {
+  __shared__ int32_t list[PLAN_THREADS];
   pdl_launch_dependents();
   pdl_wait();
-  int32_t* list = ws;               // [pages]
-  int32_t* fresh = ws + pages;      // [n]
-  int need = 0;
   for (int f0 = 0; f0 < n; f0 += PLAN_THREADS) {
     const int f = f0 + static_cast<int>(threadIdx.x);
     bool wants = false;
+    int32_t* entry = nullptr;   // of the fork's last page, where it is partly filled
     if (f < n) {
       const int a = src[f], d = dst[f];
       if (a >= 0 && a < rows && d >= 0 && d < rows && a != d) {
@@ -286,23 +285,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_fork_plan_kernel(const int32_
         if (len > 0 && len % page_size != 0 && len / page_size < max_pages) {
           const int p = table[a * table_stride + len / page_size];
           wants = p >= 0 && p < pages;
+          entry = table + d * table_stride + len / page_size;
         }
       } else {
         atomicExch(status, NVFP4_ERR_INVALID_ARG);
       }
     }
-    int total;
-    const int at = need + plan_scan(wants, &total);
-    if (f < n) fresh[f] = wants ? at : -1;
-    need += total;
-  }
-  const int have = lowest_free(refs, pages, need < pages ? need : static_cast<int>(pages), list);
-  if (threadIdx.x == 0 && have < need) atomicExch(status, NVFP4_ERR_NO_PAGES);
-  for (int f = threadIdx.x; f < n; f += PLAN_THREADS) {
-    const int at = fresh[f];
-    const int p = at >= 0 && at < have ? list[at] : -1;
-    fresh[f] = p;
+    int need;
+    const int at = plan_scan(wants, &need);
+    const int have = lowest_free(refs, pages, need, list);
+    if (threadIdx.x == 0 && have < need) atomicExch(status, NVFP4_ERR_NO_PAGES);
+    const int p = wants && at < have ? list[at] : -1;
+    if (entry) *entry = p;
     if (p >= 0) refs[p] = 1;
+    __syncthreads();   // the list has been read, and these pages are taken for the next forks
   }
 }
 
@@ -311,15 +307,16 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_fork_plan_kernel(const int32_
 __global__ void __launch_bounds__(128) kv_fork_copy_kernel(const nvfp4_kv_cache_t c, int32_t* table,
                                                            int64_t table_stride, int max_pages, int32_t* lens,
                                                            int rows, int32_t* refs, const int32_t* src,
-                                                           const int32_t* dst, const int32_t* ws, int elem_bytes) {
+                                                           const int32_t* dst, int elem_bytes) {
   pdl_launch_dependents();
   pdl_wait();
   const int f = blockIdx.x, y = blockIdx.y;
   const int a = src[f], d = dst[f];
   if (a < 0 || a >= rows || d < 0 || d >= rows || a == d) return;
-  const int fresh = ws[c.pages + f];
   const int len = lens[a] > 0 ? lens[a] : 0;
   const int full = len / c.page_size, tail = len % c.page_size;
+  // the plan wrote it; the block that writes the row writes it again as it is
+  const int fresh = tail && full < max_pages ? table[d * table_stride + full] : -1;
   const int32_t* from = table + a * table_stride;
   if (y < 2 * c.heads) {
     if (fresh < 0) return;
@@ -526,17 +523,15 @@ int launch_kv_reserve(const KvSeqs& s, int page_size, int32_t* table, int32_t* r
 }
 
 int launch_kv_fork(const nvfp4_kv_cache_t& c, int32_t* table, int64_t table_stride, int max_pages, int32_t* lens,
-                   int rows, int32_t* refs, const int32_t* src, const int32_t* dst, int n, void* ws,
-                   cudaStream_t stream) {
+                   int rows, int32_t* refs, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream) {
   int* status = device_status_ptr();
   if (!status) return NVFP4_ERR_CUDA;
-  int32_t* w = static_cast<int32_t*>(ws);
-  int rc = launch_ex(kv_fork_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, 1, true, stream,
-                     static_cast<const int32_t*>(table), table_stride, max_pages, static_cast<const int32_t*>(lens),
-                     rows, refs, static_cast<int64_t>(c.pages), static_cast<int>(c.page_size), src, dst, n, w, status);
+  int rc = launch_ex(kv_fork_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, 1, true, stream, table, table_stride, max_pages,
+                     static_cast<const int32_t*>(lens), rows, refs, static_cast<int64_t>(c.pages),
+                     static_cast<int>(c.page_size), src, dst, n, status);
   if (rc) return rc;
   return launch_ex(kv_fork_copy_kernel, dim3(n, 2 * c.heads + 1), dim3(128), 0, 1, true, stream, c, table, table_stride,
-                   max_pages, lens, rows, refs, src, dst, static_cast<const int32_t*>(w), elem_bytes_of(c));
+                   max_pages, lens, rows, refs, src, dst, elem_bytes_of(c));
 }
 
 int launch_kv_release(int32_t* table, int64_t table_stride, int max_pages, int32_t* lens, int rows, int32_t* refs,

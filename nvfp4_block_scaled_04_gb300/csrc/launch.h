@@ -160,8 +160,7 @@ size_t kv_pages_workspace_bytes(int64_t pages, int64_t n);
 int launch_kv_reserve(const KvSeqs& s, int page_size, int32_t* table, int32_t* refs, int64_t pages, void* ws,
                       cudaStream_t stream);
 int launch_kv_fork(const nvfp4_kv_cache_t& c, int32_t* table, int64_t table_stride, int max_pages, int32_t* lens,
-                   int rows, int32_t* refs, const int32_t* src, const int32_t* dst, int n, void* ws,
-                   cudaStream_t stream);
+                   int rows, int32_t* refs, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream);
 int launch_kv_release(int32_t* table, int64_t table_stride, int max_pages, int32_t* lens, int rows, int32_t* refs,
                       int64_t pages, const int32_t* seqs, int n, cudaStream_t stream);
 int launch_kv_compact(const nvfp4_kv_cache_t& c, int32_t* table, int64_t table_stride, int max_pages, int rows,

@@ -226,3 +226,100 @@ def test_more_new_tokens_than_announced_are_computed():
                             torch.tensor(c.lens, dtype=torch.int32, device=DEV), start=offsets(news).to(DEV), max_new=3)
     got = got.float().cpu().double().numpy()
     assert (np.abs(got - ref) <= bound(ref, size, 6, "bf16")).all()
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [[1, 1], [60, 70]])
+def test_scales_that_are_not_positive(kv, news, scale):
+    c = Cache([300, 90], 2, 32, 64, kv, seed=15)
+    check(c, news, 4, scale=scale, window=100, sinks=2)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group,news", [(64, [1, 5]), (65, [1, 2]), (96, [9]), (128, [2, 3])])
+def test_many_query_heads_on_one(kv, group, news):
+    c = Cache([n + 200 for n in news], 1, 16, 64, kv, seed=16)
+    check(c, news, group)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_short_chunk_on_a_long_context(kv):
+    """Few row blocks: each is split over the positions and joined."""
+    c = Cache([9000 + 40, 3000 + 33], 2, 64, 128, kv, seed=17)
+    check(c, [40, 33], 4)
+    check(c, [40, 33], 4, window=4000, sinks=200)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("magnitude", [1e-30, 1e30])
+def test_prompt_queries_of_any_magnitude(kv, magnitude):
+    m = nv()
+    c = Cache([300], 2, 16, 128, kv, seed=18)
+    q = (queries(100, 8, 128, 1).double() * magnitude).bfloat16()
+    q[50:60] = 0
+    scale = 128 ** -0.5 / magnitude
+    ref, size = attention(c, q, [100], scale=scale)
+    got = m.paged_attention(q.to(DEV), device_cache(m, c), c.table.to(DEV), torch.tensor(c.lens, dtype=torch.int32,
+                                                                                          device=DEV), max_new=100, scale=scale)
+    got = got.float().cpu().double().numpy()
+    assert (np.abs(got - ref) <= bound(ref, size, 400, kv)).all()
+
+
+def test_calls_on_two_streams_do_not_meet():
+    """Two calls at once, each with its own workspace."""
+    m = nv()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    work = []
+    for i, side in enumerate(sides):
+        c = Cache([4000 + i, 33], 2, 64, 128, "bf16", seed=20 + i)
+        q = queries(2, 8, 128, i)
+        work.append((side, c, q, device_cache(m, c), c.table.to(DEV), torch.tensor(c.lens, dtype=torch.int32, device=DEV),
+                     q.to(DEV), m.attention_workspace(2, 1, 8, 2, 128)))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, (side, c, q, dc, table, lens, qd, ws) in enumerate(work):
+            with torch.cuda.stream(side):
+                outs[i].append(m.paged_attention(qd, dc, table, lens, workspace=ws))
+    torch.cuda.synchronize()
+    for (side, c, q, *_), got in zip(work, outs):
+        ref, size = attention(c, q, [1, 1])
+        for x in got:
+            assert torch.equal(x, got[0])
+        assert (np.abs(got[0].float().cpu().double().numpy() - ref) <= bound(ref, size, 4, "bf16")).all()
+
+
+def test_python_refusals():
+    m = nv()
+    k = torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16, device=DEV)
+    cache = m.KVCache(k, k.clone())
+    table, lens = torch.zeros(2, 4, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV)
+    m.paged_attention(q, cache, table, lens)
+    for bad in (dict(q=q.float()), dict(q=q[:, :, :32]), dict(q=q[0]), dict(table=table.long()), dict(lens=lens[:1]),
+                dict(start=lens), dict(table=table.t()), dict(out=q.float()), dict(out=q[:1])):
+        args = dict(q=q, table=table, lens=lens)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            m.paged_attention(args.pop("q"), cache, args.pop("table"), args.pop("lens"), **args)
+    for bad in (dict(max_new=0), dict(window=-1), dict(workspace=torch.zeros(64, dtype=torch.uint8, device=DEV)),
+                dict(q=q[:1]), dict(q=q[:, :3])):
+        args = dict(q=q)
+        args.update(bad)
+        with pytest.raises(RuntimeError):
+            m.paged_attention(args.pop("q"), cache, table, lens, **args)
+    with pytest.raises(RuntimeError):
+        m.paged_attention(q, cache, table.cpu(), lens)
+    with pytest.raises(ValueError):
+        m.KVCache(k.view(torch.uint8), k.view(torch.uint8))
+    with pytest.raises(ValueError):
+        m.KVCache(k[..., ::2], k[..., ::2])
+    codes = torch.zeros(8, 2, 16, 64, dtype=torch.float8_e4m3fn, device=DEV)
+    with pytest.raises(ValueError):
+        m.KVCache(codes, codes)
+    with pytest.raises(ValueError):
+        m.kv_append(cache, q, q[:1], table, lens)
+    with pytest.raises(ValueError):
+        m.kv_fork(cache, table, lens, lens, lens[:1], lens[:1])   # one count for each page
+    assert m.read_device_status() == 0
