@@ -529,8 +529,9 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
           ldsm_x4(kb + swz(k_row, 2 * k2 + (lane >> 4)), r);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * hf] & 0xFFFFu), e4m3x2_to_f16x2(r[2 * hf + 1] & 0xFFFFu),
-                                   e4m3x2_to_f16x2(r[2 * hf] >> 16), e4m3x2_to_f16x2(r[2 * hf + 1] >> 16)};
+            uint32_t a[4];
+            e4m3x4_to_f16x2(r[2 * hf], a[0], a[2]);
+            e4m3x4_to_f16x2(r[2 * hf + 1], a[1], a[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16_16816(hf && NT == 2 ? s2[nt] : s[nt], a, q_at(2 * k2 + hf, nt).x, q_at(2 * k2 + hf, nt).y);
           }
@@ -623,9 +624,10 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<
           ldsm_x4_t(vb + swz(v_row, 2 * m2 + (lane >> 4)), r);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t x = __byte_perm(r[2 * hf], 0, 0x3120), y = __byte_perm(r[2 * hf + 1], 0, 0x3120);
-            const uint32_t a[4] = {e4m3x2_to_f16x2(x & 0xFFFFu) & keep[0], e4m3x2_to_f16x2(x >> 16) & keep[0],
-                                   e4m3x2_to_f16x2(y & 0xFFFFu) & keep[1], e4m3x2_to_f16x2(y >> 16) & keep[1]};
+            // a word holds two tokens' codes of two d's: (token, d), (token, d + 1), (token + 1, d), ...
+            uint32_t a[4];
+            e4m3x4_to_f16x2(__byte_perm(r[2 * hf] & keep[0], 0, 0x3120), a[0], a[1]);
+            e4m3x4_to_f16x2(__byte_perm(r[2 * hf + 1] & keep[1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[2 * m2 + hf][nt], a, hi[nt][0], hi[nt][1]);
           }

@@ -831,8 +831,9 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
                   const uint32_t y[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
                   for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t h[4] = {e4m3x2_to_f16x2(y[2 * hf] & 0xFFFFu), e4m3x2_to_f16x2(y[2 * hf] >> 16),
-                                           e4m3x2_to_f16x2(y[2 * hf + 1] & 0xFFFFu), e4m3x2_to_f16x2(y[2 * hf + 1] >> 16)};
+                    uint32_t h[4];
+                    e4m3x4_to_f16x2(y[2 * hf], h[0], h[1]);
+                    e4m3x4_to_f16x2(y[2 * hf + 1], h[2], h[3]);
                     const int c8 = 2 * piece + hf;   // 16-byte chunk of the f16 row
                     sts128(slot(s) + (c8 >> 3) * (AT_TILE * 128) + row * 128 + (((c8 & 7) ^ (row & 7)) << 4), h);
                   }

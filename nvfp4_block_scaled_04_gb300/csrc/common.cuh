@@ -67,6 +67,16 @@ NVFP4_DEV uint32_t f32_to_e4m3(float v) {
   return out & 0xFFu;
 }
 
+// Four E4M3 codes (low byte first) -> two f16x2 words.
+NVFP4_DEV void e4m3x4_to_f16x2(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
+
 // Two fp32 -> two E4M3 codes (lo in the low byte), round to nearest even, saturating at 448.
 NVFP4_DEV uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   uint32_t out;
