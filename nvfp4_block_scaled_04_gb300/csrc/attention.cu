@@ -18,13 +18,11 @@ int log2_of(int x) {
   return n;
 }
 
-// Eight-row tiles of an item of the split kernel. An E4M3 cache with more than
-// 24 rows takes two items of 16: the fragments of four tiles beside the
-// conversions' do not fit the registers.
-int rows_nt(int64_t rows, bool e4m3) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : e4m3 ? 2 : 4; }
+// Eight-row tiles of an item of the split kernel (more than 32 rows: several items).
+int rows_nt(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
 
-// CTAs of the split kernel: two per SM for one eight-row tile, else one of more warps.
-int rows_grid(int nt) { return (nt == 1 ? 2 : 1) * sm_count(); }
+// Its CTAs: two per SM while the accumulators leave room (ArShape::CTAS).
+int rows_grid(int nt) { return (nt <= 3 ? 2 : 1) * sm_count(); }
 
 constexpr int64_t COUNTER_BYTES = 4096;   // arrival counters at the front of the workspace
 constexpr int SMEM_SM = 227 * 1024;       // dynamic shared memory of the CTAs of an SM (1 KB each is reserved beside it)
@@ -40,9 +38,9 @@ int kv_map(CUtensorMap* map, const void* pool, const nvfp4_kv_cache_t& c, int bo
                          !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : seg == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-template <bool E4M3, int D, int WARPS, int NT>
+template <bool E4M3, int D, int NT>
 int launch_rows(ArParams p, const nvfp4_kv_cache_t& c, cudaStream_t stream) {
-  using S = ArShape<E4M3, D, WARPS, NT>;
+  using S = ArShape<E4M3, D, NT>;
   CUtensorMap mk, mv;
   const int box = c.page_size < S::TILE ? c.page_size : S::TILE;
   if (int rc = kv_map(&mk, c.k, c, box, S::HALVES)) return rc;
@@ -51,21 +49,19 @@ int launch_rows(ArParams p, const nvfp4_kv_cache_t& c, cudaStream_t stream) {
   const int room = (SMEM_SM - (S::CTAS - 1) * 1024) / S::CTAS - fixed;
   p.stages = std::max(2, std::min(AR_MAX_STAGES, room / S::STAGE_BYTES));
   const int smem = fixed + p.stages * S::STAGE_BYTES;
-  const int rc = ensure_smem(attention_rows_kernel<E4M3, D, WARPS, NT>, smem);
+  const int rc = ensure_smem(attention_rows_kernel<E4M3, D, NT>, smem);
   if (rc) return rc;
-  return launch_ex(attention_rows_kernel<E4M3, D, WARPS, NT>, dim3(rows_grid(NT)), dim3(S::THREADS), smem, 1, true, stream,
+  return launch_ex(attention_rows_kernel<E4M3, D, NT>, dim3(rows_grid(NT)), dim3(S::THREADS), smem, 1, true, stream,
                    mk, mv, p);
 }
 
 template <bool E4M3, int D>
 int launch_rows_nt(int nt, const ArParams& p, const nvfp4_kv_cache_t& c, cudaStream_t stream) {
   switch (nt) {
-    case 1: return launch_rows<E4M3, D, 4, 1>(p, c, stream);
-    case 2: return launch_rows<E4M3, D, 8, 2>(p, c, stream);
-    case 3: return launch_rows<E4M3, D, 8, 3>(p, c, stream);
-    default:
-      if constexpr (E4M3) return NVFP4_ERR_UNSUPPORTED_SHAPE;   // not chosen (rows_nt)
-      else return launch_rows<E4M3, D, 8, 4>(p, c, stream);
+    case 1: return launch_rows<E4M3, D, 1>(p, c, stream);
+    case 2: return launch_rows<E4M3, D, 2>(p, c, stream);
+    case 3: return launch_rows<E4M3, D, 3>(p, c, stream);
+    default: return launch_rows<E4M3, D, 4>(p, c, stream);
   }
 }
 
@@ -107,11 +103,8 @@ bool takes_tiles(int64_t rows) { return rows > 32; }
 size_t attention_workspace_bytes(int64_t batch, int64_t max_new, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
   if (batch <= 0 || max_new <= 0 || kv_heads <= 0 || q_heads <= 0 || head_dim <= 0) return 0;
   const int64_t rows = max_new * (q_heads / kv_heads);
-  int64_t parts = 0;                                                              // rows of partial sums
-  for (bool e4m3 : {false, true}) {
-    const int nt = rows_nt(rows, e4m3);
-    parts = std::max(parts, static_cast<int64_t>(rows_grid(nt)) * 2 * 8 * nt);
-  }
+  const int nt = rows_nt(rows);
+  int64_t parts = static_cast<int64_t>(rows_grid(nt)) * 2 * 8 * nt;               // rows of partial sums
   if (takes_tiles(rows)) parts = std::max(parts, static_cast<int64_t>(sm_count()) * 2 * AT_ROWS);
   return static_cast<size_t>(COUNTER_BYTES + parts * (head_dim + 2) * 4);
 }
@@ -147,7 +140,7 @@ int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, con
     return e4m3 ? launch_tiles<true, 64>(Q, q_stride, q_heads, c, p, stream)
                 : launch_tiles<false, 64>(Q, q_stride, q_heads, c, p, stream);
   }
-  const int nt = rows_nt(rows, e4m3);
+  const int nt = rows_nt(rows);
   if (4 * rows_grid(nt) > COUNTER_BYTES) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   ArParams p;
   p.s = s;

@@ -23,11 +23,10 @@
 //
 // One producer warp keeps a ring of tiles full (a page's rows are one 4-D box;
 // pages shorter than 64 tokens give several boxes), another one brings the next
-// item and its query rows as fragments. Consumer warps take 16 tokens of a tile
-// each, with an online softmax of their own, and meet at the end of an item.
-// Up to 8 rows: four of them and two CTAs per SM; more rows (up to 32): eight
-// and one CTA, so that a key or value fragment is loaded (and from E4M3
-// converted) once for all rows.
+// item and its query rows as fragments. Four consumer warps take 16 tokens of a
+// tile each, with an online softmax of their own, and meet at the end of an
+// item. A key or value fragment is loaded (and from E4M3 converted) once for all
+// rows of an item.
 //
 // Roundings. Products are exact in fp32 sums. bf16 caches: q and k as they
 // are; p is split into two bf16 halves (p = hi + lo to 2^-17), since one bf16
@@ -47,6 +46,7 @@
 namespace nvfp4 {
 namespace {
 
+constexpr int AR_WARPS = 4;                  // consumer warps, 16 tokens of a tile each
 constexpr int AR_MAX_STAGES = 8;
 constexpr int AR_ITEMS = 2;                  // items announced ahead
 constexpr float AR_SLACK = 8.0f;             // powers of two that p may exceed 1 by before sums are rescaled
@@ -72,16 +72,18 @@ struct ArParams {
   int* status;
 };
 
-// A shape of the kernel: WARPS consumer warps take 16 tokens each of a tile,
-// and NT eight-row tiles of queries.
-template <bool E4M3, int D, int WARPS, int NT>
+// A shape of the kernel for NT eight-row tiles of queries. Up to three, two CTAs
+// fit an SM's registers; four need 255 a thread (8 sequences of 22k positions,
+// E4M3, 20 rows: eight warps of one CTA 120 us, four of two CTAs 100 us; bf16,
+// 32 rows: eight warps 183 us, spilling, four warps of one CTA 150 us).
+template <bool E4M3, int D, int NT>
 struct ArShape {
-  static constexpr int TILE = 16 * WARPS;                        // tokens of a tile
+  static constexpr int TILE = 16 * AR_WARPS;                        // tokens of a tile
   static constexpr int ROWS = 8 * NT;
-  static constexpr int THREADS = (WARPS + 2) * 32;               // consumers, the producer, the item warp
-  static constexpr int CTAS = WARPS == 4 ? 2 : 1;                // per SM
+  static constexpr int THREADS = (AR_WARPS + 2) * 32;               // consumers, the producer, the item warp
+  static constexpr int CTAS = NT <= 3 ? 2 : 1;                   // per SM
   static constexpr int EXTRA = 3;                                // tiles' time that an item costs beside its tiles
-  static constexpr int BUFS = ROWS <= 16 && WARPS == 8 ? 4 : 2;  // merge buffers
+  static constexpr int BUFS = NT <= 3 ? 2 : 4;                   // merge buffers
   static constexpr bool Q_REGS = NT <= 2;                        // query fragments in registers, else read per tile
   static constexpr int ROW_BYTES = D * (E4M3 ? 1 : 2);
   static constexpr int SEG = ROW_BYTES >= 128 ? 128 : 64;        // bytes of a swizzled row of a box
@@ -93,7 +95,7 @@ struct ArShape {
   static constexpr int QFRAGS = KS * NT * 32;
   // shared memory without the ring: merge buffers, fragments, multipliers and
   // positions of the announced items, each warp's m and l, barriers
-  static constexpr int FIXED_BYTES = 1024 + BUFS * ROWS * OSTR * 4 + AR_ITEMS * (QFRAGS * 8 + ROWS * 8) + 2 * WARPS * ROWS * 4 +
+  static constexpr int FIXED_BYTES = 1024 + BUFS * ROWS * OSTR * 4 + AR_ITEMS * (QFRAGS * 8 + ROWS * 8) + 2 * AR_WARPS * ROWS * 4 +
                                      8 * (2 * AR_MAX_STAGES + 2 * AR_ITEMS) + 4 * AR_MAX_STAGES + AR_ITEMS * 64 + 64;
 };
 
@@ -232,11 +234,12 @@ NVFP4_DEV unsigned ar_seq_tiles(const ArParams& p, int n, int len) {
   return static_cast<unsigned>(max(most, 1) + S::EXTRA) * static_cast<unsigned>(blocks * p.heads);
 }
 
-template <bool E4M3, int D, int WARPS, int NT>
-__global__ void __launch_bounds__(ArShape<E4M3, D, WARPS, NT>::THREADS, ArShape<E4M3, D, WARPS, NT>::CTAS)
+template <bool E4M3, int D, int NT>
+__global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D, NT>::CTAS)
     attention_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                           const ArParams p) {
-  using S = ArShape<E4M3, D, WARPS, NT>;
+  using S = ArShape<E4M3, D, NT>;
+  constexpr int WARPS = AR_WARPS;
   constexpr int ROWS = S::ROWS, KS = S::KS, BUFS = S::BUFS, OSTR = S::OSTR, TILE = S::TILE, CONSUMERS = WARPS * 32;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
