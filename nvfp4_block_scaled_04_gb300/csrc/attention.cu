@@ -145,6 +145,7 @@ int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, con
   ArParams p;
   p.s = s;
   p.q = Q;
+  p.v = c.v;
   p.q_stride = q_stride;
   p.out = out;
   p.k_scale = c.k_scale;

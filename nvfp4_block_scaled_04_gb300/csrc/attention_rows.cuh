@@ -42,6 +42,7 @@
 #pragma once
 
 #include "kv.cuh"
+#include "tcgen05.cuh"
 
 namespace nvfp4 {
 namespace {
@@ -57,6 +58,7 @@ constexpr unsigned AR_ALL = 0xffffffffu;
 struct ArParams {
   KvSeqs s;
   const uint16_t* q;
+  const void* v;          // the value pool
   int64_t q_stride;
   uint16_t* out;
   const float* k_scale;
@@ -96,7 +98,8 @@ struct ArShape {
   // shared memory without the ring: merge buffers, fragments, multipliers and
   // positions of the announced items, each warp's m and l, barriers
   static constexpr int FIXED_BYTES = 1024 + BUFS * ROWS * OSTR * 4 + AR_ITEMS * (QFRAGS * 8 + ROWS * 8) + 2 * AR_WARPS * ROWS * 4 +
-                                     8 * (2 * AR_MAX_STAGES + 2 * AR_ITEMS) + 4 * AR_MAX_STAGES + AR_ITEMS * 64 + 64;
+                                     8 * (2 * AR_MAX_STAGES + 2 * AR_ITEMS + 1) + 4 * AR_MAX_STAGES + AR_ITEMS * 64 +
+                                     KV_BAD * static_cast<int>(sizeof(KvBad)) + 64;
 };
 
 NVFP4_DEV void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -155,6 +158,7 @@ struct ArItem {
   int key_end;            // positions at or past it hold nothing
   KvTiles tiles;
   int i0, i1;             // the piece's tiles
+  int b;                  // sequence
   unsigned first_cta, last_cta;   // CTAs that share the item
 };
 static_assert(sizeof(ArItem) <= 64, "announced items");
@@ -165,7 +169,6 @@ struct ArWalk {
   const unsigned* pre;   // tiles of the sequences before (shared memory)
   const int* rows;       // first new-token rows [batch + 1] and lengths [batch], for batches up to AR_KEPT
   unsigned per, u, end;
-  int b;                 // the sequence
 
   NVFP4_DEV bool next(ArItem& g) {
     while (u < end) {
@@ -177,7 +180,7 @@ struct ArWalk {
         else
           hi = mid;
       }
-      b = lo;
+      g.b = lo;
       g.done = 0;
       const bool kept = p.s.batch <= AR_KEPT;
       g.row0 = kept ? rows[lo] : kv_row0(p.s, lo);
@@ -253,20 +256,24 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
   ArItem* items = reinterpret_cast<ArItem*>(at);                   // [AR_ITEMS]
   at += AR_ITEMS * 64;
   uint64_t* bars = reinterpret_cast<uint64_t*>(at);
-  float* row_mult = reinterpret_cast<float*>(bars + 2 * AR_MAX_STAGES + 2 * AR_ITEMS);   // [AR_ITEMS][ROWS]
+  float* row_mult = reinterpret_cast<float*>(bars + 2 * AR_MAX_STAGES + 2 * AR_ITEMS + 1);   // [AR_ITEMS][ROWS]
   int* row_pos = reinterpret_cast<int*>(row_mult + AR_ITEMS * ROWS);                     // [AR_ITEMS][ROWS]
   float* warp_m = reinterpret_cast<float*>(row_pos + AR_ITEMS * ROWS);                   // [WARPS][ROWS]
   float* warp_l = warp_m + WARPS * ROWS;
   unsigned* stage_ok = reinterpret_cast<unsigned*>(warp_l + WARPS * ROWS);               // which boxes hold pages
   volatile int* abort_flag = reinterpret_cast<volatile int*>(stage_ok + AR_MAX_STAGES);
   unsigned* last_flag = stage_ok + AR_MAX_STAGES + 1;
-  unsigned* pre = last_flag + 1;                                                         // [batch + 1]
+  unsigned* bad_items = last_flag + 1;                                                   // items with elements taken out, a bit each
+  int* bad_count = reinterpret_cast<int*>(last_flag + 2);
+  KvBad* bad = reinterpret_cast<KvBad*>(last_flag + 3);                                  // those elements
+  unsigned* pre = reinterpret_cast<unsigned*>(bad + KV_BAD);                                                         // [batch + 1]
   int* rows = reinterpret_cast<int*>(pre + p.s.batch + 1);                               // [2 batch + 1]
   const uint32_t bar0 = smem_addr(bars);
   auto full_bar = [&](int st) { return bar0 + 8u * st; };
   auto empty_bar = [&](int st) { return bar0 + 8u * (AR_MAX_STAGES + st); };
   auto item_full = [&](int i) { return bar0 + 8u * (2 * AR_MAX_STAGES + i); };
   auto item_empty = [&](int i) { return bar0 + 8u * (2 * AR_MAX_STAGES + AR_ITEMS + i); };
+  const uint32_t check_bar = bar0 + 8u * (2 * AR_MAX_STAGES + 2 * AR_ITEMS);
   auto stage_k = [&](int st) { return base + st * S::STAGE_BYTES; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -279,7 +286,9 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
       mbar_init(item_full(i), 1);
       mbar_init(item_empty(i), WARPS);
     }
+    mbar_init(check_bar, 1);
     *abort_flag = 0;
+    *bad_items = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
@@ -319,7 +328,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
   if (per == 1 && total >= (16u + S::EXTRA) * static_cast<unsigned>(p.s.batch * p.heads)) per = 2;
   const uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * per;
   if (u0 >= total) return;
-  ArWalk<S> walk{p, pre, rows, per, static_cast<unsigned>(u0), static_cast<unsigned>(u0 + per < total ? u0 + per : total), 0};
+  ArWalk<S> walk{p, pre, rows, per, static_cast<unsigned>(u0), static_cast<unsigned>(u0 + per < total ? u0 + per : total)};
   ArItem g;
   const int box = p.page_size < TILE ? p.page_size : TILE;   // tokens of one copied box
   const int box_log2 = 31 - __clz(box), boxes = TILE >> box_log2, boxes_log2 = 31 - __clz(boxes);
@@ -327,9 +336,11 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
   if (warp == WARPS) {
     // ------------------------------------------------------------ producer
     int st = 0, par = 1, used = 0;   // ring slot, parity of its last release, slots used
+    int item = -1, checks = 0;       // items begun, tiles looked at
     bool ok = true;
     while (ok && walk.next(g)) {
-      const int32_t* row = p.s.table + static_cast<int64_t>(walk.b) * p.s.table_stride;
+      ++item;
+      const int32_t* row = p.s.table + static_cast<int64_t>(g.b) * p.s.table_stride;
       // page ids of 32 boxes at a time, one per lane
       int page = -1;
       for (int i = g.i0; i < g.i1; ++i) {
@@ -344,19 +355,57 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
         if (!ok) break;
         const int mine = __shfl_sync(AR_ALL, page, (k & 31) + (lane & (boxes - 1)));
         const unsigned there = __ballot_sync(AR_ALL, lane < boxes && mine >= 0);
+        // tokens that later rows of the item see and earlier ones do not, and the
+        // other way round at a window's edge: the tile is looked at before the
+        // consumers get it
+        const int j0 = g.tiles.tile(i) * TILE;
+        const int lo_b = max(g.p0 - p.window + 1, p.sinks), hi_b = p.window > 0 ? min(g.p1 - p.window, g.p0) : -1;
+        const bool mixed = (g.p1 > g.p0 && j0 + TILE - 1 > g.p0 && j0 <= g.p1) || (j0 <= hi_b && j0 + TILE - 1 >= lo_b);
+        const uint32_t landed = mixed ? check_bar : full_bar(st);
         if (lane == 0) {
           stage_ok[st] = there;
-          mbar_arrive_expect_tx(full_bar(st), S::STAGE_BYTES);
+          mbar_arrive_expect_tx(landed, S::STAGE_BYTES);
         }
         __syncwarp();
         if (lane < boxes) {
-          const int j = g.tiles.tile(i) * TILE + (lane << box_log2);
+          const int j = j0 + (lane << box_log2);
           // a page that is not there: a box past the pool's end, which the copy fills with zeros
           const int64_t block = mine >= 0 ? static_cast<int64_t>(mine) * p.heads + g.h : p.pages * p.heads;
           const int y = j & (p.page_size - 1);
           const uint32_t dst = stage_k(st) + (lane << box_log2) * S::ROW_BYTES;
-          tma_load_4d(dst, &map_k, 0, y, 0, static_cast<int>(block), full_bar(st));
-          tma_load_4d(dst + S::MAT_BYTES, &map_v, 0, y, 0, static_cast<int>(block), full_bar(st));
+          tma_load_4d(dst, &map_k, 0, y, 0, static_cast<int>(block), landed);
+          tma_load_4d(dst + S::MAT_BYTES, &map_v, 0, y, 0, static_cast<int>(block), landed);
+        }
+        if (mixed) {
+          // value elements that are not finite are taken out and added at the
+          // end to the rows that see them (kv.cuh)
+          ok = __all_sync(AR_ALL, mbar_wait_bounded(check_bar, checks++ & 1, abort_flag, p.status));
+          if (!ok) break;
+          constexpr int CHUNKS = S::ROW_BYTES / 16;
+#pragma unroll 2
+          for (int u = lane; u < TILE * CHUNKS; u += 32) {
+            const int row = u / CHUNKS, chunk = u % CHUNKS, jj = j0 + row;
+            if (!((jj > g.p0 && jj <= g.p1) || (jj >= lo_b && jj <= hi_b))) continue;
+            const int r = row & (box - 1), half = S::SEG == 128 ? chunk >> 3 : 0;
+            const int c16 = S::SEG == 128 ? (chunk & 7) ^ (r & 7) : chunk ^ ((r >> 1) & 3);
+            const uint32_t addr = stage_k(st) + S::MAT_BYTES + (row - r) * S::ROW_BYTES + ((half << box_log2) + r) * S::SEG + (c16 << 4);
+            const uint4 w = lds128(addr);
+            uint32_t y[4] = {w.x, w.y, w.z, w.w}, any = 0;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              // the top bit of each element whose exponent (E4M3: code) is all ones
+              const uint32_t top = E4M3 ? ((y[z] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u
+                                        : ((y[z] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+              any |= top;
+              y[z] &= ~(E4M3 ? (top >> 7) * 0xFFu : (top >> 15) * 0xFFFFu);
+            }
+            if (!any) continue;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the slot's next copy comes after
+            atomicOr(bad_items, 1u << (item & 31));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full_bar(st));
         }
         ++used;
         if (++st == stages) {
@@ -629,8 +678,10 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
           for (int hf = 0; hf < 2; ++hf) {
             // a word holds two tokens' codes of two d's: (token, d), (token, d + 1), (token + 1, d), ...
             uint32_t a[4];
-            e4m3x4_to_f16x2(__byte_perm(r[2 * hf] & keep[0], 0, 0x3120), a[0], a[1]);
-            e4m3x4_to_f16x2(__byte_perm(r[2 * hf + 1] & keep[1], 0, 0x3120), a[2], a[3]);
+            r[2 * hf] &= keep[0];
+            r[2 * hf + 1] &= keep[1];
+            e4m3x4_to_f16x2(__byte_perm(r[2 * hf], 0, 0x3120), a[0], a[1]);
+            e4m3x4_to_f16x2(__byte_perm(r[2 * hf + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[2 * m2 + hf][nt], a, hi[nt][0], hi[nt][1]);
           }
@@ -708,12 +759,51 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
       }
       ar_consumer_sync<CONSUMERS>();
     }
+    const bool any_bad = (*reinterpret_cast<volatile unsigned*>(bad_items) >> (k & 31)) & 1u;
+    if (any_bad) {
+      // the elements that were taken out of this piece's tiles, from the pool itself
+      ar_consumer_sync<CONSUMERS>();   // every thread has seen the bit
+      if (threadIdx.x == 0) {
+        *bad_count = 0;
+        atomicAnd(bad_items, ~(1u << (k & 31)));
+      }
+      ar_consumer_sync<CONSUMERS>();
+      const int lo_a = g.p0 + 1, n_a = g.p1 - g.p0;
+      const int lo_b = max(max(g.p0 - p.window + 1, p.sinks), 0);
+      const int n_b = p.window > 0 ? max(min(g.p1 - p.window, g.p0) + 1 - lo_b, 0) : 0;
+      const int32_t* row = p.s.table + static_cast<int64_t>(g.b) * p.s.table_stride;
+      for (int x = threadIdx.x; x < (n_a + n_b) * D; x += CONSUMERS) {
+        const int n = x / D, d = x % D, j = n < n_a ? lo_a + n : lo_b + (n - n_a);
+        const int t = j / TILE, i = t < g.tiles.st ? t : t - g.tiles.w0 + g.tiles.st;
+        if (j < 0 || j >= g.key_end || i < g.i0 || i >= g.i1 || (t >= g.tiles.st && t < g.tiles.w0)) continue;
+        const int page = row[j >> p.page_log2];
+        if (page < 0 || page >= p.pages) continue;
+        const int64_t at = ((static_cast<int64_t>(page) * p.heads + g.h) * p.page_size + (j & (p.page_size - 1))) * D + d;
+        const uint32_t w = E4M3 ? static_cast<const uint8_t*>(p.v)[at] : static_cast<const uint16_t*>(p.v)[at];
+        if (E4M3 ? (w & 0x7Fu) == 0x7Fu : (w & 0x7F80u) == 0x7F80u)
+          kv_remember(bad_count, bad, k, j, d, E4M3 ? NAN : bf16_bits_to_f32(w));
+      }
+      ar_consumer_sync<CONSUMERS>();
+    }
     auto merged = [&](int r, int d) {
       float4 x = *reinterpret_cast<const float4*>(merge + r * OSTR + d);
 #pragma unroll
       for (int w = 1; w < BUFS; ++w) {
         const float4 y = *reinterpret_cast<const float4*>(merge + (w * ROWS + r) * OSTR + d);
         x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+      }
+      if (any_bad) {
+        const int n_bad = *bad_count, pos = g.p0 + ((g.r0 + r) / p.group - g.r0 / p.group);
+#pragma unroll 1
+        for (int n = 0; n < min(n_bad, KV_BAD); ++n) {
+          const KvBad e = bad[n];
+          if (e.d < d || e.d >= d + 4 || !kv_sees(pos, e.j, p.window, p.sinks)) continue;
+          x.x += e.d == d ? e.v : 0.0f;
+          x.y += e.d == d + 1 ? e.v : 0.0f;
+          x.z += e.d == d + 2 ? e.v : 0.0f;
+          x.w += e.d == d + 3 ? e.v : 0.0f;
+        }
+        if (n_bad > KV_BAD) x = make_float4(NAN, NAN, NAN, NAN);   // more than are remembered
       }
       return x;
     };

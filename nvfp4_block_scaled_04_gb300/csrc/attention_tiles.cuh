@@ -21,10 +21,12 @@
 //   warp 8            producer: hands out work items, loads Q, K and V (a box
 //                     per page and 64 d's) by TMA
 //   warp 9            tensor-memory allocation; issues the MMAs
-//   warp 10           zeroes value rows no row of the item sees (they may hold
-//                     anything, and 0 * NaN is not 0)
-//   warps 10, 12..15  with E4M3 caches: a producer of its own for V, and codes,
-//                     which the producers copy in chunks of 32 rows, to f16 tiles (two
+//   warps 10, 11      zero value rows that no row of the item sees (they may
+//                     hold anything, and 0 * NaN is not 0), and take elements
+//                     that are not finite out of rows that only some rows see
+//                     (kv.cuh), which the softmax warps add at the end
+//   warps 10..15      with E4M3 caches: a producer of its own for V, a warp that
+//                     takes such elements out, and codes, which the producers copy in chunks of 32 rows, to f16 tiles (two
 //                     warps for K, two for V); the MMAs are f16 then, and the
 //                     softmax warps bring each item's Q to f16
 // S and P of a tile share 128 columns: S(j + 1) is issued after O += P(j) V(j),
@@ -59,13 +61,14 @@ constexpr int AT_CHUNKS = 4;                 // chunks of K, and of V, in flight
 constexpr int AT_ITEMS = 2;                  // items announced ahead
 constexpr int AT_OKS = 8;                    // announced page masks of tiles
 constexpr int AT_SOFTMAX_WARPS = 8;
-constexpr int AT_PROD_WARP = 8, AT_MMA_WARP = 9, AT_CLEAN_WARP = 10;
-constexpr int AT_V_PROD_WARP = 10;           // (E4M3 caches)
+constexpr int AT_PROD_WARP = 8, AT_MMA_WARP = 9, AT_CLEAN_WARP = 10;   // 10, 11: half a tile each
+constexpr int AT_V_PROD_WARP = 10, AT_CHECK_WARP = 11;   // (E4M3 caches)
 constexpr int AT_CONVERT_WARP = 12;          // 12, 13: K's codes, 14, 15: V's (E4M3 caches)
 constexpr float AT_SLACK = 8.0f;             // powers of two that p may exceed 1 by
 // slot full / empty / clean, item full / empty, q full / empty, s full, p full,
-// o full, join, q ready (each for A and B), chunk full / empty (K's, V's), drain
-constexpr int AT_BARS = 3 * AT_SLOTS + 2 * AT_ITEMS + 2 + 10 + 4 * AT_CHUNKS + 1;
+// o full, join, q ready (each for A and B), chunk full / empty (K's, V's), chunk
+// checked (V's), drain
+constexpr int AT_BARS = 3 * AT_SLOTS + 2 * AT_ITEMS + 2 + 10 + 5 * AT_CHUNKS + 1;
 
 struct AtItem {
   int done;
@@ -103,7 +106,8 @@ struct AtShape {
   // 32 output rows x 64 d's
   static constexpr int STAGING = E4M3 ? 0 : AT_SOFTMAX_WARPS * 32 * 128;
   static constexpr int DATA = (2 + K_SLOTS + V_SLOTS) * MAT_BYTES + 2 * AT_CHUNKS * CHUNK_BYTES + STAGING;
-  static constexpr int SMEM = DATA + AT_ITEMS * static_cast<int>(sizeof(AtItem)) + AT_OKS * 4 + AT_BARS * 8 + 64 + 1024;
+  static constexpr int SMEM = DATA + AT_ITEMS * static_cast<int>(sizeof(AtItem)) + AT_OKS * 4 + AT_BARS * 8 +
+                              KV_BAD * static_cast<int>(sizeof(KvBad)) + 64 + 1024;
   static constexpr int O_COL0 = 256;                       // tensor memory: S_A, S_B, O_A, O_B
   // Registers a thread, moved from the other warpgroups to the two softmax
   // ones: 384 x 168 = 64512 at launch, 256 x 208 + 128 x 80 = 63488 after; with
@@ -200,6 +204,8 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
   uint32_t* tmem_slot = oks + AT_OKS;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   unsigned* last_flag = tmem_slot + 2;   // [2]
+  int* bad_count = reinterpret_cast<int*>(tmem_slot + 4);
+  KvBad* bad = reinterpret_cast<KvBad*>(tmem_slot + 5);
   const uint32_t bar0 = smem_addr(bars);
   auto kv_full = [&](int s) { return bar0 + 8u * s; };
   auto kv_empty = [&](int s) { return bar0 + 8u * (AT_SLOTS + s); };
@@ -215,7 +221,8 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
   auto q_ready = [&](int x) { return bar0 + 8u * (B1 + 10 + x); };
   auto chunk_full = [&](int kv, int s) { return bar0 + 8u * (B1 + 12 + 2 * AT_CHUNKS * kv + s); };
   auto chunk_empty = [&](int kv, int s) { return bar0 + 8u * (B1 + 12 + 2 * AT_CHUNKS * kv + AT_CHUNKS + s); };
-  const uint32_t drain_bar = bar0 + 8u * (B1 + 12 + 4 * AT_CHUNKS);
+  auto chunk_ok = [&](int s) { return bar0 + 8u * (B1 + 12 + 4 * AT_CHUNKS + s); };
+  const uint32_t drain_bar = bar0 + 8u * (B1 + 12 + 5 * AT_CHUNKS);
   auto q_tile = [&](int x) { return base + x * S::MAT_BYTES; };
   auto slot = [&](int s) { return base + (2 + s) * S::MAT_BYTES; };
   auto chunk = [&](int kv, int s) { return base + (2 + S::K_SLOTS + S::V_SLOTS) * S::MAT_BYTES + (kv * AT_CHUNKS + s) * S::CHUNK_BYTES; };
@@ -225,11 +232,11 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
     for (int s = 0; s < AT_SLOTS; ++s) {
       mbar_init(kv_full(s), E4M3 ? 2 : 1);
       mbar_init(kv_empty(s), 1);
-      mbar_init(kv_clean(s), E4M3 ? 2 : 1);
+      mbar_init(kv_clean(s), 2);
     }
     for (int s = 0; s < AT_ITEMS; ++s) {
       mbar_init(item_full(s), 1);
-      mbar_init(item_empty(s), AT_SOFTMAX_WARPS + (E4M3 ? 5 : 2));
+      mbar_init(item_empty(s), AT_SOFTMAX_WARPS + (E4M3 ? 6 : 3));
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -242,10 +249,12 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
       for (int s = 0; s < AT_CHUNKS; ++s) {
         mbar_init(chunk_full(x, s), 1);
         mbar_init(chunk_empty(x, s), 1);
+        if (x == 0) mbar_init(chunk_ok(s), 1);
       }
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
+    *bad_count = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
@@ -450,6 +459,18 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
         ++outs;
         tc_fence_after();
       }
+      // elements that were not finite, to the rows that see them (columns c0.. of o)
+      const int n_bad = min(*reinterpret_cast<volatile int*>(bad_count), KV_BAD);
+      auto add_bad = [&](uint32_t (&o)[32], int c0) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (int n = 0; n < n_bad; ++n) {
+          const KvBad e = bad[n];
+          if (e.item != k || e.d < c0 || e.d >= c0 + 32 || !kv_sees(pos, e.j, p.window, p.sinks)) continue;
+#pragma unroll
+          for (int z = 0; z < 32; ++z)
+            o[z] = __float_as_uint(__uint_as_float(o[z]) + (e.d - c0 == z ? e.v : 0.0f));   // (no indexing: o stays in registers)
+        }
+      };
       uint16_t* dst = p.out + (static_cast<int64_t>(g.row0 + tok) * p.heads * p.group + static_cast<int64_t>(g.h) * p.group + my_head) * D;
       if (g.parts == 1) {
         const float inv = sum_l > 0.0f ? v_mult / sum_l : (sum_l == 0.0f ? 0.0f : sum_l);   // a NaN stays one
@@ -469,6 +490,10 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[0][e] = o[1][e] = 0u;
+          }
+          if (n_bad > 0) {
+            add_bad(o[0], 64 * hf);
+            add_bad(o[1], 64 * hf + 32);
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -515,6 +540,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
+          if (n_bad > 0) add_bad(o, 32 * q);
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             __stcg(reinterpret_cast<float4*>(mine) + (8 * q + e / 4) * AT_ROWS + r,
@@ -792,6 +818,47 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
       mbar_wait_bounded(drain_bar, 0, nullptr, p.status);
       __syncwarp();
     } else if constexpr (E4M3) {
+      if (warp == AT_CHECK_WARP) {
+        // ----------------------------- V's codes on their way to the converters
+        int tiles = 0;
+        bool ok = true;
+        AtItem g;
+        for (int k = 0; ok && get_item(k, g); ++k) {
+          const int p1 = g.p0 + g.n_tok - 1;
+          for (int i = g.i0; i < g.i1 && ok; ++i, ++tiles) {
+            // tile rows that later rows of the item see and earlier ones do not, and the other way round
+            const int j0 = tile_pos(g, i), a0 = g.p0 + 1 - j0, a1 = p1 + 1 - j0;
+            const int b0 = max(g.p0 - p.window + 1, p.sinks) - j0, b1 = p.window > 0 ? min(p1 - p.window, g.p0) + 1 - j0 : b0;
+            for (int cu = 0; cu < AT_CHUNKS; ++cu) {
+              if (!(ok = wait(chunk_full(1, cu), tiles & 1))) break;
+              const int c0 = cu * AT_CHUNK, c1 = c0 + AT_CHUNK;
+              if ((max(a0, c0) < min(a1, c1)) || (max(b0, c0) < min(b1, c1))) {
+#pragma unroll 2
+                for (int u = 0; u < D / 16; ++u) {
+                  const int row = c0 + (u * 32 + lane) / (D / 16), piece = lane % (D / 16);
+                  if (!((row >= a0 && row < a1) || (row >= b0 && row < b1))) continue;
+                  const uint32_t addr = chunk(1, cu) + (u * 32 + lane) * 16;
+                  const uint4 w = lds128(addr);
+                  uint32_t y[4] = {w.x, w.y, w.z, w.w}, any = 0;   // bit 7 of a NaN's byte
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) any |= (y[z] & 0x7F7F7F7Fu) + 0x01010101u;
+                  if (!(any & 0x80808080u)) continue;
+#pragma unroll
+                  for (int z = 0; z < 16; ++z) {
+                    const uint32_t sh = 8 * (z & 3);
+                    if (((y[z >> 2] >> sh) & 0x7Fu) == 0x7Fu && kv_remember(bad_count, bad, k, j0 + row, piece * 16 + z, NAN))
+                      y[z >> 2] &= ~(0xFFu << sh);
+                  }
+                  sts128(addr, y);
+                  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the chunk's next copy comes after
+                }
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(chunk_ok(cu));
+            }
+          }
+        }
+      }
       if (warp >= AT_CONVERT_WARP) {
         // ---------------- codes to f16 tiles: two warps for K, two for V, which
         // also do the clean warp's work; each takes every second chunk
@@ -810,7 +877,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
               break;
             const bool unclean = kv && at_unclean(j0, g.p0, p1, p.window, p.sinks);
             for (int cu = sub; cu < AT_CHUNKS; cu += 2) {
-              if (!(ok = wait(chunk_full(kv, cu), tiles & 1))) break;
+              if (!(ok = wait(kv ? chunk_ok(cu) : chunk_full(0, cu), tiles & 1))) break;
 #pragma unroll
               for (int u0 = 0; u0 < UNITS; u0 += BATCH) {
                 uint4 w[BATCH];
@@ -828,7 +895,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
                     const int j = j0 + row;
                     if (j > p1 || (p.window > 0 && j >= p.sinks && g.p0 - j >= p.window)) w[u] = make_uint4(0u, 0u, 0u, 0u);
                   }
-                  const uint32_t y[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+                  uint32_t y[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
                   for (int hf = 0; hf < 2; ++hf) {
                     uint32_t h[4];
@@ -847,9 +914,10 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
           }
         }
       }
-    } else if (warp == AT_CLEAN_WARP) {
+    } else if (warp == AT_CLEAN_WARP || warp == AT_CLEAN_WARP + 1) {
       // --------------------------------------- value rows that no row may take in
-      // every V tile passes here, so this warp and the rings stay in step
+      // every V tile passes here, so these warps and the rings stay in step
+      const int half = warp - AT_CLEAN_WARP;
       int tiles = 0;
       bool ok = true;
       AtItem g;
@@ -859,20 +927,38 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
           const int j0 = tile_pos(g, i), s = v_slot(tiles);
           ok = wait(kv_full(s), v_par(tiles));
           if (!ok) break;
-          const bool unclean = at_unclean(j0, g.p0, p1, p.window, p.sinks);
-          if (unclean) {
-            // rows past the item's last position, and rows between the sinks and its first window
-            auto zero = [&](int c0, int c1) {
-              for (int e = c0 * 8 + lane; e < c1 * 8; e += 32)
+          bool wrote = false;
+          // tile rows c0 .. c1 - 1, 16 bytes a step, shared by the two warps
+          auto each = [&](int c0, int c1, auto f) {
+            c0 = max(c0, 0);
+            c1 = min(c1, AT_TILE);
+            for (int e = c0 * 8 + half * 32 + lane; e < c1 * 8; e += 64)
 #pragma unroll
-                for (int hf = 0; hf < S::HALVES; ++hf)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot(s) + hf * (AT_TILE * 128) + e * 16), "r"(0)
-                               : "memory");
-            };
-            zero(max(p1 + 1 - j0, 0), AT_TILE);
-            if (p.window > 0) zero(max(p.sinks - j0, 0), min(g.p0 - p.window + 1 - j0, AT_TILE));
-          }
-          if (unclean) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              for (int hf = 0; hf < S::HALVES; ++hf) f(slot(s) + hf * (AT_TILE * 128) + e * 16, e >> 3, hf * 64 + (((e & 7) ^ (e >> 3 & 7)) << 3));
+            wrote = wrote || c0 < c1;
+          };
+          // rows past the item's last position, and rows between the sinks and its first window
+          auto zero = [&](uint32_t addr, int, int) { sts128(addr, {0u, 0u, 0u, 0u}); };
+          each(p1 + 1 - j0, AT_TILE, zero);
+          if (p.window > 0) each(p.sinks - j0, g.p0 - p.window + 1 - j0, zero);
+          // rows that later rows of the item see and earlier ones do not, and the other way round
+          auto check = [&](uint32_t addr, int row, int d0) {
+            const uint4 w = lds128(addr);
+            uint32_t y[4] = {w.x, w.y, w.z, w.w}, any = 0;   // bit 15 of a half whose exponent is all ones
+#pragma unroll
+            for (int z = 0; z < 4; ++z) any |= (y[z] & 0x7F807F80u) + 0x00800080u;
+            if (!(any & 0x80008000u)) return;
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              const uint32_t sh = 16 * (z & 1), h = (y[z >> 1] >> sh) & 0xFFFFu;
+              if ((h & 0x7F80u) == 0x7F80u && kv_remember(bad_count, bad, k, j0 + row, d0 + z, bf16_bits_to_f32(h)))
+                y[z >> 1] &= ~(0xFFFFu << sh);
+            }
+            sts128(addr, y);
+          };
+          each(g.p0 + 1 - j0, p1 + 1 - j0, check);
+          if (p.window > 0) each(max(g.p0 - p.window + 1, p.sinks) - j0, min(p1 - p.window, g.p0) + 1 - j0, check);
+          if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(kv_clean(s));
         }

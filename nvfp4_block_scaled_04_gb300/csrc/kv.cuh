@@ -52,6 +52,27 @@ NVFP4_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, i
       : "memory");
 }
 
+// Non-finite elements of value rows that some rows of a block see and others do
+// not. As an operand they would reach the others too (0 * inf is NaN), so the
+// kernels put zeros in their place and add them, at the end, to the rows that
+// see them. A CTA remembers KV_BAD of them; further ones stay where they are.
+constexpr int KV_BAD = 16;
+struct KvBad {
+  int item, j, d;      // item of the CTA, position, element
+  float v;
+};
+// Remembers one; false if there is no room left.
+NVFP4_DEV bool kv_remember(int* count, KvBad* list, int item, int j, int d, float v) {
+  const int n = atomicAdd(count, 1);
+  if (n < KV_BAD) list[n] = {item, j, d, v};
+  return n < KV_BAD;
+}
+
+// Whether a row at position pos sees position j.
+NVFP4_DEV bool kv_sees(int pos, int j, int window, int sinks) {
+  return j <= pos && (window <= 0 || pos - j < window || j < sinks);
+}
+
 // 2^x (2 ulp), zero for -inf.
 NVFP4_DEV float exp2_approx(float x) {
   float y;

@@ -323,3 +323,46 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         m.kv_fork(cache, table, lens, lens, lens[:1], lens[:1])   # one count for each page
     assert m.read_device_status() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("news,past,window,sinks", [([5], [300], 0, 0), ([4, 3], [40, 200], 50, 3), ([90, 130], [0, 500], 0, 0),
+                                                    ([200, 64], [300, 77], 100, 5), ([40], [9000], 0, 0)])
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(kv, dim, news, past, window, sinks):
+    """Infinite and NaN elements in new tokens' values (and in one at a window's edge): rows that do not see the
+    token are as if it were finite, rows that see it carry the element's own output column away, others stay."""
+    m = nv()
+    lens = [a + b for a, b in zip(news, past)]
+    c = Cache(lens, 2, 16, dim, kv, seed=30 + dim)
+    heads, group = 2, 4
+    q = queries(sum(news), heads * group, dim, 9)
+    ref, size = attention(c, q, news, window, sinks)
+    places = []   # (sequence, position, kv head, element)
+    for b, (n, length) in enumerate(zip(news, lens)):
+        for x, d in ((length - 1, 3), (length - n // 2, dim - 1), (max(0, length - n + 1 - max(window, 1) // 2), 17)):
+            places.append((b, x, b % heads, d))
+    for i, (b, x, h, d) in enumerate(places):
+        page, row = int(c.table[b, x // 16]), x % 16
+        if kv == "e4m3":
+            c.v.view(torch.uint8)[page, h, row, d] = 0x7F if i % 2 else 0xFF
+        else:
+            c.v[page, h, row, d] = float(("inf", "-inf", "nan")[i % 3])
+    got = m.paged_attention(q.to(DEV), device_cache(m, c), c.table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                            start=offsets(news).to(DEV), max_new=max(news), window=window, sinks=sinks)
+    assert m.read_device_status() == 0
+    got = got.float().cpu().double().numpy()
+    hit = np.zeros(got.shape, dtype=bool)
+    t = 0
+    for b, n in enumerate(news):
+        for i in range(n):
+            pos = lens[b] - n + i
+            for bb, x, h, d in places:
+                if bb == b and x <= pos and (not window or pos - x < window or x < sinks):
+                    hit[t + i, h * group:(h + 1) * group, d] = True
+        t += n
+    assert hit.any() and not hit.all()
+    assert not np.isfinite(got[hit]).any()
+    limit = bound(ref, size, max(news) * group, kv)
+    # the finite elements of these rows count as they are: the reference has the same ones
+    assert (np.abs(got - ref)[~hit] <= limit[~hit]).all()
