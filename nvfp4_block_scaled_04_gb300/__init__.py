@@ -358,33 +358,36 @@ def verify_accept(h: torch.Tensor, w: QTensor, draft_ids: torch.Tensor, workspac
     return tokens, n_acc
 
 
-@dataclass(frozen=True)
 class KVCache:
     """One layer's paged key-value cache: pools k, v [pages][heads][page_size]
     [head_dim], bf16, or float8_e4m3fn with a scale for each kv head
-    (value = code * scale). Page sizes 16, 32, 64, 128; head_dim 64 or 128."""
-    k: torch.Tensor
-    v: torch.Tensor
-    k_scale: torch.Tensor | None = None
-    v_scale: torch.Tensor | None = None
+    (value = code * scale). Page sizes 16, 32, 64, 128; head_dim 64 or 128.
+    (A plain class, its tensors fixed: engines make one per layer and step.)"""
+    __slots__ = ("_tensors", "_c")
 
-    def __post_init__(self):
-        k, v = self.k, self.v
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
         shape, dtype = k.shape, k.dtype
         if len(shape) != 4 or shape != v.shape or dtype != v.dtype or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("KVCache: k and v are contiguous pools [pages][heads][page_size][head_dim] of one type")
-        _require_cuda(k, v)
+        if not (k.is_cuda and v.is_cuda):
+            _require_cuda(k, v)
+        self._tensors = (k, v, k_scale, v_scale)
         if dtype == torch.bfloat16:
-            object.__setattr__(self, "_c", CKVCache(k.data_ptr(), v.data_ptr(), None, None, *shape, DTYPE_BF16))
+            self._c = CKVCache(k.data_ptr(), v.data_ptr(), None, None, *shape, DTYPE_BF16)
             return
         if dtype != torch.float8_e4m3fn:
             raise ValueError("KVCache: pools are bfloat16 or float8_e4m3fn")
-        for t in (self.k_scale, self.v_scale):
+        for t in (k_scale, v_scale):
             if t is None or t.dtype != torch.float32 or t.shape != shape[1:2] or not t.is_contiguous():
                 raise ValueError("KVCache: an E4M3 cache needs fp32 scales [heads]")
-        _require_cuda(self.k_scale, self.v_scale)
-        object.__setattr__(self, "_c", CKVCache(k.data_ptr(), v.data_ptr(), self.k_scale.data_ptr(),
-                                                self.v_scale.data_ptr(), *shape, DTYPE_E4M3))
+        _require_cuda(k_scale, v_scale)
+        self._c = CKVCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *shape, DTYPE_E4M3)
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
     def c(self) -> CKVCache:
         return self._c
