@@ -35,6 +35,11 @@
 // power of two into f16 (exact for elements above amax 2^-29), p is one f16
 // (2^-12, a sixteenth of the output's rounding).
 //
+// Measured, 8 kv heads, D = 128: 64 sequences of 9k..22k positions, bf16, 578 us
+// (the copy rate); 8 sequences of 517..24k, 20 rows, E4M3, 63.0 us against 29.7
+// for the bytes (bound by instruction latency); one sequence of 2k positions,
+// 8.4 us on the device.
+//
 // Masked places: scores are replaced, not added to; a token no row of the item
 // sees has its value row replaced by zeros (stale page contents may be NaN),
 // and pages that are not there are filled with zeros by the copy engine

@@ -21,13 +21,13 @@
 //   warp 8            producer: hands out work items, loads Q, K and V (a box
 //                     per page and 64 d's) by TMA
 //   warp 9            tensor-memory allocation; issues the MMAs
-//   warps 10, 11      zero value rows that no row of the item sees (they may
-//                     hold anything, and 0 * NaN is not 0), and take elements
-//                     that are not finite out of rows that only some rows see
-//                     (kv.cuh), which the softmax warps add at the end
-//   warps 10..15      with E4M3 caches: a producer of its own for V, a warp that
-//                     takes such elements out, and codes, which the producers copy in chunks of 32 rows, to f16 tiles (two
-//                     warps for K, two for V); the MMAs are f16 then, and the
+//   warps 10, 11      (bf16 caches) zero value rows that no row of the item sees
+//                     (they may hold anything, and 0 * NaN is not 0), and take
+//                     elements that are not finite out of rows that only some
+//                     rows see (kv.cuh); the softmax warps add them at the end
+//   warps 10..15      (E4M3 caches) 10 loads V, 11 takes such elements out, 12, 13
+//                     turn K's codes and 14, 15 V's, copied in chunks of 32
+//                     rows, into f16 tiles; the MMAs are f16 then, and the
 //                     softmax warps bring each item's Q to f16
 // S and P of a tile share 128 columns: S(j + 1) is issued after O += P(j) V(j),
 // and the tensor cores run one thread's MMAs in order. For the same reason a
@@ -42,6 +42,13 @@
 // Few items (a short chunk on a long context) are split over the positions:
 // each part leaves (m, l, o) in the workspace and the last part of a row tile
 // to arrive joins them in order.
+//
+// Measured, bf16, D = 128: 1500 and 2048 new tokens of two sequences, 32 heads on
+// 8, on up to 14k positions, 594-600 us (76% of the bf16 burst rate that a large
+// matrix product reaches; under the power cap); an 8k prompt, 40 heads on 8, with
+// a window of 1024, 182-196 us (84 us of MMAs, 111 in whole tiles). Two row tiles rather than
+// one: a tile's exponentials hide behind the other's MMAs. A warpgroup of its own
+// for the output was slower (2k on 8k: 188 -> 211 us).
 //
 // Every wait is bounded; one that gives up raises the CTA's abort flag, every
 // role leaves its loop, and nothing more is written.
