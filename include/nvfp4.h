@@ -377,7 +377,9 @@ typedef struct nvfp4_kv_cache {
  *   lens     device int32 [batch]: positions in use, the call's new ones among them
  *   start    device int32 [batch + 1]: the new tokens of sequence b are rows
  *            start[b] .. start[b + 1] - 1 of the call's token arrays, and its
- *            last positions; NULL: max_new tokens for every sequence
+ *            last positions; NULL: max_new tokens for every sequence. Offsets do
+ *            not fall and lie in [0, tokens]; where they fall, rows may be left
+ *            out (attention then puts NVFP4_ERR_INVALID_ARG in the status word)
  *   batch    1 .. 4096
  *   max_new  >= 1: the most new tokens of a sequence. It chooses the kernel;
  *            with `start`, a sequence that has more is still computed. */

@@ -65,7 +65,8 @@ int launch_rows_nt(int nt, const ArParams& p, const nvfp4_kv_cache_t& c, cudaStr
   }
 }
 
-// Blocks of rows (256 at most, whole tokens) times kv heads of a call of the tile kernel, at most.
+// Blocks of rows (256 at most, whole tokens) times kv heads of a call of the tile kernel, at most
+// (where `start` does not fall: the sequences' rows add up to `tokens` or fewer).
 int64_t tiles_items(int64_t tokens, int64_t batch, int64_t heads, int group) {
   const int64_t block = 2 * (AT_ROWS / group);
   return heads * ((tokens + batch * (block - 1)) / block);
@@ -88,10 +89,10 @@ int launch_tiles(const uint16_t* Q, int64_t q_stride, int q_heads, const nvfp4_k
   const int ctas = sm_count();
   // fewer items than half the SMs: each is split over its positions
   p.parts = items < ctas ? static_cast<int>(ctas / items) : 1;
-  const int64_t units = items * p.parts;
+  p.units = items * p.parts;
   const int rc = ensure_smem(attention_tiles_kernel<E4M3, D>, AtShape<E4M3, D>::SMEM);
   if (rc) return rc;
-  return launch_ex(attention_tiles_kernel<E4M3, D>, dim3(static_cast<unsigned>(units < ctas ? units : ctas)), dim3(AtShape<E4M3, D>::THREADS),
+  return launch_ex(attention_tiles_kernel<E4M3, D>, dim3(static_cast<unsigned>(p.units < ctas ? p.units : ctas)), dim3(AtShape<E4M3, D>::THREADS),
                    AtShape<E4M3, D>::SMEM, 1, true, stream, mq, mk, mv, p);
 }
 

@@ -96,6 +96,7 @@ struct AtParams {
   int window, sinks;
   float scale;           // softmax scale * log2 e, > 0
   int parts;             // parts of an item (1: no split)
+  int64_t units;         // work items that the launch and the workspace were sized for
   const float* k_scale;  // E4M3 only
   const float* v_scale;
   unsigned* arrived;     // [items][2], zero between calls (split only)
@@ -661,6 +662,11 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
             row = p.s.table + static_cast<int64_t>(b0 + src) * p.s.table_stride;
           }
           run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (!g.done && w >= p.units) {
+          // more blocks than `tokens` rows can hold: offsets that fall. The workspace has no room for them.
+          if (lane == 0) atomicExch(p.status, NVFP4_ERR_INVALID_ARG);
+          g.done = 1;
         }
         if (!g.done && g.part >= g.parts) continue;   // fewer parts than the launch has room for
         ++k;

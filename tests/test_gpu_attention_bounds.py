@@ -1,0 +1,39 @@
+"""What a call of the attention kernels may touch when its device-side arrays
+hold what they should not."""
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_common import DEV, nv
+from tests.kv_oracle import Cache, attention
+from tests.test_gpu_attention import bound, device_cache, offsets, queries
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_offsets_that_fall_stay_inside_the_workspace(kv):
+    """start = 0, 1000, 0, 1000, ...: the sequences' rows add up to 16 times the rows that q has. The split prompt
+    kernel's partial sums must stay inside the workspace, and the status word says that something is wrong."""
+    m = nv()
+    batch, tokens = 32, 1000
+    c = Cache([1200], 1, 64, 64, kv, seed=1)
+    table = c.table.to(DEV).expand(batch, -1).contiguous()
+    lens = torch.full((batch,), 1200, dtype=torch.int32, device=DEV)
+    start = torch.tensor([0, tokens] * (batch // 2) + [0], dtype=torch.int32, device=DEV)
+    need = m.workspace_size(m.OP_PAGED_ATTENTION, batch, tokens, 1, 1, 64)
+    room = torch.full((need + (64 << 20),), 0x5A, dtype=torch.uint8, device=DEV)
+    room[:4096] = 0
+    q = queries(tokens, 1, 64, 2)
+    out = torch.zeros(tokens, 1, 64, dtype=torch.bfloat16, device=DEV)
+    m.paged_attention(q.to(DEV), device_cache(m, c), table, lens, start=start, max_new=tokens, out=out, workspace=room[:need])
+    assert m.read_device_status() == m.ERR_INVALID_ARG
+    assert (room[need:] == 0x5A).all()
+    assert torch.isfinite(out.float()).all()
+    # the counters are back at zero, and the workspace serves an orderly call afterwards
+    assert not room[:4096].any()
+    ref, size = attention(c, q, [tokens])
+    got = m.paged_attention(q.to(DEV), device_cache(m, c), table[:1], lens[:1], start=offsets([tokens]).to(DEV), max_new=tokens,
+                            workspace=room[:need]).float().cpu().double().numpy()
+    assert m.read_device_status() == 0
+    assert (np.abs(got - ref) <= bound(ref, size, tokens, kv)).all()
