@@ -103,7 +103,7 @@ struct ArShape {
   // shared memory without the ring: merge buffers, fragments, multipliers and
   // positions of the announced items, each warp's m and l, barriers
   static constexpr int FIXED_BYTES = 1024 + BUFS * ROWS * OSTR * 4 + AR_ITEMS * (QFRAGS * 8 + ROWS * 8) + 2 * AR_WARPS * ROWS * 4 +
-                                     8 * (2 * AR_MAX_STAGES + 2 * AR_ITEMS + 1) + 4 * AR_MAX_STAGES + AR_ITEMS * 64 +
+                                     8 * (2 * AR_MAX_STAGES + 2 * AR_ITEMS + 1) + 8 * AR_MAX_STAGES + AR_ITEMS * 64 +
                                      KV_BAD * static_cast<int>(sizeof(KvBad)) + 64;
 };
 
@@ -266,11 +266,11 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
   float* warp_m = reinterpret_cast<float*>(row_pos + AR_ITEMS * ROWS);                   // [WARPS][ROWS]
   float* warp_l = warp_m + WARPS * ROWS;
   unsigned* stage_ok = reinterpret_cast<unsigned*>(warp_l + WARPS * ROWS);               // which boxes hold pages
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(stage_ok + AR_MAX_STAGES);
-  unsigned* last_flag = stage_ok + AR_MAX_STAGES + 1;
-  unsigned* bad_items = last_flag + 1;                                                   // items with elements taken out, a bit each
-  int* bad_count = reinterpret_cast<int*>(last_flag + 2);
-  KvBad* bad = reinterpret_cast<KvBad*>(last_flag + 3);                                  // those elements
+  unsigned* stage_cut = stage_ok + AR_MAX_STAGES;                                        // 1: elements were taken out of the slot's V
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(stage_cut + AR_MAX_STAGES);
+  unsigned* last_flag = stage_cut + AR_MAX_STAGES + 1;
+  int* bad_count = reinterpret_cast<int*>(last_flag + 1);
+  KvBad* bad = reinterpret_cast<KvBad*>(last_flag + 2);                                  // those elements
   unsigned* pre = reinterpret_cast<unsigned*>(bad + KV_BAD);                                                         // [batch + 1]
   int* rows = reinterpret_cast<int*>(pre + p.s.batch + 1);                               // [2 batch + 1]
   const uint32_t bar0 = smem_addr(bars);
@@ -293,7 +293,6 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
     }
     mbar_init(check_bar, 1);
     *abort_flag = 0;
-    *bad_items = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
@@ -341,10 +340,9 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
   if (warp == WARPS) {
     // ------------------------------------------------------------ producer
     int st = 0, par = 1, used = 0;   // ring slot, parity of its last release, slots used
-    int item = -1, checks = 0;       // items begun, tiles looked at
+    int checks = 0;                  // tiles looked at
     bool ok = true;
     while (ok && walk.next(g)) {
-      ++item;
       const int32_t* row = p.s.table + static_cast<int64_t>(g.b) * p.s.table_stride;
       // page ids of 32 boxes at a time, one per lane
       int page = -1;
@@ -369,6 +367,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
         const uint32_t landed = mixed ? check_bar : full_bar(st);
         if (lane == 0) {
           stage_ok[st] = there;
+          stage_cut[st] = 0;
           mbar_arrive_expect_tx(landed, S::STAGE_BYTES);
         }
         __syncwarp();
@@ -387,6 +386,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
           ok = __all_sync(AR_ALL, mbar_wait_bounded(check_bar, checks++ & 1, abort_flag, p.status));
           if (!ok) break;
           constexpr int CHUNKS = S::ROW_BYTES / 16;
+          bool cut = false;
 #pragma unroll 2
           for (int u = lane; u < TILE * CHUNKS; u += 32) {
             const int row = u / CHUNKS, chunk = u % CHUNKS, jj = j0 + row;
@@ -407,10 +407,13 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
             if (!any) continue;
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the slot's next copy comes after
-            atomicOr(bad_items, 1u << (item & 31));
+            cut = true;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full_bar(st));
+          cut = __any_sync(AR_ALL, cut);
+          if (lane == 0) {
+            stage_cut[st] = cut;   // read with the slot, before the slot is released
+            mbar_arrive(full_bar(st));
+          }
         }
         ++used;
         if (++st == stages) {
@@ -562,6 +565,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[mt][nt][c] = 0.0f;
 
+    unsigned any_bad = 0;   // elements were taken out of the piece's tiles: every warp reads every tile's word, so all agree
     for (int i = g.i0; i < g.i1; ++i) {
       if (ok) ok = __all_sync(AR_ALL, mbar_wait_bounded(full_bar(st), par, abort_flag, p.status));
       if (!ok) break;
@@ -611,7 +615,8 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[nt][c] = (s[nt][c] + s2[nt][c]) * mult[nt][c & 1];
-      if (!all_seen) {
+      if (!all_seen) {   // (a tile that the producer looked at is one of these)
+        any_bad |= stage_cut[st];
         auto none_sees = [&](int j) {
           return !box_ok || j > g.p1 || j >= g.key_end || (p.window > 0 && j >= p.sinks && g.p0 - j >= p.window);
         };
@@ -730,7 +735,8 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
           warp_l[warp * ROWS + nt * 8 + 2 * quad + c] = l[nt][c];
         }
       }
-    ar_consumer_sync<CONSUMERS>();
+    ok = ar_all<CONSUMERS>(ok);
+    if (!ok) continue;   // a wait gave up: nothing more is written
     auto row_max = [&](int r) {
       float x = warp_m[r];
 #pragma unroll
@@ -764,14 +770,9 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
       }
       ar_consumer_sync<CONSUMERS>();
     }
-    const bool any_bad = (*reinterpret_cast<volatile unsigned*>(bad_items) >> (k & 31)) & 1u;
     if (any_bad) {
       // the elements that were taken out of this piece's tiles, from the pool itself
-      ar_consumer_sync<CONSUMERS>();   // every thread has seen the bit
-      if (threadIdx.x == 0) {
-        *bad_count = 0;
-        atomicAnd(bad_items, ~(1u << (k & 31)));
-      }
+      if (threadIdx.x == 0) *bad_count = 0;   // (the last item's readers have met since)
       ar_consumer_sync<CONSUMERS>();
       const int lo_a = g.p0 + 1, n_a = g.p1 - g.p0;
       const int lo_b = max(max(g.p0 - p.window + 1, p.sinks), 0);
@@ -827,8 +828,6 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
       uint16_t* dst = p.out + (static_cast<int64_t>(g.row0 + i) * p.heads * p.group + head) * D + d;
       *reinterpret_cast<uint2*>(dst) = make_uint2(f32x2_to_bf16x2(x.x * inv, x.y * inv), f32x2_to_bf16x2(x.z * inv, x.w * inv));
     };
-    ok = ar_all<CONSUMERS>(ok);
-    if (!ok) continue;   // a wait gave up: nothing more is written
     const unsigned first_cta = g.first_cta, last_cta = g.last_cta;
     if (first_cta == last_cta) {
       for (int x = threadIdx.x; x < g.n_rows * (D / 4); x += CONSUMERS) {

@@ -1,0 +1,73 @@
+"""Value elements that are not finite, in every place that a cache's user can
+have them: rows that do not see their token are as if they were finite, in rows
+that see it their own output columns are not finite and the others stay. The
+reference counts such an element as zero, so the bounds are those of
+test_gpu_attention."""
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_common import DEV, nv
+from tests.kv_oracle import Cache, attention
+from tests.test_gpu_attention import bound, device_cache, offsets, queries
+
+pytestmark = pytest.mark.gpu
+
+
+def plant(c, places):
+    """Elements (sequence, position, kv head, element) of the values; element None: all of the token's."""
+    for i, (b, x, h, d) in enumerate(places):
+        page, row = int(c.table[b, x // c.page]), x % c.page
+        d = slice(None) if d is None else d
+        if c.kv == "e4m3":
+            c.v.view(torch.uint8)[page, h, row, d] = 0x7F if i % 2 else 0xFF
+        else:
+            c.v[page, h, row, d] = float(("nan", "inf", "-inf")[i % 3])
+
+
+def seen_by(c, news, group, window, sinks, places):
+    """Which outputs [T][q_heads][dim] see one of the places."""
+    hit = np.zeros((sum(news), c.heads * group, c.dim), dtype=bool)
+    first = np.concatenate([[0], np.cumsum(news)])
+    for b, x, h, d in places:
+        pos = np.arange(c.lens[b] - news[b], c.lens[b])
+        sees = (x <= pos) & ((pos - x < window) | (x < sinks) if window else True)
+        rows = first[b] + np.flatnonzero(sees)
+        hit[rows, h * group:(h + 1) * group, slice(None) if d is None else d] = True
+    return hit
+
+
+def check(c, news, group, places, window=0, sinks=0, uniform=False, times=1, seed=9):
+    m = nv()
+    q = queries(sum(news), c.heads * group, c.dim, seed)
+    plant(c, places)
+    ref, size = attention(c, q, news, window, sinks)
+    hit = seen_by(c, news, group, window, sinks, places)
+    limit = bound(ref, size, max(news) * group, c.kv)
+    lens = torch.tensor(c.lens, dtype=torch.int32, device=DEV)
+    args = dict(start=None if uniform else offsets(news).to(DEV), max_new=max(news), window=window, sinks=sinks,
+                workspace=m.attention_workspace(len(news), max(news), c.heads * group, c.heads, c.dim))
+    dc, table, qd = device_cache(m, c), c.table.to(DEV), q.to(DEV)
+    for _ in range(times):
+        got = m.paged_attention(qd, dc, table, lens, **args)
+        assert m.read_device_status() == 0
+        got = got.float().cpu().double().numpy()
+        assert not np.isfinite(got[hit]).any()
+        assert (np.abs(got - ref)[~hit] <= limit[~hit]).all()
+    return hit
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_between_many_idle_sequences(kv):
+    """A padded verify batch: 64 live sequences among 2048, the others of length 0. The copies of a live item are
+    asked for many idle items before its turn; what was taken out of its values has to come back to it."""
+    batch, heads, group, new, dim = 2048, 8, 2, 3, 64
+    g = np.random.default_rng(3)
+    live = sorted(int(b) for b in g.choice(batch, 64, replace=False))
+    lens = [0] * batch
+    for b in live:
+        lens[b] = int(g.integers(4, 200))
+    c = Cache(lens, heads, 16, dim, kv, seed=5)
+    places = [(b, lens[b] - 1 - i % 2, h, (7 * b + h) % dim) for i, b in enumerate(live) for h in range(0, heads, 1 + i % 3)]
+    hit = check(c, [new] * batch, group, places, uniform=True, times=5)
+    assert hit.any() and not hit.all()
