@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     *bad_count = 0;
+    for (int n = 0; n < KV_BAD; ++n) bad[n].item = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
@@ -472,8 +473,9 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
       auto add_bad = [&](uint32_t (&o)[32], int c0) __attribute__((always_inline)) {
 #pragma unroll 1
         for (int n = 0; n < n_bad; ++n) {
+          if (*reinterpret_cast<volatile int*>(&bad[n].item) != k) continue;
           const KvBad e = bad[n];
-          if (e.item != k || e.d < c0 || e.d >= c0 + 32 || !kv_sees(pos, e.j, p.window, p.sinks)) continue;
+          if (e.d < c0 || e.d >= c0 + 32 || !kv_sees(pos, e.j, p.window, p.sinks)) continue;
 #pragma unroll
           for (int z = 0; z < 32; ++z)
             o[z] = __float_as_uint(__uint_as_float(o[z]) + (e.d - c0 == z ? e.v : 0.0f));   // (no indexing: o stays in registers)

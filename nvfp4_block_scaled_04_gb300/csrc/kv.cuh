@@ -61,11 +61,18 @@ struct KvBad {
   int item, j, d;      // item of the CTA, position, element
   float v;
 };
-// Remembers one; false if there is no room left.
+// Remembers one; false if there is no room left. Other threads may be reading
+// the list for other items meanwhile: `item`, which no reader looks for yet, is
+// written last (it is -1 in entries that were never written).
 NVFP4_DEV bool kv_remember(int* count, KvBad* list, int item, int j, int d, float v) {
   const int n = atomicAdd(count, 1);
-  if (n < KV_BAD) list[n] = {item, j, d, v};
-  return n < KV_BAD;
+  if (n >= KV_BAD) return false;
+  list[n].j = j;
+  list[n].d = d;
+  list[n].v = v;
+  __threadfence_block();
+  *reinterpret_cast<volatile int*>(&list[n].item) = item;
+  return true;
 }
 
 // Whether a row at position pos sees position j.

@@ -71,3 +71,14 @@ def test_between_many_idle_sequences(kv):
     places = [(b, lens[b] - 1 - i % 2, h, (7 * b + h) % dim) for i, b in enumerate(live) for h in range(0, heads, 1 + i % 3)]
     hit = check(c, [new] * batch, group, places, uniform=True, times=5)
     assert hit.any() and not hit.all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_items_one_after_another(kv):
+    """More items than SMs, so that one item's values are looked at while the last one's outputs are written, with
+    an element in every sixteenth: no output may hold what another item remembers."""
+    batch, heads, group, new, dim = 60, 8, 4, 20, 64
+    c = Cache([new + 3 * b for b in range(batch)], heads, 16, dim, kv, seed=6)
+    places = [(b, c.lens[b] - 1 - b % 5, (5 * b) % heads, (11 * b) % dim) for b in range(batch) if b % 2 == 0]
+    hit = check(c, [new] * batch, group, places, uniform=True, times=10)
+    assert hit.any() and not hit.all()
