@@ -103,8 +103,7 @@ struct ArShape {
   // shared memory without the ring: merge buffers, fragments, multipliers and
   // positions of the announced items, each warp's m and l, barriers
   static constexpr int FIXED_BYTES = 1024 + BUFS * ROWS * OSTR * 4 + AR_ITEMS * (QFRAGS * 8 + ROWS * 8) + 2 * AR_WARPS * ROWS * 4 +
-                                     8 * (2 * AR_MAX_STAGES + 2 * AR_ITEMS + 1) + 8 * AR_MAX_STAGES + AR_ITEMS * 64 +
-                                     KV_BAD * static_cast<int>(sizeof(KvBad)) + 64;
+                                     8 * (2 * AR_MAX_STAGES + 2 * AR_ITEMS + 1) + 12 * AR_MAX_STAGES + AR_ITEMS * 64 + 64;
 };
 
 NVFP4_DEV void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -266,12 +265,10 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
   float* warp_m = reinterpret_cast<float*>(row_pos + AR_ITEMS * ROWS);                   // [WARPS][ROWS]
   float* warp_l = warp_m + WARPS * ROWS;
   unsigned* stage_ok = reinterpret_cast<unsigned*>(warp_l + WARPS * ROWS);               // which boxes hold pages
-  unsigned* stage_cut = stage_ok + AR_MAX_STAGES;                                        // 1: elements were taken out of the slot's V
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(stage_cut + AR_MAX_STAGES);
-  unsigned* last_flag = stage_cut + AR_MAX_STAGES + 1;
-  int* bad_count = reinterpret_cast<int*>(last_flag + 1);
-  KvBad* bad = reinterpret_cast<KvBad*>(last_flag + 2);                                  // those elements
-  unsigned* pre = reinterpret_cast<unsigned*>(bad + KV_BAD);                                                         // [batch + 1]
+  unsigned* stage_cut = stage_ok + AR_MAX_STAGES;                                        // [2]: tokens that elements were taken out of
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(stage_cut + 2 * AR_MAX_STAGES);
+  unsigned* last_flag = stage_cut + 2 * AR_MAX_STAGES + 1;
+  unsigned* pre = last_flag + 1;                                                         // [batch + 1]
   int* rows = reinterpret_cast<int*>(pre + p.s.batch + 1);                               // [2 batch + 1]
   const uint32_t bar0 = smem_addr(bars);
   auto full_bar = [&](int st) { return bar0 + 8u * st; };
@@ -367,7 +364,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
         const uint32_t landed = mixed ? check_bar : full_bar(st);
         if (lane == 0) {
           stage_ok[st] = there;
-          stage_cut[st] = 0;
+          stage_cut[2 * st] = stage_cut[2 * st + 1] = 0;
           mbar_arrive_expect_tx(landed, S::STAGE_BYTES);
         }
         __syncwarp();
@@ -382,11 +379,12 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
         }
         if (mixed) {
           // value elements that are not finite are taken out and added at the
-          // end to the rows that see them (kv.cuh)
+          // end to the rows that see them (kv.cuh): a bit for each of the up to
+          // 31 tokens past p0, and of those from lo_b on, that had any
           ok = __all_sync(AR_ALL, mbar_wait_bounded(check_bar, checks++ & 1, abort_flag, p.status));
           if (!ok) break;
           constexpr int CHUNKS = S::ROW_BYTES / 16;
-          bool cut = false;
+          unsigned cut_a = 0, cut_b = 0;
 #pragma unroll 2
           for (int u = lane; u < TILE * CHUNKS; u += 32) {
             const int row = u / CHUNKS, chunk = u % CHUNKS, jj = j0 + row;
@@ -407,11 +405,16 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
             if (!any) continue;
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the slot's next copy comes after
-            cut = true;
+            if (jj > g.p0)
+              cut_a |= 1u << (jj - g.p0 - 1);
+            else
+              cut_b |= 1u << (jj - lo_b);
           }
-          cut = __any_sync(AR_ALL, cut);
+          cut_a = __reduce_or_sync(AR_ALL, cut_a);
+          cut_b = __reduce_or_sync(AR_ALL, cut_b);
           if (lane == 0) {
-            stage_cut[st] = cut;   // read with the slot, before the slot is released
+            stage_cut[2 * st] = cut_a;   // read with the slot, before the slot is released
+            stage_cut[2 * st + 1] = cut_b;
             mbar_arrive(full_bar(st));
           }
         }
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[mt][nt][c] = 0.0f;
 
-    unsigned any_bad = 0;   // elements were taken out of the piece's tiles: every warp reads every tile's word, so all agree
+    unsigned cut_a = 0, cut_b = 0;   // tokens that elements were taken out of: every warp reads every tile's words, so all agree
     for (int i = g.i0; i < g.i1; ++i) {
       if (ok) ok = __all_sync(AR_ALL, mbar_wait_bounded(full_bar(st), par, abort_flag, p.status));
       if (!ok) break;
@@ -616,7 +619,8 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[nt][c] = (s[nt][c] + s2[nt][c]) * mult[nt][c & 1];
       if (!all_seen) {   // (a tile that the producer looked at is one of these)
-        any_bad |= stage_cut[st];
+        cut_a |= stage_cut[2 * st];
+        cut_b |= stage_cut[2 * st + 1];
         auto none_sees = [&](int j) {
           return !box_ok || j > g.p1 || j >= g.key_end || (p.window > 0 && j >= p.sinks && g.p0 - j >= p.window);
         };
@@ -770,27 +774,6 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
       }
       ar_consumer_sync<CONSUMERS>();
     }
-    if (any_bad) {
-      // the elements that were taken out of this piece's tiles, from the pool itself
-      if (threadIdx.x == 0) *bad_count = 0;   // (the last item's readers have met since)
-      ar_consumer_sync<CONSUMERS>();
-      const int lo_a = g.p0 + 1, n_a = g.p1 - g.p0;
-      const int lo_b = max(max(g.p0 - p.window + 1, p.sinks), 0);
-      const int n_b = p.window > 0 ? max(min(g.p1 - p.window, g.p0) + 1 - lo_b, 0) : 0;
-      const int32_t* row = p.s.table + static_cast<int64_t>(g.b) * p.s.table_stride;
-      for (int x = threadIdx.x; x < (n_a + n_b) * D; x += CONSUMERS) {
-        const int n = x / D, d = x % D, j = n < n_a ? lo_a + n : lo_b + (n - n_a);
-        const int t = j / TILE, i = t < g.tiles.st ? t : t - g.tiles.w0 + g.tiles.st;
-        if (j < 0 || j >= g.key_end || i < g.i0 || i >= g.i1 || (t >= g.tiles.st && t < g.tiles.w0)) continue;
-        const int page = row[j >> p.page_log2];
-        if (page < 0 || page >= p.pages) continue;
-        const int64_t at = ((static_cast<int64_t>(page) * p.heads + g.h) * p.page_size + (j & (p.page_size - 1))) * D + d;
-        const uint32_t w = E4M3 ? static_cast<const uint8_t*>(p.v)[at] : static_cast<const uint16_t*>(p.v)[at];
-        if (E4M3 ? (w & 0x7Fu) == 0x7Fu : (w & 0x7F80u) == 0x7F80u)
-          kv_remember(bad_count, bad, k, j, d, E4M3 ? NAN : bf16_bits_to_f32(w));
-      }
-      ar_consumer_sync<CONSUMERS>();
-    }
     auto merged = [&](int r, int d) {
       float4 x = *reinterpret_cast<const float4*>(merge + r * OSTR + d);
 #pragma unroll
@@ -798,18 +781,19 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
         const float4 y = *reinterpret_cast<const float4*>(merge + (w * ROWS + r) * OSTR + d);
         x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
       }
-      if (any_bad) {
-        const int n_bad = *bad_count, pos = g.p0 + ((g.r0 + r) / p.group - g.r0 / p.group);
+      if (cut_a | cut_b) {
+        // what was taken out of the values that this row sees, from the pool itself
+        const int pos = g.p0 + ((g.r0 + r) / p.group - g.r0 / p.group);
+        const int32_t* row = p.s.table + static_cast<int64_t>(g.b) * p.s.table_stride;
 #pragma unroll 1
-        for (int n = 0; n < min(n_bad, KV_BAD); ++n) {
-          const KvBad e = bad[n];
-          if (e.d < d || e.d >= d + 4 || !kv_sees(pos, e.j, p.window, p.sinks)) continue;
-          x.x += e.d == d ? e.v : 0.0f;
-          x.y += e.d == d + 1 ? e.v : 0.0f;
-          x.z += e.d == d + 2 ? e.v : 0.0f;
-          x.w += e.d == d + 3 ? e.v : 0.0f;
+        for (uint64_t bits = cut_a | (static_cast<uint64_t>(cut_b) << 32); bits; bits &= bits - 1) {
+          const int n = __ffsll(static_cast<long long>(bits)) - 1;
+          const int j = n < 32 ? g.p0 + 1 + n : max(g.p0 - p.window + 1, p.sinks) + (n - 32);
+          if (!kv_sees(pos, j, p.window, p.sinks)) continue;
+          const int64_t at = ((static_cast<int64_t>(row[j >> p.page_log2]) * p.heads + g.h) * p.page_size + (j & (p.page_size - 1))) * D + d;
+          const float4 v = kv_not_finite<E4M3>(p.v, at);
+          x = make_float4(x.x + v.x, x.y + v.y, x.z + v.z, x.w + v.w);
         }
-        if (n_bad > KV_BAD) x = make_float4(NAN, NAN, NAN, NAN);   // more than are remembered
       }
       return x;
     };

@@ -55,7 +55,9 @@ NVFP4_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, i
 // Non-finite elements of value rows that some rows of a block see and others do
 // not. As an operand they would reach the others too (0 * inf is NaN), so the
 // kernels put zeros in their place and add them, at the end, to the rows that
-// see them. A CTA remembers KV_BAD of them; further ones stay where they are.
+// see them. The token kernel keeps a bit for each such token and reads its values
+// again; a CTA of the prompt kernel remembers KV_BAD elements, further ones stay
+// where they are.
 constexpr int KV_BAD = 16;
 struct KvBad {
   int item, j, d;      // item of the CTA, position, element
@@ -73,6 +75,24 @@ NVFP4_DEV bool kv_remember(int* count, KvBad* list, int item, int j, int d, floa
   __threadfence_block();
   *reinterpret_cast<volatile int*>(&list[n].item) = item;
   return true;
+}
+
+// The four consecutive value elements at `at` of a pool where they are not
+// finite (E4M3: its one NaN), zeros where they are.
+template <bool E4M3>
+NVFP4_DEV float4 kv_not_finite(const void* v, int64_t at) {
+  float x[4];
+  if (E4M3) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(v) + at);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) x[z] = ((w >> (8 * z)) & 0x7Fu) == 0x7Fu ? __int_as_float(0x7FFFFFFF) : 0.0f;
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(v) + at);
+    const uint32_t h[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+#pragma unroll
+    for (int z = 0; z < 4; ++z) x[z] = (h[z] & 0x7F80u) == 0x7F80u ? bf16_bits_to_f32(h[z]) : 0.0f;
+  }
+  return make_float4(x[0], x[1], x[2], x[3]);
 }
 
 // Whether a row at position pos sees position j.

@@ -82,3 +82,35 @@ def test_items_one_after_another(kv):
     places = [(b, c.lens[b] - 1 - b % 5, (5 * b) % heads, (11 * b) % dim) for b in range(batch) if b % 2 == 0]
     hit = check(c, [new] * batch, group, places, uniform=True, times=10)
     assert hit.any() and not hit.all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group,news,past,window,sinks", [
+    (4, [4, 3], [60, 200], 0, 0),
+    (1, [32, 7], [31, 500], 0, 0),          # 32 tokens of one query head in an item
+    (5, [4, 4, 4], [0, 9000, 77], 0, 0),    # split over the length
+    (2, [9, 12], [300, 40], 20, 3),
+    (1, [32], [1000], 1, 0),
+    (1, [30, 5], [700, 90], 33, 70),
+])
+def test_whole_rows_of_few_tokens(kv, dim, group, news, past, window, sinks):
+    """A token that overflowed: all of its values. The last new one, one in the middle of the new ones, the first of a
+    window, and a sink."""
+    lens = [n + p for n, p in zip(news, past)]
+    c = Cache(lens, 2, 16, dim, kv, seed=40 + dim)
+    places = []
+    for b, (n, length) in enumerate(zip(news, lens)):
+        for x in {length - 1, length - n // 2, max(0, length - n + 1 - max(window, 1) // 2), max(0, length - max(window, 1))}:
+            places.append((b, x, b % 2, None))
+    hit = check(c, news, group, places, window, sinks)
+    assert hit.any() and not hit.all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_every_new_token_of_a_verify_step(kv):
+    """All values of all new tokens: the first row sees its own token only, and nothing reaches another head."""
+    c = Cache([25, 4, 640], 3, 32, 64, kv, seed=50)
+    places = [(b, c.lens[b] - i, 1, None) for b in range(3) for i in (1, 2, 3)]
+    hit = check(c, [4, 4, 4], 3, places, uniform=True)
+    assert not hit[:, :3].any() and not hit[:, 6:].any() and not hit[0].any() and hit[1:4, 3:6].all()
