@@ -421,10 +421,7 @@ int nvfp4_kv_append(nvfp4_kv_cache_t cache, nvfp4_kv_seqs_t seqs, const void* K,
  *            call that completes leaves them zero. One call at a time may use it.
  * Scores, softmax statistics and sums are fp32. Positions that a row does not
  * see are left out of its sums whatever they hold: stale rows of a page, keys
- * and values of later tokens, pages of others. (With more than 32 rows of a kv
- * head, max_new * q_heads / heads, value elements that are not finite and that
- * some rows of a block see and others do not are set aside, 16 of them per thread
- * block; with more of them, the block's other rows see them too.) */
+ * and values of later tokens, pages of others. */
 int nvfp4_paged_attention(const void* Q, int64_t q_stride, int q_heads, nvfp4_kv_cache_t cache, nvfp4_kv_seqs_t seqs,
                           int64_t tokens, int window, int sinks, float scale, void* out, void* workspace,
                           size_t workspace_bytes, nvfp4_stream_t stream);

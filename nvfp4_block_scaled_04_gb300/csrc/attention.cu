@@ -133,6 +133,7 @@ int launch_paged_attention(const uint16_t* Q, int64_t q_stride, int q_heads, con
     p.arrived = static_cast<unsigned*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + COUNTER_BYTES);
     p.status = status;
+    p.v = c.v;
     p.k_scale = c.k_scale;
     p.v_scale = c.v_scale;
     if (c.head_dim == 128)

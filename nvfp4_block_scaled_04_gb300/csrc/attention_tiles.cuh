@@ -67,6 +67,12 @@ constexpr int AT_CHUNK = 32;                 // rows of a chunk of 8-bit codes
 constexpr int AT_CHUNKS = 4;                 // chunks of K, and of V, in flight: a tile's
 constexpr int AT_ITEMS = 2;                  // items announced ahead
 constexpr int AT_OKS = 8;                    // announced page masks of tiles
+// Tokens of an item whose values had elements taken out: bit n for position p0 +
+// 1 + n, bit 256 + n for the n-th position of the first row's window (at most
+// 255 of either are seen by some rows of an item and not by others). A role can
+// be two items ahead of the softmax warps, so four items' bits are kept; each
+// checking warp has its own.
+constexpr int AT_CUTS = 4, AT_CUT_WORDS = 16;
 constexpr int AT_SOFTMAX_WARPS = 8;
 constexpr int AT_PROD_WARP = 8, AT_MMA_WARP = 9, AT_CLEAN_WARP = 10;   // 10, 11: half a tile each
 constexpr int AT_V_PROD_WARP = 10, AT_CHECK_WARP = 11;   // (E4M3 caches)
@@ -80,6 +86,7 @@ constexpr int AT_BARS = 3 * AT_SLOTS + 2 * AT_ITEMS + 2 + 10 + 5 * AT_CHUNKS + 1
 struct AtItem {
   int done;
   int h;                 // kv head
+  int b;                 // sequence
   int row0, n_tok;       // first new-token row, tokens
   int p0;                // first position
   int key_end;           // positions at or past it hold nothing
@@ -97,6 +104,7 @@ struct AtParams {
   float scale;           // softmax scale * log2 e, > 0
   int parts;             // parts of an item (1: no split)
   int64_t units;         // work items that the launch and the workspace were sized for
+  const void* v;         // the value pool
   const float* k_scale;  // E4M3 only
   const float* v_scale;
   unsigned* arrived;     // [items][2], zero between calls (split only)
@@ -115,7 +123,7 @@ struct AtShape {
   static constexpr int STAGING = E4M3 ? 0 : AT_SOFTMAX_WARPS * 32 * 128;
   static constexpr int DATA = (2 + K_SLOTS + V_SLOTS) * MAT_BYTES + 2 * AT_CHUNKS * CHUNK_BYTES + STAGING;
   static constexpr int SMEM = DATA + AT_ITEMS * static_cast<int>(sizeof(AtItem)) + AT_OKS * 4 + AT_BARS * 8 +
-                              KV_BAD * static_cast<int>(sizeof(KvBad)) + 64 + 1024;
+                              AT_CUTS * 2 * (AT_CUT_WORDS + 1) * 4 + 64 + 1024;
   static constexpr int O_COL0 = 256;                       // tensor memory: S_A, S_B, O_A, O_B
   // Registers a thread, moved from the other warpgroups to the two softmax
   // ones: 384 x 168 = 64512 at launch, 256 x 208 + 128 x 80 = 63488 after; with
@@ -212,8 +220,8 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
   uint32_t* tmem_slot = oks + AT_OKS;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   unsigned* last_flag = tmem_slot + 2;   // [2]
-  int* bad_count = reinterpret_cast<int*>(tmem_slot + 4);
-  KvBad* bad = reinterpret_cast<KvBad*>(tmem_slot + 5);
+  volatile unsigned* cut_any = tmem_slot + 4;               // [AT_CUTS][2]: 1 where a bit is set in
+  unsigned* cuts = tmem_slot + 4 + 2 * AT_CUTS;             // [AT_CUTS][2][AT_CUT_WORDS]
   const uint32_t bar0 = smem_addr(bars);
   auto kv_full = [&](int s) { return bar0 + 8u * s; };
   auto kv_empty = [&](int s) { return bar0 + 8u * (AT_SLOTS + s); };
@@ -262,8 +270,8 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
-    *bad_count = 0;
-    for (int n = 0; n < KV_BAD; ++n) bad[n].item = -1;
+    for (int n = 0; n < 2 * AT_CUTS; ++n) cut_any[n] = 0;
+    for (int n = 0; n < 2 * AT_CUTS * AT_CUT_WORDS; ++n) cuts[n] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
@@ -304,6 +312,21 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
   auto v_slot = [&](int n) { return S::K_SLOTS + n % S::V_SLOTS; };
   auto k_par = [&](int n) { return (n / S::K_SLOTS) & 1; };
   auto v_par = [&](int n) { return (n / S::V_SLOTS) & 1; };
+  // a checking warp's words for item k, cleared
+  auto clear_cuts = [&](int k, int half) {
+    const int at = (k % AT_CUTS) * 2 + half;
+    if (cut_any[at]) {
+      __syncwarp();
+      if (lane < AT_CUT_WORDS) cuts[at * AT_CUT_WORDS + lane] = 0;
+      if (lane == 0) cut_any[at] = 0;
+      __syncwarp();
+    }
+  };
+  auto mark_cut = [&](int k, int half, int bit) {
+    const int at = (k % AT_CUTS) * 2 + half;
+    atomicOr(cuts + at * AT_CUT_WORDS + (bit >> 5), 1u << (bit & 31));
+    cut_any[at] = 1;
+  };
   auto tile_pos = [&](const AtItem& g, int i) { return (i < g.st ? i : g.w0 + (i - g.st)) * AT_TILE; };
 
   if (warp < AT_SOFTMAX_WARPS) {
@@ -468,17 +491,26 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
         ++outs;
         tc_fence_after();
       }
-      // elements that were not finite, to the rows that see them (columns c0.. of o)
-      const int n_bad = min(*reinterpret_cast<volatile int*>(bad_count), KV_BAD);
-      auto add_bad = [&](uint32_t (&o)[32], int c0) __attribute__((always_inline)) {
+      // whether elements were taken out of the item's values; give_back(add) calls
+      // add(d, v) for those that this row sees, v four elements from d on
+      const int cut_at = (k % AT_CUTS) * 2;
+      const bool cut = nt > 0 && (cut_any[cut_at] | cut_any[cut_at + 1]) != 0;
+      auto give_back = [&](auto add) {
+        const int32_t* row = p.s.table + static_cast<int64_t>(g.b) * p.s.table_stride;
 #pragma unroll 1
-        for (int n = 0; n < n_bad; ++n) {
-          if (*reinterpret_cast<volatile int*>(&bad[n].item) != k) continue;
-          const KvBad e = bad[n];
-          if (e.d < c0 || e.d >= c0 + 32 || !kv_sees(pos, e.j, p.window, p.sinks)) continue;
-#pragma unroll
-          for (int z = 0; z < 32; ++z)
-            o[z] = __float_as_uint(__uint_as_float(o[z]) + (e.d - c0 == z ? e.v : 0.0f));   // (no indexing: o stays in registers)
+        for (int w = 0; w < 2 * AT_CUT_WORDS; ++w) {
+#pragma unroll 1
+          for (unsigned bits = *reinterpret_cast<volatile unsigned*>(cuts + cut_at * AT_CUT_WORDS + w); bits; bits &= bits - 1) {
+            const int n = (w % AT_CUT_WORDS) * 32 + __ffs(static_cast<int>(bits)) - 1;
+            const int j = n < 256 ? g.p0 + 1 + n : max(g.p0 - p.window + 1, p.sinks) + (n - 256);
+            if (!live || !kv_sees(pos, j, p.window, p.sinks)) continue;
+            const int64_t at = ((static_cast<int64_t>(row[j >> p.page_log2]) * p.heads + g.h) * p.page_size + (j & (p.page_size - 1))) * D;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 4) {
+              const float4 v = kv_not_finite<E4M3>(p.v, at + d);
+              if (v.x != 0.0f || v.y != 0.0f || v.z != 0.0f || v.w != 0.0f) add(d, v);
+            }
+          }
         }
       };
       uint16_t* dst = p.out + (static_cast<int64_t>(g.row0 + tok) * p.heads * p.group + static_cast<int64_t>(g.h) * p.group + my_head) * D;
@@ -500,10 +532,6 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[0][e] = o[1][e] = 0u;
-          }
-          if (n_bad > 0) {
-            add_bad(o[0], 64 * hf);
-            add_bad(o[1], 64 * hf + 32);
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -531,6 +559,16 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
             __syncwarp();
           }
         }
+        if (cut) {
+          // (the row was written by this warp's lanes: they have met since)
+          __syncwarp();
+          give_back([&](int d, float4 v) {
+            const uint2 y = __ldcg(reinterpret_cast<const uint2*>(dst + d));
+            *reinterpret_cast<uint2*>(dst + d) =
+                make_uint2(f32x2_to_bf16x2(bf16_bits_to_f32(y.x & 0xFFFFu) + v.x, bf16_bits_to_f32(y.x >> 16) + v.y),
+                           f32x2_to_bf16x2(bf16_bits_to_f32(y.y & 0xFFFFu) + v.z, bf16_bits_to_f32(y.y >> 16) + v.w));
+          });
+        }
         tc_fence_before();
         continue;
       }
@@ -550,7 +588,6 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
-          if (n_bad > 0) add_bad(o, 32 * q);
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             __stcg(reinterpret_cast<float4*>(mine) + (8 * q + e / 4) * AT_ROWS + r,
@@ -558,6 +595,12 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
                                __uint_as_float(o[e + 3])));
         }
         __stcg(reinterpret_cast<float2*>(mine + AT_ROWS * D + 2 * r), make_float2(m * c, sum_l));
+        if (cut)
+          give_back([&](int d, float4 v) {
+            float4* y = reinterpret_cast<float4*>(mine) + (d / 4) * AT_ROWS + r;
+            const float4 x = __ldcg(y);
+            __stcg(y, make_float4(x.x + v.x, x.y + v.y, x.z + v.z, x.w + v.w));
+          });
         tc_fence_before();
       }
       if (!meet()) break;   // the four warps' shares are written: the release below covers them
@@ -650,6 +693,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
             const int blk = nb - 1 - static_cast<int>(flat - run - before);
             const int len = kv_len(p.s, b0 + src);
             g.done = 0;
+            g.b = b0 + src;
             g.row0 = r0_b + blk * item_tok;
             g.n_tok = min(item_tok, n_b - blk * item_tok);
             g.p0 = len - n_b + blk * item_tok;
@@ -839,6 +883,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
         bool ok = true;
         AtItem g;
         for (int k = 0; ok && get_item(k, g); ++k) {
+          clear_cuts(k, 0);
           const int p1 = g.p0 + g.n_tok - 1;
           for (int i = g.i0; i < g.i1 && ok; ++i, ++tiles) {
             // tile rows that later rows of the item see and earlier ones do not, and the other way round
@@ -854,16 +899,15 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
                   if (!((row >= a0 && row < a1) || (row >= b0 && row < b1))) continue;
                   const uint32_t addr = chunk(1, cu) + (u * 32 + lane) * 16;
                   const uint4 w = lds128(addr);
-                  uint32_t y[4] = {w.x, w.y, w.z, w.w}, any = 0;   // bit 7 of a NaN's byte
+                  uint32_t y[4] = {w.x, w.y, w.z, w.w}, any = 0;
 #pragma unroll
-                  for (int z = 0; z < 4; ++z) any |= (y[z] & 0x7F7F7F7Fu) + 0x01010101u;
-                  if (!(any & 0x80808080u)) continue;
-#pragma unroll
-                  for (int z = 0; z < 16; ++z) {
-                    const uint32_t sh = 8 * (z & 3);
-                    if (((y[z >> 2] >> sh) & 0x7Fu) == 0x7Fu && kv_remember(bad_count, bad, k, j0 + row, piece * 16 + z, NAN))
-                      y[z >> 2] &= ~(0xFFu << sh);
+                  for (int z = 0; z < 4; ++z) {
+                    const uint32_t top = ((y[z] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // bit 7 of a NaN's byte
+                    any |= top;
+                    y[z] &= ~((top >> 7) * 0xFFu);
                   }
+                  if (!any) continue;
+                  mark_cut(k, 0, row >= a0 && row < a1 ? row - a0 : 256 + row - b0);
                   sts128(addr, y);
                   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the chunk's next copy comes after
                 }
@@ -937,6 +981,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
       bool ok = true;
       AtItem g;
       for (int k = 0; ok && get_item(k, g); ++k) {
+        clear_cuts(k, half);
         const int p1 = g.p0 + g.n_tok - 1;
         for (int i = g.i0; i < g.i1; ++i, ++tiles) {
           const int j0 = tile_pos(g, i), s = v_slot(tiles);
@@ -949,30 +994,35 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
             c1 = min(c1, AT_TILE);
             for (int e = c0 * 8 + half * 32 + lane; e < c1 * 8; e += 64)
 #pragma unroll
-              for (int hf = 0; hf < S::HALVES; ++hf) f(slot(s) + hf * (AT_TILE * 128) + e * 16, e >> 3, hf * 64 + (((e & 7) ^ (e >> 3 & 7)) << 3));
+              for (int hf = 0; hf < S::HALVES; ++hf) f(slot(s) + hf * (AT_TILE * 128) + e * 16, e >> 3);
             wrote = wrote || c0 < c1;
           };
           // rows past the item's last position, and rows between the sinks and its first window
-          auto zero = [&](uint32_t addr, int, int) { sts128(addr, {0u, 0u, 0u, 0u}); };
+          auto zero = [&](uint32_t addr, int) { sts128(addr, {0u, 0u, 0u, 0u}); };
           each(p1 + 1 - j0, AT_TILE, zero);
           if (p.window > 0) each(p.sinks - j0, g.p0 - p.window + 1 - j0, zero);
           // rows that later rows of the item see and earlier ones do not, and the other way round
-          auto check = [&](uint32_t addr, int row, int d0) {
-            const uint4 w = lds128(addr);
-            uint32_t y[4] = {w.x, w.y, w.z, w.w}, any = 0;   // bit 15 of a half whose exponent is all ones
+          // (bit0: the bit of tile row 0)
+          auto check = [&](int bit0) {
+            return [&, bit0](uint32_t addr, int row) {
+              const uint4 w = lds128(addr);
+              uint32_t y[4] = {w.x, w.y, w.z, w.w}, any = 0;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) any |= (y[z] & 0x7F807F80u) + 0x00800080u;
-            if (!(any & 0x80008000u)) return;
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              const uint32_t sh = 16 * (z & 1), h = (y[z >> 1] >> sh) & 0xFFFFu;
-              if ((h & 0x7F80u) == 0x7F80u && kv_remember(bad_count, bad, k, j0 + row, d0 + z, bf16_bits_to_f32(h)))
-                y[z >> 1] &= ~(0xFFFFu << sh);
-            }
-            sts128(addr, y);
+              for (int z = 0; z < 4; ++z) {
+                const uint32_t top = ((y[z] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;   // bit 15 of a half whose exponent is all ones
+                any |= top;
+                y[z] &= ~((top >> 15) * 0xFFFFu);
+              }
+              if (!any) return;
+              mark_cut(k, half, bit0 + row);
+              sts128(addr, y);
+            };
           };
-          each(g.p0 + 1 - j0, p1 + 1 - j0, check);
-          if (p.window > 0) each(max(g.p0 - p.window + 1, p.sinks) - j0, min(p1 - p.window, g.p0) + 1 - j0, check);
+          each(g.p0 + 1 - j0, p1 + 1 - j0, check(j0 - (g.p0 + 1)));
+          if (p.window > 0) {
+            const int lo_b = max(g.p0 - p.window + 1, p.sinks);
+            each(lo_b - j0, min(p1 - p.window, g.p0) + 1 - j0, check(256 + j0 - lo_b));
+          }
           if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(kv_clean(s));

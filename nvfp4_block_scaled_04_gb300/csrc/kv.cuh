@@ -54,28 +54,8 @@ NVFP4_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, i
 
 // Non-finite elements of value rows that some rows of a block see and others do
 // not. As an operand they would reach the others too (0 * inf is NaN), so the
-// kernels put zeros in their place and add them, at the end, to the rows that
-// see them. The token kernel keeps a bit for each such token and reads its values
-// again; a CTA of the prompt kernel remembers KV_BAD elements, further ones stay
-// where they are.
-constexpr int KV_BAD = 16;
-struct KvBad {
-  int item, j, d;      // item of the CTA, position, element
-  float v;
-};
-// Remembers one; false if there is no room left. Other threads may be reading
-// the list for other items meanwhile: `item`, which no reader looks for yet, is
-// written last (it is -1 in entries that were never written).
-NVFP4_DEV bool kv_remember(int* count, KvBad* list, int item, int j, int d, float v) {
-  const int n = atomicAdd(count, 1);
-  if (n >= KV_BAD) return false;
-  list[n].j = j;
-  list[n].d = d;
-  list[n].v = v;
-  __threadfence_block();
-  *reinterpret_cast<volatile int*>(&list[n].item) = item;
-  return true;
-}
+// kernels put zeros in their place and keep a bit for the token; at the end they
+// read its values again and add those elements to the rows that see them.
 
 // The four consecutive value elements at `at` of a pool where they are not
 // finite (E4M3: its one NaN), zeros where they are.

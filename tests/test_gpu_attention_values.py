@@ -114,3 +114,38 @@ def test_every_new_token_of_a_verify_step(kv):
     places = [(b, c.lens[b] - i, 1, None) for b in range(3) for i in (1, 2, 3)]
     hit = check(c, [4, 4, 4], 3, places, uniform=True)
     assert not hit[:, :3].any() and not hit[:, 6:].any() and not hit[0].any() and hit[1:4, 3:6].all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group,news,past,window,sinks", [
+    (4, [90, 130], [0, 500], 0, 0),
+    (1, [300, 257], [40, 1], 0, 0),         # 256 tokens of one query head in an item
+    (4, [40], [9000], 0, 0),                # split over the positions
+    (3, [200, 64], [300, 77], 100, 5),
+    (1, [600, 280], [0, 513], 130, 3),
+    (5, [60, 90], [300, 0], 1, 0),
+    (8, [40, 33], [2000, 700], 700, 300),
+])
+def test_whole_rows_of_prompts(kv, dim, group, news, past, window, sinks):
+    """A token that overflowed: all of its values, at the same places as for a few tokens, and one of the first."""
+    lens = [n + p for n, p in zip(news, past)]
+    c = Cache(lens, 2, 16, dim, kv, seed=60 + dim)
+    places = []
+    for b, (n, length) in enumerate(zip(news, lens)):
+        for x in {length - 1, length - n // 2, max(0, length - n + 1 - max(window, 1) // 2), max(0, length - max(window, 1)), length - n + 2}:
+            places.append((b, x, b % 2, None))
+    hit = check(c, news, group, places, window, sinks)
+    assert hit.any() and not hit.all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window", [0, 64])
+def test_every_other_new_token_of_a_prompt(kv, window):
+    """Half of all new tokens' values, in a batch whose other sequences are finite: the rows before the first stay
+    exact, and no sequence changes another, whatever a thread block has met before."""
+    batch, new = 40, 150
+    c = Cache([new + b for b in range(batch)], 4, 16, 64, kv, seed=70)
+    places = [(b, c.lens[b] - 1 - i, 2, None) for b in range(0, batch, 3) for i in range(0, new - 20, 2)]
+    hit = check(c, [new] * batch, 2, places, window=window, sinks=2 if window else 0, uniform=True, times=2)
+    assert hit.any() and not hit.all()
