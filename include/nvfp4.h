@@ -419,7 +419,10 @@ int nvfp4_kv_append(nvfp4_kv_cache_t cache, nvfp4_kv_seqs_t seqs, const void* K,
  *            q_heads, cache.heads, head_dim) bytes, 16-byte aligned. Its first
  *            4096 bytes must be zero before the first call that uses it; every
  *            call that completes leaves them zero. One call at a time may use it.
- * Scores, softmax statistics and sums are fp32. Positions that a row does not
+ * Scores, softmax statistics and sums are fp32. The softmax weights are rounded
+ * for the second product: bf16 caches, two bf16 halves (2^-16 together) for up to
+ * 32 rows of a kv head (max_new * q_heads / heads) and one bf16 (2^-8) for more;
+ * E4M3 caches, f16 (2^-11, and 2^-36 of the heaviest weight). Positions that a row does not
  * see are left out of its sums whatever they hold: stale rows of a page, keys
  * and values of later tokens, pages of others. */
 int nvfp4_paged_attention(const void* Q, int64_t q_stride, int q_heads, nvfp4_kv_cache_t cache, nvfp4_kv_seqs_t seqs,

@@ -33,7 +33,9 @@
 // would cost as much error as the output's own rounding and the second MMA
 // costs no time here. E4M3 caches: k and v are exact in f16, q is scaled by a
 // power of two into f16 (exact for elements above amax 2^-29), p is one f16
-// (2^-12, a sixteenth of the output's rounding).
+// (2^-11, an eighth of the output's rounding) in f16's upper range (kv.cuh): that
+// much down to 2^-25 of the heaviest weight so far, and an absolute 2^-36 of it
+// below.
 //
 // Measured, 8 kv heads, D = 128: 64 sequences of 9k..22k positions, bf16, 578 us
 // (the copy rate); 8 sequences of 517..24k, 20 rows, E4M3, 63.0 us against 29.7
@@ -55,7 +57,6 @@ namespace {
 constexpr int AR_WARPS = 4;                  // consumer warps, 16 tokens of a tile each
 constexpr int AR_MAX_STAGES = 8;
 constexpr int AR_ITEMS = 2;                  // items announced ahead
-constexpr float AR_SLACK = 8.0f;             // powers of two that p may exceed 1 by before sums are rescaled
 constexpr int AR_KEPT = 128;                 // sequences whose lengths are kept in shared memory
 constexpr int AR_PAD = 4;                    // fp32 words between rows of the merge buffer: no bank conflicts
 constexpr unsigned AR_ALL = 0xffffffffu;
@@ -652,12 +653,12 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
           mx = fmaxf(mx, __shfl_xor_sync(AR_ALL, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(AR_ALL, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(AR_ALL, mx, 16));
-          // m moves, and o with it, only where p would exceed 2^AR_SLACK
-          const bool grows = mx - m[nt][c] > AR_SLACK;
+          // m moves, and o with it, only where p would exceed 2^SLACK
+          const bool grows = mx - m[nt][c] > KvWeights<E4M3>::SLACK;
           alpha[nt][c] = grows ? exp2_approx(m[nt][c] - mx) : 1.0f;
           moved = moved || grows;
           if (grows) m[nt][c] = mx;
-          const float use = m[nt][c] == -INFINITY ? 0.0f : m[nt][c];
+          const float use = (m[nt][c] == -INFINITY ? 0.0f : m[nt][c]) - KvWeights<E4M3>::LIFT;
           s[nt][c] = exp2_approx(s[nt][c] - use);
           s[nt][c + 2] = exp2_approx(s[nt][c + 2] - use);
           l[nt][c] = l[nt][c] * alpha[nt][c] + (s[nt][c] + s[nt][c + 2]);

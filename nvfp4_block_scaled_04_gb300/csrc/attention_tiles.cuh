@@ -7,8 +7,8 @@
 // x the score in powers of two. The rows of one kv head share its keys and
 // values, so a 128-row tile packs (token, query head) pairs: 128 / G tokens of
 // all G heads. The running maximum that o is kept relative to moves only when
-// it would grow by more than 2^8 (p stays below 2^8, far inside bf16 and
-// fp32), so o is rescaled in tensor memory a few times per row, not per tile.
+// it would grow by more than 2^8 (E4M3 caches: 2^4; p stays below 2^15), so o is
+// rescaled in tensor memory a few times per row, not per tile.
 //
 // What bounds it: 4 * 128 * 128 * D flops per (row tile, 128 positions); K and
 // V come from L2 mostly. Per SM 1024 tensor clocks a tile at D = 128, against
@@ -34,10 +34,12 @@
 // finished S(j + 1) says that O += P(j) V(j) is finished, so the softmax warps
 // may rescale O before they publish P(j + 1).
 //
-// Roundings: q, k, v as they are, products exact, sums fp32; p is rounded to
-// one bf16 (2^-9) for the second product, as the tensor cores take it. Two
-// halves would cost a third more tensor time and halve an error that is that
-// of the output's own rounding.
+// Roundings. bf16 caches: q, k, v as they are, products exact, sums fp32; p is
+// rounded to one bf16 (2^-8) for the second product, as the tensor cores take it:
+// about as much error as the output's own rounding. Two halves, as the token
+// kernel takes, would be half as much tensor time again. E4M3 caches: k and v are
+// exact in f16, q is scaled by a power of two into f16, p is one f16 (2^-11) in
+// f16's upper range (kv.cuh).
 //
 // Few items (a short chunk on a long context) are split over the positions:
 // each part leaves (m, l, o) in the workspace and the last part of a row tile
@@ -77,7 +79,6 @@ constexpr int AT_SOFTMAX_WARPS = 8;
 constexpr int AT_PROD_WARP = 8, AT_MMA_WARP = 9, AT_CLEAN_WARP = 10;   // 10, 11: half a tile each
 constexpr int AT_V_PROD_WARP = 10, AT_CHECK_WARP = 11;   // (E4M3 caches)
 constexpr int AT_CONVERT_WARP = 12;          // 12, 13: K's codes, 14, 15: V's (E4M3 caches)
-constexpr float AT_SLACK = 8.0f;             // powers of two that p may exceed 1 by
 // slot full / empty / clean, item full / empty, q full / empty, s full, p full,
 // o full, join, q ready (each for A and B), chunk full / empty (K's, V's), chunk
 // checked (V's), drain
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
           for (int e = 2; e < 32; e += 2) mx[q] = max3(mx[q], __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
         }
         const float mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
-        const bool grows = (mn - m) * c > AT_SLACK;
+        const bool grows = (mn - m) * c > KvWeights<E4M3>::SLACK;
         if (__any_sync(0xffffffffu, grows)) {
           const float alpha = grows ? exp2_approx((m - mn) * c) : 1.0f;
           if (grows) m = mn;
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
             }
           }
         }
-        const float neg = m == -INFINITY ? 0.0f : -m * c;
+        const float neg = m == -INFINITY ? 0.0f : KvWeights<E4M3>::LIFT - m * c;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t w[16];

@@ -52,6 +52,19 @@ NVFP4_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, i
       : "memory");
 }
 
+// The scale of softmax weights: p = 2^(x - m + LIFT) with m the maximum that the
+// sums are kept relative to, which moves only where p would exceed 2^(SLACK +
+// LIFT). The lift is the same in l and o, so it leaves no trace in the output.
+// E4M3 caches take p as one f16: lifted, and with less slack, a row's heaviest
+// weight lies in [2^11, 2^15], so that weights keep f16's 11 bits down to 2^-25 of
+// it (131,072 tokens of that weight hold 2^-8 together) and lose 2^-36 of it at
+// most below. Weights in bf16 have fp32's range and need no lift.
+template <bool E4M3>
+struct KvWeights {
+  static constexpr float SLACK = E4M3 ? 4.0f : 8.0f;
+  static constexpr float LIFT = E4M3 ? 11.0f : 0.0f;
+};
+
 // Non-finite elements of value rows that some rows of a block see and others do
 // not. As an operand they would reach the others too (0 * inf is NaN), so the
 // kernels put zeros in their place and keep a bit for the token; at the end they
