@@ -416,7 +416,9 @@ int nvfp4_kv_append(nvfp4_kv_cache_t cache, nvfp4_kv_seqs_t seqs, const void* K,
  *   window   0: none;  sinks >= 0 (ignored without a window)
  *   out      device bf16 [tokens][q_heads][head_dim], 16-byte aligned
  *   workspace  >= nvfp4_workspace_size(NVFP4_OP_PAGED_ATTENTION, batch, max_new,
- *            q_heads, cache.heads, head_dim) bytes, 16-byte aligned. Its first
+ *            q_heads, cache.heads, head_dim) bytes, 16-byte aligned; one of that size
+ *            serves every call with a batch, max_new, q_heads / cache.heads and
+ *            head_dim of as much or less. Its first
  *            4096 bytes must be zero before the first call that uses it; every
  *            call that completes leaves them zero. One call at a time may use it.
  * Scores, softmax statistics and sums are fp32. The softmax weights are rounded

@@ -104,8 +104,10 @@ bool takes_tiles(int64_t rows) { return rows > 32; }
 size_t attention_workspace_bytes(int64_t batch, int64_t max_new, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
   if (batch <= 0 || max_new <= 0 || kv_heads <= 0 || q_heads <= 0 || head_dim <= 0) return 0;
   const int64_t rows = max_new * (q_heads / kv_heads);
-  const int nt = rows_nt(rows);
-  int64_t parts = static_cast<int64_t>(rows_grid(nt)) * 2 * 8 * nt;               // rows of partial sums
+  // rows of partial sums, the most of any call with as many rows or fewer (an
+  // item of 24 rows has more than one of 32, whose CTAs are half as many)
+  int64_t parts = 0;
+  for (int nt = 1; nt <= rows_nt(rows); ++nt) parts = std::max(parts, static_cast<int64_t>(rows_grid(nt)) * 2 * 8 * nt);
   if (takes_tiles(rows)) parts = std::max(parts, static_cast<int64_t>(sm_count()) * 2 * AT_ROWS);
   return static_cast<size_t>(COUNTER_BYTES + parts * (head_dim + 2) * 4);
 }

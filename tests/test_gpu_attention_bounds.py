@@ -37,3 +37,20 @@ def test_offsets_that_fall_stay_inside_the_workspace(kv):
                             workspace=room[:need]).float().cpu().double().numpy()
     assert m.read_device_status() == 0
     assert (np.abs(got - ref) <= bound(ref, size, tokens, kv)).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("most,group", [(4, 8), (32, 1), (30, 4)])
+def test_a_workspace_serves_smaller_calls(kv, most, group):
+    """A verify loop: the workspace of the largest step, steps with fewer drafts on it."""
+    m = nv()
+    lens = [1500, 300, 77]
+    c = Cache(lens, 2, 16, 128, kv, seed=2)
+    dc, table = device_cache(m, c), c.table.to(DEV)
+    ws = m.attention_workspace(3, most, 2 * group, 2, 128)
+    for new in range(most, 0, -1 if most < 9 else -5):
+        q = queries(3 * new, 2 * group, 128, new)
+        ref, size = attention(c, q, [new] * 3)
+        got = m.paged_attention(q.to(DEV), dc, table, torch.tensor(lens, dtype=torch.int32, device=DEV), max_new=new, workspace=ws)
+        assert m.read_device_status() == 0
+        assert (np.abs(got.float().cpu().double().numpy() - ref) <= bound(ref, size, new * group, kv)).all()
