@@ -332,6 +332,8 @@ int nvfp4_paged_attention(const void* Q, int64_t q_stride, int q_heads, nvfp4_kv
   if (q_heads < 1 || q_heads % cache.heads != 0 || window < 0 || sinks < 0 || !(scale - scale == 0.0f))
     return NVFP4_ERR_INVALID_ARG;
   if (q_heads / cache.heads > 128) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  // the kernels count a kv head's rows in 31 bits (more than memory holds)
+  if (tokens > ((1ll << 31) - 256) / (q_heads / cache.heads)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (tokens == 0) return NVFP4_OK;
   if (!Q || !out || q_stride < static_cast<int64_t>(q_heads) * cache.head_dim) return NVFP4_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(out) || q_stride % 8 != 0) return NVFP4_ERR_MISALIGNED;

@@ -45,7 +45,7 @@ int launch_rows(ArParams p, const nvfp4_kv_cache_t& c, cudaStream_t stream) {
   const int box = c.page_size < S::TILE ? c.page_size : S::TILE;
   if (int rc = kv_map(&mk, c.k, c, box, S::HALVES)) return rc;
   if (int rc = kv_map(&mv, c.v, c, box, S::HALVES)) return rc;
-  const int fixed = S::FIXED_BYTES + 4 * (p.s.batch + 2) + (p.s.batch <= AR_KEPT ? 4 * (2 * p.s.batch + 2) : 0);
+  const int fixed = S::FIXED_BYTES + 8 * (p.s.batch + 2) + (p.s.batch <= AR_KEPT ? 4 * (2 * p.s.batch + 2) : 0);
   const int room = (SMEM_SM - (S::CTAS - 1) * 1024) / S::CTAS - fixed;
   p.stages = std::max(2, std::min(AR_MAX_STAGES, room / S::STAGE_BYTES));
   const int smem = fixed + p.stages * S::STAGE_BYTES;

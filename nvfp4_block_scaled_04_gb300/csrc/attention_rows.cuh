@@ -152,95 +152,26 @@ NVFP4_DEV void ar_consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 
-// A piece of the line of tiles that lies inside one item, as the item warp
-// hands it to the consumers.
-struct ArItem {
-  int done;
-  int h;                  // kv head
-  int r0, n_rows;         // rows of the sequence's (token, head) pairs
-  int row0;               // the sequence's first new-token row
-  int p0, p1;             // positions of the first and the last row
-  int key_end;            // positions at or past it hold nothing
-  KvTiles tiles;
-  int i0, i1;             // the piece's tiles
-  int b;                  // sequence
-  unsigned first_cta, last_cta;   // CTAs that share the item
-};
 static_assert(sizeof(ArItem) <= 64, "announced items");
 
+// A CTA's piece of the line (kv_line.h), item by item.
 template <class S>
 struct ArWalk {
   const ArParams& p;
-  const unsigned* pre;   // tiles of the sequences before (shared memory)
+  const ArLine& line;
+  const uint64_t* pre;   // the line before each sequence (shared memory)
   const int* rows;       // first new-token rows [batch + 1] and lengths [batch], for batches up to AR_KEPT
-  unsigned per, u, end;
+  ArPiece<S::TILE, S::ROWS, S::EXTRA> piece;
 
   NVFP4_DEV bool next(ArItem& g) {
-    while (u < end) {
-      int lo = 0, hi = p.s.batch;             // last b with pre[b] <= u
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= u)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      g.b = lo;
-      g.done = 0;
-      const bool kept = p.s.batch <= AR_KEPT;
-      g.row0 = kept ? rows[lo] : kv_row0(p.s, lo);
-      const int n = (kept ? rows[lo + 1] : kv_row0(p.s, lo + 1)) - g.row0;
-      const int len = kept ? rows[p.s.batch + 1 + lo] : kv_len(p.s, lo);
-      const unsigned blocks = static_cast<unsigned>((n * p.group + S::ROWS - 1) / S::ROWS);
-      const unsigned per_item = (pre[lo + 1] - pre[lo]) / (blocks * static_cast<unsigned>(p.heads));
-      const unsigned in = u - pre[lo], item = in / per_item;
-      const int rb = static_cast<int>(item / static_cast<unsigned>(p.heads));
-      g.h = static_cast<int>(item) - rb * p.heads;
-      g.i0 = static_cast<int>(in - item * per_item);
-      const unsigned u0 = u - static_cast<unsigned>(g.i0);
-      const int i1 = static_cast<int>(min(end - u0, per_item));
-      u = u0 + static_cast<unsigned>(i1);
-      g.r0 = rb * S::ROWS;
-      g.n_rows = min(S::ROWS, n * p.group - g.r0);
-      g.p0 = len - n + g.r0 / p.group;
-      g.p1 = len - n + (g.r0 + g.n_rows - 1) / p.group;
-      const int64_t cap = static_cast<int64_t>(p.s.max_pages) * p.page_size;
-      g.key_end = static_cast<int>(cap < len ? cap : len);
-      g.tiles = kv_tiles<S::TILE>(g.p0, g.p1, p.window, p.sinks, g.key_end);
-      // what follows the item's tiles on the line is nobody's work
-      const int real = max(g.tiles.count, 1);
-      if (g.i0 >= real) continue;
-      g.i1 = min(i1, g.tiles.count);
-      g.first_cta = u0 / per;
-      g.last_cta = (u0 + static_cast<unsigned>(real) - 1u) / per;
-      return true;
-    }
-    return false;
+    auto seq = [&](int b) {
+      const bool kept = line.batch <= AR_KEPT;
+      const int r0 = kept ? rows[b] : kv_row0(p.s, b);
+      return ArSeq{r0, (kept ? rows[b + 1] : kv_row0(p.s, b + 1)) - r0, kept ? rows[line.batch + 1 + b] : kv_len(p.s, b)};
+    };
+    return piece.next(line, pre, seq, g);
   }
 };
-
-// Length on the line of all items of a sequence of n new tokens: each block of
-// rows is given the most tiles that any sees, and EXTRA more that stand for what
-// an item costs beside them (its parts' meeting and the output).
-template <class S>
-NVFP4_DEV unsigned ar_seq_tiles(const ArParams& p, int n, int len) {
-  if (n <= 0) return 0;
-  const int64_t cap = static_cast<int64_t>(p.s.max_pages) * p.page_size;
-  const int key_end = static_cast<int>(cap < len ? cap : len);
-  const int blocks = (n * p.group + S::ROWS - 1) / S::ROWS;
-  const int span = (S::ROWS - 1 + p.group - 1) / p.group;   // positions between a block's first and last row, at most
-  int most;
-  if (p.window > 0 && blocks > 1) {
-    // a block whose rows lie as late as any: two more tiles than its widest range of positions can touch
-    const int64_t st = (min(p.sinks, key_end) + S::TILE - 1) / S::TILE;
-    const int64_t w = (static_cast<int64_t>(p.window) + span) / S::TILE + 2;
-    const int64_t all = (key_end + S::TILE - 1) / S::TILE;
-    most = static_cast<int>(st + w < all ? st + w : all);
-  } else {
-    most = kv_tiles<S::TILE>(len - n, len - 1, p.window, p.sinks, key_end).count;
-  }
-  return static_cast<unsigned>(max(most, 1) + S::EXTRA) * static_cast<unsigned>(blocks * p.heads);
-}
 
 template <bool E4M3, int D, int NT>
 __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D, NT>::CTAS)
@@ -269,7 +200,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
   unsigned* stage_cut = stage_ok + AR_MAX_STAGES;                                        // [2]: tokens that elements were taken out of
   volatile int* abort_flag = reinterpret_cast<volatile int*>(stage_cut + 2 * AR_MAX_STAGES);
   unsigned* last_flag = stage_cut + 2 * AR_MAX_STAGES + 1;
-  unsigned* pre = last_flag + 1;                                                         // [batch + 1]
+  uint64_t* pre = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(last_flag + 1) + 7u) & ~static_cast<uintptr_t>(7));   // [batch + 1]
   int* rows = reinterpret_cast<int*>(pre + p.s.batch + 1);                               // [2 batch + 1]
   const uint32_t bar0 = smem_addr(bars);
   auto full_bar = [&](int st) { return bar0 + 8u * st; };
@@ -297,10 +228,11 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
   }
   pdl_launch_dependents();
   pdl_wait();
-  // the line of tiles: prefix sums over the sequences
+  // the line of work: prefix sums over the sequences
+  const ArLine line = {p.s.batch, p.heads, p.group, p.window, p.sinks, static_cast<int64_t>(p.s.max_pages) * p.page_size};
   for (int b = threadIdx.x; b < p.s.batch; b += S::THREADS) {
     const int r0 = kv_row0(p.s, b), r1 = kv_row0(p.s, b + 1), len = kv_len(p.s, b);
-    pre[b + 1] = ar_seq_tiles<S>(p, r1 - r0, len);
+    pre[b + 1] = ar_seq_units<S::TILE, S::ROWS, S::EXTRA>(line, {r0, r1 - r0, len});
     if (p.s.batch <= AR_KEPT) {
       rows[b] = r0;
       rows[b + 1] = r1;   // the next thread writes the same
@@ -309,13 +241,23 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
   }
   __syncthreads();
   if (warp == 0) {
-    unsigned run = 0;
+    uint64_t run = 0;
     for (int b0 = 0; b0 < p.s.batch; b0 += 32) {
-      unsigned x = b0 + lane < p.s.batch ? pre[b0 + lane + 1] : 0u;
+      uint64_t x = b0 + lane < p.s.batch ? pre[b0 + lane + 1] : 0u;
+      if (__any_sync(AR_ALL, (x >> 26) != 0)) {
+#pragma unroll 1
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint64_t y = __shfl_up_sync(AR_ALL, x, d);
+          if (lane >= d) x += y;
+        }
+      } else {
+        unsigned w = static_cast<unsigned>(x);   // 32 of them fit 32 bits
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const unsigned y = __shfl_up_sync(AR_ALL, x, d);
-        if (lane >= d) x += y;
+        for (int d = 1; d < 32; d <<= 1) {
+          const unsigned y = __shfl_up_sync(AR_ALL, w, d);
+          if (lane >= d) w += y;
+        }
+        x = w;
       }
       if (b0 + lane < p.s.batch) pre[b0 + lane + 1] = run + x;
       run += __shfl_sync(AR_ALL, x, 31);
@@ -323,14 +265,8 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
     if (lane == 0) pre[0] = 0;
   }
   __syncthreads();
-  const unsigned total = pre[p.s.batch];
-  unsigned per = (total + gridDim.x - 1) / gridDim.x;
-  // where a CTA's piece would be one tile of long items, two: half the parts to
-  // join (one sequence of 2,000 positions: 8.8 -> 8.0 us)
-  if (per == 1 && total >= (16u + S::EXTRA) * static_cast<unsigned>(p.s.batch * p.heads)) per = 2;
-  const uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * per;
-  if (u0 >= total) return;
-  ArWalk<S> walk{p, pre, rows, per, static_cast<unsigned>(u0), static_cast<unsigned>(u0 + per < total ? u0 + per : total)};
+  ArWalk<S> walk{p, line, pre, rows, {line, pre[p.s.batch], gridDim.x, blockIdx.x}};
+  if (walk.piece.u >= walk.piece.end) return;
   ArItem g;
   const int box = p.page_size < TILE ? p.page_size : TILE;   // tokens of one copied box
   const int box_log2 = 31 - __clz(box), boxes = TILE >> box_log2, boxes_log2 = 31 - __clz(boxes);

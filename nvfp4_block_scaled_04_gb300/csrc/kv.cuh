@@ -2,6 +2,7 @@
 // deals with, and where a sequence's new rows lie.
 #pragma once
 
+#include "kv_line.h"
 #include "launch.h"
 #include "tc_util.cuh"
 
@@ -16,33 +17,6 @@ NVFP4_DEV int kv_row0(const KvSeqs& s, int b) {
 
 // Length of sequence b, inside what position arithmetic in 32 bits can hold.
 NVFP4_DEV int kv_len(const KvSeqs& s, int b) { return min(max(s.lens[b], 0), 1 << 30); }
-
-// The tiles that a block of rows sees: [0, st) (sinks) and [w0, end).
-struct KvTiles {
-  int st, w0, count;
-  NVFP4_DEV int tile(int i) const { return i < st ? i : w0 + (i - st); }
-};
-
-// Tiles of the rows at positions p0..p1 (p1 < 0: none).
-template <int TILE>
-NVFP4_DEV KvTiles kv_tiles(int p0, int p1, int window, int sinks, int key_end) {
-  KvTiles t;
-  const int end = (min(p1 + 1, key_end) + TILE - 1) / TILE;   // one past the last
-  t.st = 0;
-  t.w0 = 0;
-  if (window > 0) {
-    const int lo = p0 - window + 1;                                  // first position in a window
-    const int w0 = lo > 0 ? lo / TILE : 0;
-    const int st = min((min(sinks, key_end) + TILE - 1) / TILE, end);
-    if (w0 > st) {
-      t.st = st;
-      t.w0 = w0;
-    }
-  }
-  t.count = end > t.w0 ? t.st + end - t.w0 : t.st;
-  if (end <= 0) t.count = 0;
-  return t;
-}
 
 NVFP4_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
   asm volatile(

@@ -25,3 +25,9 @@ def test_attention_workspace_never_falls(nv, group):  # noqa: F811
 def test_attention_workspace_never_falls_with_the_query_heads(nv, max_new):  # noqa: F811
     sizes = [size(nv, max_new=max_new, group=g) for g in range(1, 129)]
     assert sizes == sorted(sizes)
+
+
+def test_rows_that_31_bits_do_not_count_are_refused(nv):  # noqa: F811
+    from tests.test_kv_abi import P, attend, seqs
+    assert attend(nv, tokens=(1 << 30) - 1, s=seqs(nv, start=P)) == -2        # 4 query heads on one
+    assert attend(nv, tokens=(1 << 24) - 1, heads=8 * 128, q_stride=8 * 128 * 128, s=seqs(nv, start=P)) == -2
