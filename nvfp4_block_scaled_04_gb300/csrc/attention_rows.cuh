@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
         for (int hf = 0; hf < 2; ++hf) {
           const float a = s[nt][2 * hf], b = s[nt][2 * hf + 1];
           if (E4M3) {
-            hi[nt][hf] = movmatrix_t(f32x2_to_f16x2(a, b));
+            hi[nt][hf] = movmatrix_t(kv_weights_f16x2(a, b));
           } else {
             const uint32_t w = f32x2_to_bf16x2(a, b);
             hi[nt][hf] = movmatrix_t(w);

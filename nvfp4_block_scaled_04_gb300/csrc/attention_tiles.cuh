@@ -7,7 +7,7 @@
 // x the score in powers of two. The rows of one kv head share its keys and
 // values, so a 128-row tile packs (token, query head) pairs: 128 / G tokens of
 // all G heads. The running maximum that o is kept relative to moves only when
-// it would grow by more than 2^8 (E4M3 caches: 2^4; p stays below 2^15), so o is
+// it would grow by more than 2^8 (E4M3 caches: 2^4.9; p stays below 2^16), so o is
 // rescaled in tensor memory a few times per row, not per tile.
 //
 // What bounds it: 4 * 128 * 128 * D flops per (row tile, 128 positions); K and
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
             a = exp2_approx(a);
             b = exp2_approx(b);
             add2(l[2 * (e & 1)], l[2 * (e & 1) + 1], a, b);
-            w[e] = E4M3 ? f32x2_to_f16x2(a, b) : f32x2_to_bf16x2(a, b);
+            w[e] = E4M3 ? kv_weights_f16x2(a, b) : f32x2_to_bf16x2(a, b);
           }
           tc_st_16cols(s_cols + 16 * q, w);
         }

@@ -30,14 +30,24 @@ NVFP4_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, i
 // sums are kept relative to, which moves only where p would exceed 2^(SLACK +
 // LIFT). The lift is the same in l and o, so it leaves no trace in the output.
 // E4M3 caches take p as one f16: lifted, and with less slack, a row's heaviest
-// weight lies in [2^11, 2^15], so that weights keep f16's 11 bits down to 2^-25 of
-// it (131,072 tokens of that weight hold 2^-8 together) and lose 2^-36 of it at
-// most below. Weights in bf16 have fp32's range and need no lift.
+// weight lies in [2^11, 2^15.9], so that weights keep f16's 11 bits down to 2^-25
+// of it (131,072 tokens of that weight hold 2^-8 together) and lose 2^-36 of it at
+// most below. Scores so large that x - m is off by 0.1 (2^20) could pass f16's
+// 65504: the conversion saturates. (2,048 new tokens on 6,144, 32 heads on 8: 282 us
+// with a slack of 4, 272 with 4.9, 262 with 8 and a lift of 7, which would keep 11
+// bits down to 2^-21 only.) Weights in bf16 have fp32's range and need no lift.
 template <bool E4M3>
 struct KvWeights {
-  static constexpr float SLACK = E4M3 ? 4.0f : 8.0f;
+  static constexpr float SLACK = E4M3 ? 4.9f : 8.0f;
   static constexpr float LIFT = E4M3 ? 11.0f : 0.0f;
 };
+
+// Two weights as f16, lo in the low half: to nearest even, saturating.
+NVFP4_DEV uint32_t kv_weights_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
 
 // Non-finite elements of value rows that some rows of a block see and others do
 // not. As an operand they would reach the others too (0 * inf is NaN), so the

@@ -81,3 +81,36 @@ def test_a_sink_in_a_long_context(kv, news):
     """The first token against 131 thousand light ones, which hold 0.4% of the weight together; and under a window."""
     run(kv, 64, 131072, news, 25, 0)
     run(kv, 64, 131072, news, 16, 0, window=65536, sinks=1)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [1, 4, 60])
+def test_a_key_that_is_not_a_number_shows(kv, news):
+    """Every row that sees the key is NaN, the rows of another sequence are not."""
+    m = nv()
+    c = Cache([100, 100], 1, 16, 64, kv, seed=31)
+    place = (int(c.table[0, 1]), 0, 3, 5)
+    if kv == "e4m3":
+        c.k.view(torch.uint8)[place] = 0x7F
+    else:
+        c.k[place] = float("nan")
+    q = queries(2 * news, 2, 64, 3)
+    got = m.paged_attention(q.to(DEV), device_cache(m, c), c.table.to(DEV), torch.tensor(c.lens, dtype=torch.int32, device=DEV),
+                            max_new=news).float().cpu()
+    assert torch.isnan(got[:news]).all() and torch.isfinite(got[news:]).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [1, 70])
+@pytest.mark.parametrize("scale", [30.0, 3000.0])
+def test_large_scores(kv, news, scale):
+    """Scores of hundreds to a hundred thousand powers of two: one token takes nearly all. A score of 2^17 is off by
+    about 2^-8 of a power of two, which moves 2^-8 of a weight between two tokens that come close."""
+    m = nv()
+    c = Cache([400], 2, 32, 64, kv, seed=32)
+    q = queries(news, 4, 64, 8)
+    ref, size = attention(c, q, [news], scale=scale)
+    got = m.paged_attention(q.to(DEV), device_cache(m, c), c.table.to(DEV), torch.tensor(c.lens, dtype=torch.int32, device=DEV),
+                            max_new=news, scale=scale).float().cpu().double().numpy()
+    slack = 2.0 ** -7 * size
+    assert (np.abs(got - ref) <= bound(ref, size, news * 2, kv) + slack).all()
