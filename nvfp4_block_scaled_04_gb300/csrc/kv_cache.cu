@@ -206,7 +206,7 @@ NVFP4_DEV int lowest_free(const int32_t* refs, int64_t pages, int need, int32_t*
 // ----------------------------------------------------------------- reserve
 
 // Pages for the positions of each sequence's new tokens: every table entry
-// there that holds no page gets one, in (sequence, position) order. One warp
+// there that holds no page (an id outside the pool) gets one, in (sequence, position) order. One warp
 // counts and fills a sequence's entries.
 // ws: free pages [pages], then entries needed by the sequences before each [batch].
 __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(const KvSeqs s, int page_size, int32_t* table,
@@ -225,11 +225,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(const KvSeqs s
     if (lane == 0 && end > s.max_pages) atomicExch(status, NVFP4_ERR_INVALID_ARG);
     *e1 = static_cast<int>(end < s.max_pages ? end : s.max_pages);
   };
+  auto holds_none = [&](int page) { return page < 0 || page >= pages; };
   for (int b = warp; b < s.batch; b += PLAN_THREADS / 32) {
     int e0, e1, n = 0;
     range(b, &e0, &e1);
     const int32_t* row = table + b * s.table_stride;
-    for (int e = e0 + lane; e < e1; e += 32) n += row[e] < 0;
+    for (int e = e0 + lane; e < e1; e += 32) n += holds_none(row[e]);
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) first[b] = n;
   }
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(const KvSeqs s
     int32_t* row = table + b * s.table_stride;
     int at = first[b];
     for (int e = e0; e < e1; e += 32) {
-      const bool lacks = e + lane < e1 && row[e + lane] < 0;
+      const bool lacks = e + lane < e1 && holds_none(row[e + lane]);
       const unsigned m = __ballot_sync(0xffffffffu, lacks);
       const int k = at + __popc(m & ((1u << lane) - 1u));
       if (lacks && k < have) {
