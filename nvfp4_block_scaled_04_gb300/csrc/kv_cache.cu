@@ -322,11 +322,14 @@ __global__ void __launch_bounds__(128) kv_fork_copy_kernel(const nvfp4_kv_cache_
   const int fresh = tail && full < max_pages ? table[d * table_stride + full] : -1;
   const int32_t* from = table + a * table_stride;
   if (y < 2 * c.heads) {
-    if (fresh < 0) return;
+    // (in orderly lists the plan has seen the source's page; where a source is also a
+    // fork, its row is being written meanwhile)
+    const int last = fresh >= 0 ? from[full] : -1;
+    if (last < 0 || last >= c.pages || fresh >= c.pages) return;
     const int64_t block = static_cast<int64_t>(c.page_size) * c.head_dim * elem_bytes;
     const int64_t h = y >> 1;
     uint8_t* pool = static_cast<uint8_t*>((y & 1) ? c.v : c.k);
-    const uint4* x = reinterpret_cast<const uint4*>(pool + (from[full] * static_cast<int64_t>(c.heads) + h) * block);
+    const uint4* x = reinterpret_cast<const uint4*>(pool + (last * static_cast<int64_t>(c.heads) + h) * block);
     uint4* o = reinterpret_cast<uint4*>(pool + (fresh * static_cast<int64_t>(c.heads) + h) * block);
     const int n16 = tail * c.head_dim * elem_bytes / 16;
 #pragma unroll 4

@@ -25,3 +25,26 @@ def test_reserve_takes_an_id_past_the_pool_for_no_page():
     assert m.read_device_status() == 0
     written = (cache.k[:, 0, :, 0] == 1).sum(1).cpu().tolist()
     assert written == [16, 16, 0, 8, 3, 0]
+
+
+def test_a_source_that_is_also_a_fork_stays_inside_the_pool():
+    """The lists must not do this and what the rows hold is nobody's promise, but every copy stays inside the pool:
+    pages that no row names keep their contents, and every entry names a page or none."""
+    m = nv()
+    pages, n = 64, 12
+    cache = m.kv_cache(pages, 2, 16, 64)
+    for _ in range(20):
+        for pool in (cache.k, cache.v):
+            pool.fill_(3)
+        cache.k[:2], cache.v[:2] = 1, 2
+        table = torch.full((n + 1, 4), -1, dtype=torch.int32, device=DEV)
+        table[0, :2] = ints([0, 1])
+        lens, refs = ints([25] + [21] * n), torch.zeros(pages, dtype=torch.int32, device=DEV)
+        refs[:2] = 1
+        m.kv_fork(cache, table, lens, refs, ints(range(n)), ints(range(1, n + 1)))
+        t, r = table.cpu().numpy(), refs.cpu().numpy()
+        assert m.read_device_status() == 0
+        assert ((t >= -1) & (t < pages)).all()
+        free = r == 0
+        assert free.sum() >= pages - 2 - n and not np.isin(np.flatnonzero(free), t).any()
+        assert (cache.k[torch.from_numpy(free).to(DEV)] == 3).all() and (cache.v[torch.from_numpy(free).to(DEV)] == 3).all()
