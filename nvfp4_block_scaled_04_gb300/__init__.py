@@ -467,6 +467,15 @@ def attention_workspace(batch: int, max_new: int, q_heads: int, kv_heads: int, h
                        dtype=torch.uint8, device=device)
 
 
+def _given_ws(ws):
+    """A caller's workspace: memory of the device, as much as it says."""
+    if not ws.is_cuda:
+        _require_cuda(ws)
+    if not ws.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor is needed")
+    return ws
+
+
 def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
                     start: torch.Tensor | None = None, max_new: int = 1, window: int = 0, sinks: int = 0,
                     scale: float | None = None, out: torch.Tensor | None = None,
@@ -488,7 +497,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
         if o.shape != (T, heads, D) or o.dtype != torch.bfloat16 or not o.is_contiguous():
             raise ValueError("out: contiguous bf16 of q's shape is needed")
     seqs = _seqs(table, lens, start, max_new)
-    ws = workspace if workspace is not None else attention_workspace(seqs.batch, max_new, heads, c.heads, D, q.device)
+    ws = _given_ws(workspace) if workspace is not None else attention_workspace(seqs.batch, max_new, heads, c.heads, D, q.device)
     _check(lib().nvfp4_paged_attention(q.data_ptr(), q.stride(0) if T > 1 else heads * D, heads, c, seqs, T, window,
                                        sinks, D ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr(),
                                        ws.numel(), _stream()), "nvfp4_paged_attention")
@@ -496,7 +505,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
 
 
 def _pages_ws(workspace, pages, n, device):
-    return workspace if workspace is not None else _workspace(workspace_size(OP_KV_PAGES, pages, n), device)
+    return _given_ws(workspace) if workspace is not None else _workspace(workspace_size(OP_KV_PAGES, pages, n), device)
 
 
 def kv_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int,

@@ -54,3 +54,23 @@ def test_a_workspace_serves_smaller_calls(kv, most, group):
         got = m.paged_attention(q.to(DEV), dc, table, torch.tensor(lens, dtype=torch.int32, device=DEV), max_new=new, workspace=ws)
         assert m.read_device_status() == 0
         assert (np.abs(got.float().cpu().double().numpy() - ref) <= bound(ref, size, new * group, kv)).all()
+
+
+def test_workspaces_that_are_not_device_memory_are_refused():
+    m = nv()
+    cache = m.kv_cache(8, 2, 16, 64)
+    table, lens = torch.zeros(2, 4, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    refs, q = torch.ones(8, dtype=torch.int32, device=DEV), torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV)
+    size = max(m.workspace_size(m.OP_PAGED_ATTENTION, 2, 1, 4, 2, 64), m.workspace_size(m.OP_KV_PAGES, 8, 2))
+    calls = (lambda ws: m.paged_attention(q, cache, table, lens, workspace=ws),
+             lambda ws: m.kv_reserve(table, lens, refs, 16, workspace=ws),
+             lambda ws: m.kv_compact(cache, table, refs, workspace=ws))
+    one = torch.zeros(1, dtype=torch.uint8, device=DEV)
+    for call in calls:
+        with pytest.raises(RuntimeError):
+            call(torch.zeros(size, dtype=torch.uint8))
+        for bad in (one.expand(size), torch.zeros(2 * size, dtype=torch.uint8, device=DEV)[::2]):
+            with pytest.raises(ValueError):
+                call(bad)
+        call(torch.zeros(size, dtype=torch.uint8, device=DEV))
+    assert m.read_device_status() == 0
