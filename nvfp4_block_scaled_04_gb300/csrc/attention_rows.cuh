@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
         // other way round at a window's edge: the tile is looked at before the
         // consumers get it
         const int j0 = g.tiles.tile(i) * TILE;
-        const int lo_b = max(g.p0 - p.window + 1, p.sinks), hi_b = p.window > 0 ? min(g.p1 - p.window, g.p0) : -1;
-        const bool mixed = (g.p1 > g.p0 && j0 + TILE - 1 > g.p0 && j0 <= g.p1) || (j0 <= hi_b && j0 + TILE - 1 >= lo_b);
+        const KvPartly part = kv_partly(g.p0, g.p1, p.window, p.sinks);
+        const bool mixed = part.meets(j0, TILE);
         const uint32_t landed = mixed ? check_bar : full_bar(st);
         if (lane == 0) {
           stage_ok[st] = there;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
         if (mixed) {
           // value elements that are not finite are taken out and added at the
           // end to the rows that see them (kv.cuh): a bit for each of the up to
-          // 31 tokens past p0, and of those from lo_b on, that had any
+          // 31 tokens from part.a0 on, and of those from part.b0 on, that had any
           ok = __all_sync(AR_ALL, mbar_wait_bounded(check_bar, checks++ & 1, abort_flag, p.status));
           if (!ok) break;
           constexpr int CHUNKS = S::ROW_BYTES / 16;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
 #pragma unroll 2
           for (int u = lane; u < TILE * CHUNKS; u += 32) {
             const int row = u / CHUNKS, chunk = u % CHUNKS, jj = j0 + row;
-            if (!((jj > g.p0 && jj <= g.p1) || (jj >= lo_b && jj <= hi_b))) continue;
+            if (!((jj >= part.a0 && jj < part.a1) || (jj >= part.b0 && jj < part.b1))) continue;
             const int r = row & (box - 1), half = S::SEG == 128 ? chunk >> 3 : 0;
             const int c16 = S::SEG == 128 ? (chunk & 7) ^ (r & 7) : chunk ^ ((r >> 1) & 3);
             const uint32_t addr = stage_k(st) + S::MAT_BYTES + (row - r) * S::ROW_BYTES + ((half << box_log2) + r) * S::SEG + (c16 << 4);
@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
             if (!any) continue;
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the slot's next copy comes after
-            if (jj > g.p0)
-              cut_a |= 1u << (jj - g.p0 - 1);
+            if (jj >= part.a0)
+              cut_a |= 1u << (jj - part.a0);
             else
-              cut_b |= 1u << (jj - lo_b);
+              cut_b |= 1u << (jj - part.b0);
           }
           cut_a = __reduce_or_sync(AR_ALL, cut_a);
           cut_b = __reduce_or_sync(AR_ALL, cut_b);
@@ -722,10 +722,11 @@ __global__ void __launch_bounds__(ArShape<E4M3, D, NT>::THREADS, ArShape<E4M3, D
         // what was taken out of the values that this row sees, from the pool itself
         const int pos = g.p0 + ((g.r0 + r) / p.group - g.r0 / p.group);
         const int32_t* row = p.s.table + static_cast<int64_t>(g.b) * p.s.table_stride;
+        const KvPartly part = kv_partly(g.p0, g.p1, p.window, p.sinks);
 #pragma unroll 1
         for (uint64_t bits = cut_a | (static_cast<uint64_t>(cut_b) << 32); bits; bits &= bits - 1) {
           const int n = __ffsll(static_cast<long long>(bits)) - 1;
-          const int j = n < 32 ? g.p0 + 1 + n : max(g.p0 - p.window + 1, p.sinks) + (n - 32);
+          const int j = n < 32 ? part.a0 + n : part.b0 + (n - 32);
           if (!kv_sees(pos, j, p.window, p.sinks)) continue;
           const int64_t at = ((static_cast<int64_t>(row[j >> p.page_log2]) * p.heads + g.h) * p.page_size + (j & (p.page_size - 1))) * D + d;
           const float4 v = kv_not_finite<E4M3>(p.v, at);

@@ -53,6 +53,24 @@ NVFP4_HD KvTiles kv_tiles(int p0, int p1, int window, int sinks, int key_end) {
   return t;
 }
 
+// The positions that some of the rows at positions p0..p1 see and others do not:
+// [a0, a1), seen by the later rows only, and [b0, b1), which the later rows'
+// windows have left behind. Either may be empty; neither holds more than p1 - p0.
+struct KvPartly {
+  int a0, a1, b0, b1;
+  NVFP4_HD bool meets(int j0, int tile) const {   // whether the tile at j0 has any
+    return most_of(a0, j0) < least(a1, j0 + tile) || most_of(b0, j0) < least(b1, j0 + tile);
+  }
+};
+NVFP4_HD KvPartly kv_partly(int p0, int p1, int window, int sinks) {
+  KvPartly x = {p0 + 1, p1 + 1, 0, 0};
+  if (window > 0) {
+    x.b0 = most_of(p0 - window + 1, sinks);
+    x.b1 = least(p1 - window, p0) + 1;
+  }
+  return x;
+}
+
 // What the line depends on beside the sequences.
 struct ArLine {
   int batch, heads, group;   // sequences, kv heads, query heads of each

@@ -26,6 +26,10 @@ int pieces(const ArLine& a, const ArSeq* s, unsigned ctas, unsigned cta, uint64_
   return n;
 }
 }  // namespace
+extern "C" void partly(int p0, int p1, int window, int sinks, int j0, int tile, int* out) {
+  const KvPartly x = kv_partly(p0, p1, window, sinks);
+  out[0] = x.a0, out[1] = x.a1, out[2] = x.b0, out[3] = x.b1, out[4] = x.meets(j0, tile);
+}
 extern "C" int line_pieces(int rows, const ArLine* a, const ArSeq* s, unsigned ctas, unsigned cta, uint64_t* pre, uint64_t* per,
                            ArItem* out, int room) {
   switch (rows) {
@@ -149,3 +153,23 @@ def test_lines_longer_than_32_bits(lib, rows, group, heads, news, length):
             assert (it.b, it.h, it.r0, it.i0, it.i1, it.count) == (b, h, rb * rows, i0, min(i1, count), count)
             assert (it.first_cta, it.last_cta) == (start // per, (start + count - 1) // per)
         assert items
+
+
+@pytest.mark.parametrize("window", [0, 1, 2, 3, 7, 20])
+@pytest.mark.parametrize("sinks", [0, 1, 5, 40])
+def test_positions_that_some_rows_see_and_others_do_not(lib, window, sinks):
+    """Against every row's mask; a tile has some exactly where one of its positions is such (a tile that is looked at
+    without need costs a wait: a single row has none at all)."""
+    out = (ctypes.c_int * 5)()
+    for p0 in range(-3, 30):
+        for p1 in range(p0, p0 + 9):
+            def sees(p, j):
+                return j <= p and (not window or p - j < window or j < sinks)
+            want = [j for j in range(0, 45) if len({sees(p, j) for p in range(p0, p1 + 1)}) == 2]
+            for j0 in range(0, 44, 4):
+                lib.partly(p0, p1, window, sinks, j0, 4, out)
+                a0, a1, b0, b1, meets = out
+                got = [j for j in range(0, 45) if a0 <= j < a1 or b0 <= j < b1]
+                assert got == want
+                assert max(0, a1 - a0) <= p1 - p0 and max(0, b1 - b0) <= p1 - p0
+                assert bool(meets) == any(j0 <= j < j0 + 4 for j in want), (p0, p1, j0)
