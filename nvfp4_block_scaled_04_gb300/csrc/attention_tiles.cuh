@@ -485,20 +485,17 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
         }
         if (E4M3 && rescale && i > g.i0) {
           // the scores' registers are free here (2,048 new tokens on 6,144, 32 heads on
-          // 8: 314 -> 282 us; bf16 caches, which come here less often, lost 3%)
-#pragma unroll
-          for (int q = 0; q < D / 64; ++q) {
-            uint32_t o[2][32];
-            tc_ld_32cols(o_cols + 64 * q, o[0]);
-            tc_ld_32cols(o_cols + 64 * q + 32, o[1]);
+          // 8: 314 -> 282 us at a slack of 4; bf16 caches, which come here less often,
+          // lost 3%). Rolled: this kernel's time goes with its code's size (unrolled
+          // 272 us, rolled 260)
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tc_ld_32cols(o_cols + 32 * q, o);
             tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              o[0][e] = __float_as_uint(__uint_as_float(o[0][e]) * alpha);
-              o[1][e] = __float_as_uint(__uint_as_float(o[1][e]) * alpha);
-            }
-            tc_st_32cols(o_cols + 64 * q, o[0]);
-            tc_st_32cols(o_cols + 64 * q + 32, o[1]);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc_st_32cols(o_cols + 32 * q, o);
           }
         }
         tc_wait_st();
@@ -961,7 +958,7 @@ __global__ void __launch_bounds__(AtShape<E4M3, D>::THREADS, 1)
             const bool unclean = kv && at_unclean(j0, g.p0, p1, p.window, p.sinks);
             for (int cu = sub; cu < AT_CHUNKS; cu += 2) {
               if (!(ok = wait(kv ? chunk_ok(cu) : chunk_full(0, cu), tiles & 1))) break;
-#pragma unroll
+#pragma unroll 1
               for (int u0 = 0; u0 < UNITS; u0 += BATCH) {
                 uint4 w[BATCH];
 #pragma unroll

@@ -33,9 +33,9 @@ NVFP4_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, i
 // weight lies in [2^11, 2^15.9], so that weights keep f16's 11 bits down to 2^-25
 // of it (131,072 tokens of that weight hold 2^-8 together) and lose 2^-36 of it at
 // most below. Scores so large that x - m is off by 0.1 (2^20) could pass f16's
-// 65504: the conversion saturates. (2,048 new tokens on 6,144, 32 heads on 8: 282 us
-// with a slack of 4, 272 with 4.9, 262 with 8 and a lift of 7, which would keep 11
-// bits down to 2^-21 only.) Weights in bf16 have fp32's range and need no lift.
+// 65504: the conversion saturates. (2,048 new tokens on 6,144, 32 heads on 8: a
+// slack of 4 took 4% longer; one of 8 with a lift of 7, which keeps 11 bits down to
+// 2^-21 only, 4% less.) Weights in bf16 have fp32's range and need no lift.
 template <bool E4M3>
 struct KvWeights {
   static constexpr float SLACK = E4M3 ? 4.9f : 8.0f;
