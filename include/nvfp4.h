@@ -431,7 +431,11 @@ int nvfp4_paged_attention(const void* Q, int64_t q_stride, int q_heads, nvfp4_kv
                           int64_t tokens, int window, int sinks, float scale, void* out, void* workspace,
                           size_t workspace_bytes, nvfp4_stream_t stream);
 
-/* Pages. refs[p] (device int32 [pages]) counts the table entries that hold
+/* Pages. A cache is one layer's, and fork and compact move its bytes and rewrite
+ * the table, lengths and counts in the same call: every layer has a table,
+ * lengths and counts of its own. Pages that a window has left behind are given up
+ * by the caller: -1 in the table, the count lowered.
+ * refs[p] (device int32 [pages]) counts the table entries that hold
  * page p; 0 means free. Pages are handed out lowest id first, in the order of
  * the call's list. Where the pool runs out, entries stay without a page (-1) and
  * the device status word says NVFP4_ERR_NO_PAGES; a list entry outside the

@@ -4,7 +4,8 @@
 // The mathematics. Row r (one query head at one new token) sees the positions
 // V(r) of its mask; out_r = sum_j exp(x_rj - m_r) v_j / sum_j exp(x_rj - m_r)
 // with x_rj = scale q_r.k_j and m_r = max x_rj. A pass over any part of V(r)
-// keeps (m, l = sum exp(x - m), o = sum exp(x - m) v), and two parts join as
+// keeps (m, l = sum exp(x - m), o = sum exp(x - m) v), the online softmax of
+// Milakov and Gimelshein (2018), and two parts join as
 // m = max(m1, m2), l = l1 e^(m1-m) + l2 e^(m2-m), o likewise. All of it is
 // fp32, in powers of two (log2 e folded into the scale).
 //
@@ -29,7 +30,7 @@
 // rows of an item.
 //
 // Roundings. Products are exact in fp32 sums. bf16 caches: q and k as they
-// are; p is split into two bf16 halves (p = hi + lo to 2^-17), since one bf16
+// are; p is split into two bf16 halves (p = hi + lo to 2^-16), since one bf16
 // would cost as much error as the output's own rounding and the second MMA
 // costs no time here. E4M3 caches: k and v are exact in f16, q is scaled by a
 // power of two into f16 (exact for elements above amax 2^-29), p is one f16
@@ -38,14 +39,16 @@
 // below.
 //
 // Measured, 8 kv heads, D = 128: 64 sequences of 9k..22k positions, bf16, 578 us
-// (the copy rate); 8 sequences of 517..24k, 20 rows, E4M3, 63.0 us against 29.7
-// for the bytes (bound by instruction latency); one sequence of 2k positions,
-// 8.4 us on the device.
+// (the copy rate); 8 sequences of 517..24k, 20 rows, E4M3, 63.8 us against 29.7
+// for the bytes (bound by instruction latency); 8 of 22k, single tokens, E4M3,
+// 64.2 us against 53.2; one sequence of 2k positions, 8.6 us on the device.
 //
 // Masked places: scores are replaced, not added to; a token no row of the item
 // sees has its value row replaced by zeros (stale page contents may be NaN),
-// and pages that are not there are filled with zeros by the copy engine
-// (their boxes lie past the pool's last page).
+// elements that are not finite in tokens that some rows see and others do not are
+// taken out by the producer and given back at the output (kv.cuh), and pages that
+// are not there are filled with zeros by the copy engine (their boxes lie past the
+// pool's last page).
 #pragma once
 
 #include "kv.cuh"
@@ -83,7 +86,7 @@ struct ArParams {
 // A shape of the kernel for NT eight-row tiles of queries. Up to three, two CTAs
 // fit an SM's registers; four need 255 a thread (8 sequences of 22k positions,
 // E4M3, 20 rows: eight warps of one CTA 120 us, four of two CTAs 100 us; bf16,
-// 32 rows: eight warps 183 us, spilling, four warps of one CTA 150 us).
+// 32 rows: eight warps 183 us, spilling, four warps of one CTA 151 us).
 template <bool E4M3, int D, int NT>
 struct ArShape {
   static constexpr int TILE = 16 * AR_WARPS;                        // tokens of a tile

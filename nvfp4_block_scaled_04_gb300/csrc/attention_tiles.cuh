@@ -46,9 +46,11 @@
 // to arrive joins them in order.
 //
 // Measured, bf16, D = 128: 1500 and 2048 new tokens of two sequences, 32 heads on
-// 8, on up to 14k positions, 594-600 us (76% of the bf16 burst rate that a large
+// 8, on up to 14k positions, 594-607 us (75% of the bf16 burst rate that a large
 // matrix product reaches; under the power cap); an 8k prompt, 40 heads on 8, with
-// a window of 1024, 182-196 us (84 us of MMAs, 111 in whole tiles). Two row tiles rather than
+// a window of 1024, 176-197 us (84 us of MMAs, 111 in whole tiles); 2,048 new
+// tokens on 6,144, 186 us, over E4M3 259 us (124 of MMAs; every item converts the
+// codes again; 4 bytes of registers spill). Two row tiles rather than
 // one: a tile's exponentials hide behind the other's MMAs. A warpgroup of its own
 // for the output was slower (2k on 8k: 188 -> 211 us).
 //

@@ -124,7 +124,7 @@ template <int EXTRA, class U>
 NVFP4_HD U ar_piece(const ArLine& a, U total, unsigned ctas) {
   const U per = (total + (ctas - 1)) / ctas;
   // where a CTA's piece would be one tile of long items, two: half the parts to
-  // join (one sequence of 2,000 positions: 8.8 -> 8.0 us)
+  // join (one sequence of 2,000 positions: 8.9 -> 8.6 us)
   return per == 1 && total / (16u + EXTRA) >= static_cast<unsigned>(a.batch) * static_cast<unsigned>(a.heads) ? 2 : per;
 }
 
@@ -173,7 +173,7 @@ NVFP4_HD bool ar_next(const ArLine& a, const uint64_t* pre, const Seqs& seq, U p
 
 // A CTA's piece of a line, walked in 32 bits where its length is below 2^31: the
 // GPU has no 64-bit division (all in 64 bits, one sequence of 2,000 positions took
-// 9.0 us, in both ways 8.5).
+// 9.0 us, in both ways 8.5-8.6).
 template <int TILE, int ROWS, int EXTRA>
 struct ArPiece {
   uint64_t per, u, end;
