@@ -102,6 +102,7 @@ typedef struct nvfp4_tensor {
 #define NVFP4_OP_GROUPED_GEMM_W4A4 6
 #define NVFP4_OP_PAGED_ATTENTION 7
 #define NVFP4_OP_KV_PAGES        8
+#define NVFP4_OP_RMS_NORM_QUANTIZE 9
 
 /* ---- entry points ----------------------------------------------------------- */
 
@@ -469,6 +470,61 @@ int nvfp4_kv_release(int32_t* table, int64_t table_stride, int max_pages, int32_
 int nvfp4_kv_compact(nvfp4_kv_cache_t cache, int32_t* table, int64_t table_stride, int max_pages, int rows,
                      int32_t* refs, int32_t* live, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
 
+/* ---- norm in front of a linear ------------------------------------------------- */
+
+/* The rows of a root-mean-square norm: tokens * heads rows of K elements.
+ *   s = x + residual              (rounded to the residual's type; s = x without one)
+ *   y = s / sqrt(mean(s^2) + eps) * (weight + weight_offset)
+ * in fp32, the norm that of s as it is stored.
+ *   x         device bf16: token t's rows [heads][K] start at x + t * x_stride
+ *             elements (e.g. the query heads inside a fused projection's
+ *             output); x_stride >= heads * K, a multiple of 8
+ *   weight    device bf16 [K]; NULL: a gain of 1 (weight_offset ignored)
+ *   residual  device [tokens][heads][K], bf16 or fp32 (residual_dtype); NULL: none
+ *   residual_out  device, like residual: receives s; may be residual itself.
+ *             NULL exactly if residual is
+ *   K         a multiple of 8 (NVFP4 output: of 16), at most 32768
+ *   tokens * heads <= 2^30; eps >= 0, finite.
+ * All base pointers 16-byte aligned. Sums of squares are fp32: rows whose mean
+ * square lies above 2^127 / K give zeros. A NaN in a row makes the row NaN. */
+typedef struct nvfp4_norm {
+  const void* x;
+  const void* weight;
+  const void* residual;
+  void* residual_out;
+  int64_t tokens;
+  int64_t x_stride;
+  int32_t heads;
+  int32_t K;
+  int32_t residual_dtype;   /* NVFP4_DTYPE_BF16 or NVFP4_DTYPE_F32 (ignored without a residual) */
+  float eps;
+  float weight_offset;
+  int32_t reserved;         /* 0 */
+} nvfp4_norm_t;
+
+/* y as bf16, for the W4A16 linears, attention and the heads.
+ *   Y  device bf16: token t's rows at Y + t * y_stride elements (>= heads * K,
+ *      a multiple of 8); may be x itself with the same stride. */
+int nvfp4_rms_norm(nvfp4_norm_t in, void* Y, int64_t y_stride, nvfp4_stream_t stream);
+
+/* y as E4M3 with one scale for each row, for linears kept in 8 bits:
+ *   scales[row] = max|y| / 448 (1 for a row of zeros), codes = y / scales[row]
+ * rounded to nearest even. A NaN of y is the code 0x7F.
+ *   codes   device out uint8 [tokens][heads][K], 16-byte aligned
+ *   scales  device out fp32 [tokens * heads] */
+int nvfp4_rms_norm_e4m3(nvfp4_norm_t in, uint8_t* codes, float* scales, nvfp4_stream_t stream);
+
+/* y as NVFP4, the input of a W4A4 linear: the codes and scales that
+ * nvfp4_quantize gives for y in fp32, with no y in memory between the two.
+ *   codes, scales, s_t, s_t_mode, scale_layout  as for nvfp4_quantize, of
+ *      tokens * heads rows; padding bytes of the MMA layout are written as zero.
+ *      GIVEN is one pass. COMPUTE finds s_t first and forms y again from s (or
+ *      x), which must not change before the call has finished.
+ *   workspace  >= nvfp4_workspace_size(NVFP4_OP_RMS_NORM_QUANTIZE, tokens * heads, ...)
+ *      bytes, 16-byte aligned (COMPUTE only; may be NULL for GIVEN); scratch. */
+int nvfp4_rms_norm_quantize(nvfp4_norm_t in, uint8_t* codes, uint8_t* scales, float* s_t, int s_t_mode,
+                            int scale_layout, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
 /* ---- helpers --------------------------------------------------------------- */
 
 /* Bytes of one matrix's block scales in the given layout. */
@@ -483,7 +539,8 @@ size_t nvfp4_scales_bytes(int64_t rows, int64_t K, int scale_layout);
  *   GEMM_W4A4_QUANT: (M, N, K, -, -)
  *   GROUPED_GEMM_W4A4: (T, H, I, E, topk)
  *   PAGED_ATTENTION: (batch, max_new, q_heads, kv_heads, head_dim)
- *   KV_PAGES:      (pages, batch, -, -, -) */
+ *   KV_PAGES:      (pages, batch, -, -, -)
+ *   RMS_NORM_QUANTIZE: (rows, -, -, -, -) */
 size_t nvfp4_workspace_size(int op, int64_t a, int64_t b, int64_t c, int64_t e, int64_t topk);
 
 /* Human-readable name of a status code (static storage). */

@@ -22,7 +22,7 @@ DTYPE_F32, DTYPE_BF16, DTYPE_E4M3 = 0, 1, 2
 ST_COMPUTE, ST_GIVEN = 0, 1
 SCALES_ROWMAJOR, SCALES_MMA = 0, 1
 (OP_QUANTIZE, OP_GEMM_W4A16, OP_GEMM_W4A4, OP_GROUPED_GEMM, OP_GATHER_ARGMAX, OP_GEMM_W4A4_QUANT,
- OP_GROUPED_GEMM_W4A4, OP_PAGED_ATTENTION, OP_KV_PAGES) = range(9)
+ OP_GROUPED_GEMM_W4A4, OP_PAGED_ATTENTION, OP_KV_PAGES, OP_RMS_NORM_QUANTIZE) = range(10)
 
 EXPORTS = [
     "nvfp4_quantize", "nvfp4_prepack_scales", "nvfp4_gemm_w4a16", "nvfp4_gemm_w4a4",
@@ -32,7 +32,7 @@ EXPORTS = [
     "nvfp4_gemm_w4a16_noalloc", "nvfp4_verify_accept", "nvfp4_probe_fp4_mma_rate",
     "nvfp4_gemm_w4a16_silu_mul", "nvfp4_gemm_w4a4_quant", "nvfp4_grouped_gemm_w4a4",
     "nvfp4_kv_append", "nvfp4_paged_attention", "nvfp4_kv_reserve", "nvfp4_kv_fork", "nvfp4_kv_release",
-    "nvfp4_kv_compact",
+    "nvfp4_kv_compact", "nvfp4_rms_norm", "nvfp4_rms_norm_e4m3", "nvfp4_rms_norm_quantize",
 ]
 _NON_INT = ("nvfp4_scales_bytes", "nvfp4_workspace_size", "nvfp4_status_string")
 
@@ -56,6 +56,14 @@ class CKVSeqs(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("start", ctypes.c_void_p),
                 ("table_stride", ctypes.c_int64), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("max_new", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class CNorm(ctypes.Structure):
+    """Mirror of nvfp4_norm_t."""
+    _fields_ = [("x", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("residual_out", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("K", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -89,6 +97,9 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_kv_fork.argtypes = [CKVCache, vp, i64, i32, vp, i32, vp, vp, vp, i32, vp]
         L.nvfp4_kv_release.argtypes = [vp, i64, i32, vp, i32, vp, i64, vp, i32, vp]
         L.nvfp4_kv_compact.argtypes = [CKVCache, vp, i64, i32, i32, vp, vp, vp, sz, vp]
+        L.nvfp4_rms_norm.argtypes = [CNorm, vp, i64, vp]
+        L.nvfp4_rms_norm_e4m3.argtypes = [CNorm, vp, vp, vp]
+        L.nvfp4_rms_norm_quantize.argtypes = [CNorm, vp, vp, vp, i32, i32, vp, sz, vp]
         L.nvfp4_scales_bytes.argtypes = [i64, i64, i32]
         L.nvfp4_scales_bytes.restype = sz
         L.nvfp4_workspace_size.argtypes = [i32, i64, i64, i64, i64, i64]
@@ -570,6 +581,109 @@ def kv_compact(cache: KVCache, table: torch.Tensor, refs: torch.Tensor,
     _check(lib().nvfp4_kv_compact(c, *args, table.shape[0], refs.data_ptr(), live.data_ptr(), ws.data_ptr(),
                                   ws.numel(), _stream()), "nvfp4_kv_compact")
     return live
+
+
+def _beside(x, *ts):
+    """x on the current device, and every tensor of ts beside it."""
+    d = x.device
+    if d.type != "cuda":
+        _require_cuda(x)
+    if d.index != torch.cuda.current_device():
+        raise RuntimeError("nvfp4: tensors must live on the current device")
+    for t in ts:
+        if t is not None and t.device != d:
+            raise RuntimeError("nvfp4: tensors must live on one CUDA device (no CPU path exists)")
+
+
+def _norm(x, weight, eps, residual, residual_out, weight_offset):
+    """(x as the kernels take it, its CNorm, the stream that goes on or None)"""
+    shape = x.shape
+    if x.dtype != torch.bfloat16 or len(shape) not in (2, 3):
+        raise ValueError("rms_norm: x is bf16 [rows][K] or [tokens][heads][K]")
+    _beside(x, weight, residual, residual_out)
+    K, heads = shape[-1], shape[1] if len(shape) == 3 else 1
+    row = heads * K
+    st = x.stride()
+    stride = st[0] if shape[0] > 1 else row
+    if (st[-1] != 1 and K > 1) or (heads > 1 and st[1] != K) or stride % 8 or stride < row or x.data_ptr() % 16:
+        x, stride = x.clone(memory_format=torch.contiguous_format), row
+    w = None
+    if weight is not None:
+        if weight.dtype != torch.bfloat16 or weight.shape != shape[-1:] or not weight.is_contiguous():
+            raise ValueError("rms_norm: weight is contiguous bf16 [K]")
+        w = weight.data_ptr()
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("rms_norm: residual_out needs a residual")
+        return x, CNorm(x.data_ptr(), w, None, None, shape[0], stride, heads, K, DTYPE_BF16, eps, weight_offset, 0), None
+    if residual_out is None:
+        residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+    for t in (residual, residual_out):
+        if t.shape != shape or t.dtype != residual.dtype or not t.is_contiguous():
+            raise ValueError("rms_norm: residual and residual_out are contiguous, of x's shape and of one type")
+    if residual.dtype != torch.bfloat16 and residual.dtype != torch.float32:
+        raise ValueError("rms_norm: a residual is bf16 or fp32")
+    return x, CNorm(x.data_ptr(), w, residual.data_ptr(), residual_out.data_ptr(), shape[0], stride, heads, K,
+                    DTYPE_BF16 if residual.dtype == torch.bfloat16 else DTYPE_F32, eps, weight_offset, 0), residual_out
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+             residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+             weight_offset: float = 0.0, out: torch.Tensor | None = None):
+    """y = s / sqrt(mean(s^2) + eps) * (weight + weight_offset), s = x + residual; bf16.
+    x [rows][K], or [tokens][heads][K] (each head by itself; slices of a fused
+    projection are read in place). With a residual (bf16 or fp32): (y, s), s in
+    residual_out (a new tensor if None; may be residual). out may be x."""
+    x0 = x
+    x, c, s = _norm(x, weight, eps, residual, residual_out, weight_offset)
+    row = c.heads * c.K
+    if out is None:
+        out = torch.empty(x0.shape, dtype=x0.dtype, device=x0.device)
+        stride = row
+    else:
+        st = out.stride()
+        stride = st[0] if x0.shape[0] > 1 else row
+        if out.shape != x0.shape or out.dtype != torch.bfloat16 or st[-1] != 1 or (c.heads > 1 and st[1] != c.K):
+            raise ValueError("out: bf16 of x's shape, rows contiguous, is needed")
+        _beside(x, out)
+    _check(lib().nvfp4_rms_norm(c, out.data_ptr(), stride, _stream()), "nvfp4_rms_norm")
+    return out if s is None else (out, s)
+
+
+def rms_norm_e4m3(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                  residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                  weight_offset: float = 0.0):
+    """rms_norm's y as float8_e4m3fn codes of x's shape and fp32 scales [rows] (y = code * scale of its row):
+    (codes, scales), with a residual (codes, scales, s)."""
+    x, c, s = _norm(x, weight, eps, residual, residual_out, weight_offset)
+    codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    scales = torch.empty(c.tokens * c.heads, dtype=torch.float32, device=x.device)
+    _check(lib().nvfp4_rms_norm_e4m3(c, codes.data_ptr(), scales.data_ptr(), _stream()), "nvfp4_rms_norm_e4m3")
+    return (codes, scales) if s is None else (codes, scales, s)
+
+
+def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                      residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                      weight_offset: float = 0.0, s_t: torch.Tensor | None = None, scale_layout: int = SCALES_MMA,
+                      workspace: torch.Tensor | None = None):
+    """rms_norm's y as NVFP4 (a QTensor of tokens * heads rows), the input of a W4A4 linear; with a residual
+    (QTensor, s). s_t None -> computed from y (amax / 2688); else a 1-element fp32 tensor to use."""
+    x, c, s = _norm(x, weight, eps, residual, residual_out, weight_offset)
+    rows, K, dev = c.tokens * c.heads, c.K, x.device
+    codes = torch.empty(rows, K // 2, dtype=torch.uint8, device=dev)
+    scales = torch.empty(max(scales_bytes(rows, K, scale_layout), 1), dtype=torch.uint8, device=dev)
+    if s_t is None:
+        st, mode = torch.empty(1, dtype=torch.float32, device=dev), ST_COMPUTE
+        ws = _given_ws(workspace) if workspace is not None else _workspace(workspace_size(OP_RMS_NORM_QUANTIZE, rows), dev)
+    else:
+        st, mode, ws = s_t.to(device=dev, dtype=torch.float32).reshape(1).contiguous(), ST_GIVEN, None
+    _check(lib().nvfp4_rms_norm_quantize(c, codes.data_ptr(), scales.data_ptr(), st.data_ptr(), mode, scale_layout,
+                                         _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
+           "nvfp4_rms_norm_quantize")
+    if scale_layout == SCALES_ROWMAJOR:
+        scales = scales[: rows * (K // 16)].view(rows, K // 16)
+    q = QTensor(codes, scales, st, rows, K, 1, scale_layout)
+    return q if s is None else (q, s)
 
 
 def read_device_status() -> int:

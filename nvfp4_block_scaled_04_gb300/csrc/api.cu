@@ -91,6 +91,24 @@ int pages_ws_check(const void* ws, size_t bytes, int64_t pages, int64_t n) {
   return aligned16(ws) ? NVFP4_OK : NVFP4_ERR_MISALIGNED;
 }
 
+// the rows of a norm: NVFP4_OK or what is wrong with them (granule: of K)
+int norm_check(const nvfp4_norm_t& n, int granule) {
+  if (n.tokens < 0 || n.heads < 1 || n.K < 1 || n.reserved != 0) return NVFP4_ERR_INVALID_ARG;
+  if (!(n.eps >= 0.0f) || !(n.eps - n.eps == 0.0f) || !(n.weight_offset - n.weight_offset == 0.0f))
+    return NVFP4_ERR_INVALID_ARG;
+  if ((n.residual == nullptr) != (n.residual_out == nullptr)) return NVFP4_ERR_INVALID_ARG;
+  if (n.residual && n.residual_dtype != NVFP4_DTYPE_BF16 && n.residual_dtype != NVFP4_DTYPE_F32)
+    return NVFP4_ERR_INVALID_ARG;
+  if (n.K % granule != 0 || n.K > 32768) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (n.tokens > (1ll << 30) / n.heads) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (n.tokens == 0) return NVFP4_OK;
+  if (!n.x || n.x_stride < static_cast<int64_t>(n.heads) * n.K) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(n.x) || n.x_stride % 8 != 0 || !aligned16(n.weight) || !aligned16(n.residual) ||
+      !aligned16(n.residual_out))
+    return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
 }  // namespace
 }  // namespace nvfp4
 
@@ -133,6 +151,7 @@ size_t nvfp4_workspace_size(int op, int64_t a, int64_t b, int64_t c, int64_t e, 
     case NVFP4_OP_GATHER_ARGMAX: return a > 0 && c > 0 ? argmax_workspace_bytes(a, c) : 0;
     case NVFP4_OP_PAGED_ATTENTION: return attention_workspace_bytes(a, b, c, e, topk);
     case NVFP4_OP_KV_PAGES: return kv_pages_workspace_bytes(a, b);
+    case NVFP4_OP_RMS_NORM_QUANTIZE: return norm_workspace_bytes(a);
     default: return 0;
   }
 }
@@ -385,6 +404,39 @@ int nvfp4_kv_compact(nvfp4_kv_cache_t cache, int32_t* table, int64_t table_strid
   if (int rc = pages_ws_check(workspace, workspace_bytes, cache.pages, 0)) return rc;
   return launch_kv_compact(cache, table, table_stride, max_pages, rows, refs, live, workspace,
                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_rms_norm(nvfp4_norm_t in, void* Y, int64_t y_stride, nvfp4_stream_t stream) {
+  if (int rc = norm_check(in, 8)) return rc;
+  if (in.tokens == 0) return NVFP4_OK;
+  if (!Y || y_stride < static_cast<int64_t>(in.heads) * in.K) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(Y) || y_stride % 8 != 0) return NVFP4_ERR_MISALIGNED;
+  return launch_rms_norm(in, Y, y_stride, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_rms_norm_e4m3(nvfp4_norm_t in, uint8_t* codes, float* scales, nvfp4_stream_t stream) {
+  if (int rc = norm_check(in, 8)) return rc;
+  if (in.tokens == 0) return NVFP4_OK;
+  if (!codes || !scales) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(codes)) return NVFP4_ERR_MISALIGNED;
+  return launch_rms_norm_e4m3(in, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_rms_norm_quantize(nvfp4_norm_t in, uint8_t* codes, uint8_t* scales, float* s_t, int s_t_mode,
+                            int scale_layout, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream) {
+  if (int rc = norm_check(in, 16)) return rc;
+  if (!s_t || (s_t_mode != NVFP4_ST_COMPUTE && s_t_mode != NVFP4_ST_GIVEN)) return NVFP4_ERR_INVALID_ARG;
+  if (scale_layout != NVFP4_SCALES_ROWMAJOR && scale_layout != NVFP4_SCALES_MMA) return NVFP4_ERR_INVALID_ARG;
+  if (in.tokens > 0 && (!codes || !scales)) return NVFP4_ERR_INVALID_ARG;
+  if (in.tokens > 0 && !aligned16(codes)) return NVFP4_ERR_MISALIGNED;
+  if (s_t_mode == NVFP4_ST_COMPUTE) {
+    if (!workspace || workspace_bytes < norm_workspace_bytes(in.tokens * in.heads)) return NVFP4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
+  } else if (in.tokens == 0) {
+    return NVFP4_OK;
+  }
+  return launch_rms_norm_quantize(in, codes, scales, s_t, s_t_mode, scale_layout, workspace,
+                                  reinterpret_cast<cudaStream_t>(stream));
 }
 
 int nvfp4_read_device_status(int* out, nvfp4_stream_t stream) {

@@ -139,6 +139,13 @@ int launch_grouped_w4a4(bool gateup, const uint8_t* a_codes, const uint8_t* a_sc
                         uint16_t* h_out, unsigned int* amax_bits, uint16_t* y_out, int64_t out_rows, bool pair,
                         cudaStream_t stream);
 
+// ---- norm.cu
+size_t norm_workspace_bytes(int64_t rows);
+int launch_rms_norm(const nvfp4_norm_t& n, void* y, int64_t y_stride, cudaStream_t stream);
+int launch_rms_norm_e4m3(const nvfp4_norm_t& n, uint8_t* codes, float* scales, cudaStream_t stream);
+int launch_rms_norm_quantize(const nvfp4_norm_t& n, uint8_t* codes, uint8_t* scales, float* s_t, int s_t_mode,
+                             int scale_layout, void* workspace, cudaStream_t stream);
+
 // ---- paged key-value cache (kv_cache.cu, attention.cu)
 // The sequences of a call (nvfp4_kv_seqs_t) and the number of rows that the
 // caller's arrays of new tokens hold. Lengths, page ids and offsets come from

@@ -1,0 +1,493 @@
+// Root-mean-square norm of bf16 rows, with the residual's addition in front and
+// the conversion to what the next linear takes behind:
+//   s = x + residual          (rounded to the residual's type and stored; s = x without one)
+//   t = s * (w + offset),  r = 1 / sqrt(mean(s^2) + eps),  y = t * r
+//   out: bf16 y | E4M3 codes of y / a with a = max|y| / 448 of the row | NVFP4 of y
+//
+// The gain goes in before the row's r, so the sum of squares and the largest
+// |t| come out of one reduction: rounding is monotone, so fl(max|t| * r) is
+// max|y| exactly, for a row (E4M3), a block of 16 (NVFP4) and the tensor.
+// Sums and all arithmetic are fp32; s is rounded because it is the stream that
+// the next layer reads, and the norm is that of the stored stream.
+//
+// Bound by HBM for many rows, by latency (one load, one reduction, one store)
+// for few. One row stays in registers between its only read and its only
+// write. Rows of up to 1024 elements (heads of 64 or 128 among them) belong to
+// 8, 16 or 32 lanes of a warp and need no block-wide step; longer rows to a CTA.
+#include "common.cuh"
+#include "launch.h"
+#include "quant_core.cuh"
+#include "tc_util.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+enum { OUT_BF16 = 0, OUT_E4M3 = 1, OUT_NVFP4 = 2, OUT_STATS = 3 };
+enum { RES_NONE = 0, RES_BF16 = 1, RES_F32 = 2 };
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* weight;
+  const void* residual;
+  void* residual_out;
+  int64_t x_stride;    // elements between tokens
+  int64_t y_stride;
+  int rows;            // tokens * heads
+  int heads;
+  int K;
+  float eps;
+  float offset;
+  void* out;           // bf16 rows, or codes
+  void* scales;        // fp32 [rows] (E4M3), block scales (NVFP4)
+  const float* s_t;    // NVFP4 with a given tensor scale
+  float* row_r;        // OUT_STATS: r of each row
+  unsigned int* partial;  // OUT_STATS: largest |y| (fp32 bits) of each CTA's rows
+  int64_t cols4;       // block-scale columns with their padding (MMA layout)
+  int rows_p;          // rows with their padding (MMA layout; else rows)
+  int mma;             // block scales in the MMA layout
+};
+
+// Byte of (row, 0) in the block scales, and the step from one column tile of four to the next.
+NVFP4_DEV int64_t mma_row_offset(int row, int64_t cols4) {
+  return static_cast<int64_t>(row >> 7) * (cols4 >> 2) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+
+NVFP4_DEV void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(w[e] << 16);
+    v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  }
+}
+
+NVFP4_DEV uint4 pack8(const float (&v)[8]) {
+  return make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
+                    f32x2_to_bf16x2(v[6], v[7]));
+}
+
+// The raw words of eight elements of a row: x, and the residual's.
+template <int RES>
+struct Raw {
+  uint4 x;
+  uint4 r[RES == RES_F32 ? 2 : 1];
+};
+
+template <int RES>
+NVFP4_DEV void load_raw(const uint16_t* x, const void* residual, int64_t at, Raw<RES>& raw) {
+  raw.x = *reinterpret_cast<const uint4*>(x);
+  if (RES == RES_BF16) raw.r[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(residual) + at);
+  if (RES == RES_F32) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(residual) + at);
+    raw.r[0] = p[0];
+    raw.r[RES == RES_F32 ? 1 : 0] = p[1];
+  }
+}
+
+// s of eight elements, stored to residual_out on the way.
+template <int RES>
+NVFP4_DEV void stream8(const Raw<RES>& raw, void* residual_out, int64_t at, float (&s)[8]) {
+  unpack8(raw.x, s);
+  if (RES == RES_BF16) {
+    float r[8];
+    unpack8(raw.r[0], r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += r[e];
+    const uint4 u = pack8(s);   // 24 bits hold the sum of two bf16 well enough for one rounding to be exact
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(residual_out) + at) = u;
+    unpack8(u, s);
+  }
+  if (RES == RES_F32) {
+    const uint32_t w[8] = {raw.r[0].x, raw.r[0].y, raw.r[0].z, raw.r[0].w, raw.r[RES == RES_F32 ? 1 : 0].x,
+                           raw.r[RES == RES_F32 ? 1 : 0].y, raw.r[RES == RES_F32 ? 1 : 0].z,
+                           raw.r[RES == RES_F32 ? 1 : 0].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += __uint_as_float(w[e]);
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(residual_out) + at);
+    p[0] = make_float4(s[0], s[1], s[2], s[3]);
+    p[1] = make_float4(s[4], s[5], s[6], s[7]);
+  }
+}
+
+// t = s * gain
+NVFP4_DEV void gain8(const uint16_t* weight, float offset, int k, float (&s)[8]) {
+  if (weight) {
+    float w[8];
+    unpack8(__ldg(reinterpret_cast<const uint4*>(weight + k)), w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] *= w[e] + offset;
+  }
+}
+
+NVFP4_DEV float amax8(const float (&t)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(t[e]));
+  return m;
+}
+
+// Codes and block scale of eight elements of a block whose other eight are in
+// the neighbouring lane (lanes 2j, 2j + 1; both run this): the decisions of
+// the quantiser on y.
+struct TensorScale {
+  float st, d, rdh, rdl;
+};
+
+NVFP4_DEV TensorScale tensor_scale(float st) {
+  TensorScale ts;
+  ts.st = st;
+  ts.d = __fmul_rn(st, 6.0f);
+  recip_brackets(ts.d, ts.rdh, ts.rdl);
+  return ts;
+}
+
+NVFP4_DEV uint32_t quant8(const float (&y)[8], const TensorScale& ts, uint32_t& scale) {
+  float ab = amax8(y);
+  ab = fmaxf(ab, __shfl_xor_sync(3u << (threadIdx.x & 30), ab, 1));
+  scale = block_scale_code(ab, ts.d, ts.rdh, ts.rdl);
+  if (scale == 0) return 0u;
+  return e2m1x8(y, __fmul_rn(e4m3_to_f32(scale), ts.st));
+}
+
+// Writes eight elements of y = t * r (k: their first column).
+template <int OUT>
+NVFP4_DEV void store8(const NormArgs& a, int row, int64_t y_at, int k, float (&t)[8], float r, float inv, const TensorScale* ts) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] *= r;
+  if (OUT == OUT_BF16) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + y_at + k) = pack8(t);
+  if (OUT == OUT_E4M3) {
+    uint2 c;
+    c.x = f32x2_to_e4m3x2(t[0] * inv, t[1] * inv) | f32x2_to_e4m3x2(t[2] * inv, t[3] * inv) << 16;
+    c.y = f32x2_to_e4m3x2(t[4] * inv, t[5] * inv) | f32x2_to_e4m3x2(t[6] * inv, t[7] * inv) << 16;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + static_cast<int64_t>(row) * a.K + k) = c;
+  }
+  if (OUT == OUT_NVFP4) {
+    uint32_t sc;
+    const uint32_t codes = quant8(t, *ts, sc);
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row) * a.K + k) / 2) = codes;
+    const int b = k >> 4;
+    if ((k & 8) == 0)
+      static_cast<uint8_t*>(a.scales)[a.mma ? mma_row_offset(row, a.cols4) + (b >> 2) * 512 + (b & 3)
+                                            : static_cast<int64_t>(row) * (a.K >> 4) + b] = static_cast<uint8_t>(sc);
+  }
+}
+
+// The scale columns behind the last block of a row, and the rows behind the last one, are zero (MMA layout).
+NVFP4_DEV void pad_scales(const NormArgs& a, int row, int first, int lane, int lanes) {
+  uint8_t* p = static_cast<uint8_t*>(a.scales) + mma_row_offset(row, a.cols4);
+  for (int c = first + lane; c < a.cols4; c += lanes) p[static_cast<int64_t>(c >> 2) * 512 + (c & 3)] = 0;
+}
+
+// The row's E4M3 scale a = max|y| / 448 (1 for a row of zeros) and what y is multiplied with.
+NVFP4_DEV float e4m3_row_scale(float most, float& inv) {
+  const float a = most > 0.f ? __fdiv_rn(most, 448.0f) : 1.0f;
+  inv = __fdiv_rn(1.0f, a);
+  return a;
+}
+
+NVFP4_DEV float rms_r(float sum, const NormArgs& a) { return rsqrtf(sum / static_cast<float>(a.K) + a.eps); }
+
+// ---- a row for TPR lanes of a warp: K <= 8 * TPR * VPT
+template <int OUT, int RES, int TPR, int VPT>
+__global__ void __launch_bounds__(256) norm_lanes_kernel(const NormArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & (TPR - 1);
+  const int per_cta = 256 / TPR;
+  const int nvec = a.K >> 3;
+  const TensorScale ts = tensor_scale(OUT == OUT_NVFP4 ? *a.s_t : 1.0f);
+  float most_all = 0.f;
+  // (all lanes of a warp walk the same number of rows: the reductions are warp-wide)
+  for (int row0 = blockIdx.x * per_cta; row0 < a.rows_p; row0 += gridDim.x * per_cta) {
+    const int row = row0 + threadIdx.x / TPR;
+    const bool live = row < a.rows;
+    const int token = live ? row / a.heads : 0, head = live ? row - token * a.heads : 0;
+    const uint16_t* xr = a.x + token * a.x_stride + static_cast<int64_t>(head) * a.K;
+    const int64_t base = static_cast<int64_t>(row) * a.K;
+    Raw<RES> raw[VPT];
+    float t[VPT][8], sum = 0.f, most = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = lane + i * TPR;
+      if (live && v < nvec) load_raw<RES>(xr + v * 8, a.residual, base + v * 8, raw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = lane + i * TPR;
+      if (live && v < nvec) {
+        stream8<RES>(raw[i], a.residual_out, base + v * 8, t[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(t[i][e], t[i][e], sum);
+        gain8(a.weight, a.offset, v * 8, t[i]);
+        if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, amax8(t[i]));
+      }
+    }
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    const float r = rms_r(sum, a);
+    float inv = 0.f;
+    if (OUT == OUT_E4M3) {
+      const float scale = e4m3_row_scale(most * r, inv);
+      if (live && lane == 0) static_cast<float*>(a.scales)[row] = scale;
+    }
+    if (OUT == OUT_STATS) {
+      if (live && lane == 0) a.row_r[row] = r;
+      if (live) most_all = fmaxf(most_all, most * r);
+      continue;
+    }
+    const int64_t y_at = token * a.y_stride + static_cast<int64_t>(head) * a.K;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = lane + i * TPR;
+      if (live && v < nvec) store8<OUT>(a, row, y_at, v * 8, t[i], r, inv, &ts);
+    }
+    if (OUT == OUT_NVFP4 && a.mma && row < a.rows_p) pad_scales(a, row, live ? a.K >> 4 : 0, lane, TPR);
+  }
+  if (OUT == OUT_STATS) {
+    __shared__ unsigned int s_most;
+    if (threadIdx.x == 0) s_most = 0u;
+    __syncthreads();
+    const unsigned int m = __reduce_max_sync(0xffffffffu, __float_as_uint(most_all));
+    if ((threadIdx.x & 31) == 0) atomicMax(&s_most, m);
+    __syncthreads();
+    if (threadIdx.x == 0) a.partial[blockIdx.x] = s_most;
+  }
+}
+
+// ---- a row for a CTA: K <= 8 * blockDim.x * VPT
+template <int OUT, int RES, int VPT>
+__global__ void __launch_bounds__(VPT > 1 ? 512 : 1024) norm_cta_kernel(const NormArgs a) {
+  __shared__ float s_sum[2][32], s_most[2][32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int nvec = a.K >> 3, warps = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const TensorScale ts = tensor_scale(OUT == OUT_NVFP4 ? *a.s_t : 1.0f);
+  float most_all = 0.f;
+  int turn = 0;
+  for (int row = blockIdx.x; row < a.rows_p; row += gridDim.x, turn ^= 1) {
+    if (row >= a.rows) {   // padding rows of the block scales (whole CTAs)
+      pad_scales(a, row, 0, threadIdx.x, blockDim.x);
+      continue;
+    }
+    const int token = row / a.heads, head = row - token * a.heads;
+    const uint16_t* xr = a.x + token * a.x_stride + static_cast<int64_t>(head) * a.K;
+    const int64_t base = static_cast<int64_t>(row) * a.K;
+    // (rows of more than 16384 elements: the loads of two or four vectors at a time, as registers allow)
+    constexpr int AT_ONCE = VPT < 8 ? VPT : RES == RES_F32 ? 2 : 4;
+    float t[VPT][8], sum = 0.f, most = 0.f;
+#pragma unroll
+    for (int i0 = 0; i0 < VPT; i0 += AT_ONCE) {
+      Raw<RES> raw[AT_ONCE];
+#pragma unroll
+      for (int i = i0; i < i0 + AT_ONCE; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v < nvec) load_raw<RES>(xr + v * 8, a.residual, base + v * 8, raw[i - i0]);
+      }
+#pragma unroll
+      for (int i = i0; i < i0 + AT_ONCE; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v < nvec) {
+          stream8<RES>(raw[i - i0], a.residual_out, base + v * 8, t[i]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum = fmaf(t[i][e], t[i][e], sum);
+          gain8(a.weight, a.offset, v * 8, t[i]);
+          if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, amax8(t[i]));
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    // (two sets of slots in turn: a warp that is a row ahead does not overwrite what a slower one still reads)
+    if (lane == 0) {
+      s_sum[turn][warp] = sum;
+      s_most[turn][warp] = most;
+    }
+    __syncthreads();
+    sum = lane < warps ? s_sum[turn][lane] : 0.f;
+    most = lane < warps ? s_most[turn][lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    const float r = rms_r(sum, a);
+    float inv = 0.f;
+    if (OUT == OUT_E4M3) {
+      const float scale = e4m3_row_scale(most * r, inv);
+      if (threadIdx.x == 0) static_cast<float*>(a.scales)[row] = scale;
+    }
+    if (OUT == OUT_STATS) {
+      if (threadIdx.x == 0) a.row_r[row] = r;
+      most_all = fmaxf(most_all, most * r);
+      continue;
+    }
+    const int64_t y_at = token * a.y_stride + static_cast<int64_t>(head) * a.K;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v < nvec) store8<OUT>(a, row, y_at, v * 8, t[i], r, inv, &ts);
+    }
+    if (OUT == OUT_NVFP4 && a.mma) pad_scales(a, row, a.K >> 4, threadIdx.x, blockDim.x);
+  }
+  if (OUT == OUT_STATS && threadIdx.x == 0) a.partial[blockIdx.x] = __float_as_uint(most_all);
+}
+
+// ---- the codes of a tensor whose scale had to be found first: y = s * (w + offset) * r is formed again
+// from the stream (or x) and each row's r, so both passes see the same y.
+template <bool F32>
+__global__ void __launch_bounds__(256) norm_encode_kernel(const NormArgs a, const void* s, int64_t s_stride, int n_partial,
+                                                          float* s_t) {
+  __shared__ unsigned int s_most;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) s_most = 0u;
+  __syncthreads();
+  unsigned int m = 0u;
+  for (int i = threadIdx.x; i < n_partial; i += blockDim.x) m = max(m, __ldcg(a.partial + i));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) atomicMax(&s_most, m);
+  __syncthreads();
+  const float amax = __uint_as_float(s_most);
+  const TensorScale ts = tensor_scale(amax > 0.f ? __fdiv_rn(amax, 2688.0f) : 1.0f);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *s_t = ts.st;
+  const int nvec = a.K >> 3;
+  for (int row = blockIdx.x; row < a.rows_p; row += gridDim.x) {
+    if (row >= a.rows) {
+      pad_scales(a, row, 0, threadIdx.x, blockDim.x);
+      continue;
+    }
+    const int token = row / a.heads, head = row - token * a.heads;
+    const int64_t at = token * s_stride + static_cast<int64_t>(head) * a.K;
+    const float r = a.row_r[row];
+    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+      float t[8];
+      if (F32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(s) + at + v * 8);
+        const float4 lo = p[0], hi = p[1];
+        t[0] = lo.x; t[1] = lo.y; t[2] = lo.z; t[3] = lo.w;
+        t[4] = hi.x; t[5] = hi.y; t[6] = hi.z; t[7] = hi.w;
+      } else {
+        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s) + at + v * 8), t);
+      }
+      gain8(a.weight, a.offset, v * 8, t);
+      store8<OUT_NVFP4>(a, row, 0, v * 8, t, r, 0.f, &ts);
+    }
+    if (a.mma) pad_scales(a, row, a.K >> 4, threadIdx.x, blockDim.x);
+  }
+}
+
+constexpr int PARTIALS = 2048;   // CTAs of a statistics pass at most
+
+// Launches the kernel for the rows' length; `grid` says how many CTAs it had.
+template <int OUT, int RES>
+int launch_rows(const NormArgs& a, int* grid, cudaStream_t stream) {
+  const int nvec = a.K / 8;
+  const int most = OUT == OUT_STATS ? PARTIALS : 1 << 30;
+  if (a.K <= 1024) {
+    const int tpr = nvec <= 8 ? 8 : nvec <= 16 ? 16 : 32, vpt = static_cast<int>(ceil_div(nvec, tpr));
+    const int64_t want = ceil_div(a.rows_p, 256 / tpr);
+    *grid = static_cast<int>(want < most ? want : most);
+#define NVFP4_LANES(T, V) return launch_ex(norm_lanes_kernel<OUT, RES, T, V>, dim3(*grid), dim3(256), 0, 1, true, stream, a)
+    if (tpr == 8) NVFP4_LANES(8, 1);
+    if (tpr == 16) NVFP4_LANES(16, 1);
+    if (vpt == 1) NVFP4_LANES(32, 1);
+    if (vpt == 2) NVFP4_LANES(32, 2);
+    NVFP4_LANES(32, 4);
+#undef NVFP4_LANES
+  }
+  // few rows: as many threads as a row has vectors of eight; many rows: four vectors a thread, so that
+  // more loads are in flight for each reduction
+  const int vpt = nvec > 2048 ? 8 : nvec > 1024 || a.rows >= 4 * sm_count() ? 4 : 1;
+  const int threads = static_cast<int>(ceil_div(ceil_div(nvec, vpt), 32) * 32);
+  *grid = a.rows_p < most ? a.rows_p : most;
+#define NVFP4_CTA(V) return launch_ex(norm_cta_kernel<OUT, RES, V>, dim3(*grid), dim3(threads), 0, 1, true, stream, a)
+  if (vpt == 1) NVFP4_CTA(1);
+  if (vpt == 4) NVFP4_CTA(4);
+  NVFP4_CTA(8);
+#undef NVFP4_CTA
+}
+
+template <int OUT>
+int launch_out(const NormArgs& a, int res, int* grid, cudaStream_t stream) {
+  if (res == RES_NONE) return launch_rows<OUT, RES_NONE>(a, grid, stream);
+  if (res == RES_BF16) return launch_rows<OUT, RES_BF16>(a, grid, stream);
+  return launch_rows<OUT, RES_F32>(a, grid, stream);
+}
+
+int res_of(const nvfp4_norm_t& n) {
+  return !n.residual ? RES_NONE : n.residual_dtype == NVFP4_DTYPE_F32 ? RES_F32 : RES_BF16;
+}
+
+NormArgs args_of(const nvfp4_norm_t& n) {
+  NormArgs a = {};
+  a.x = static_cast<const uint16_t*>(n.x);
+  a.weight = static_cast<const uint16_t*>(n.weight);
+  a.residual = n.residual;
+  a.residual_out = n.residual_out;
+  a.x_stride = n.x_stride;
+  a.heads = n.heads;
+  a.rows = static_cast<int>(n.tokens * n.heads);
+  a.rows_p = a.rows;
+  a.K = n.K;
+  a.eps = n.eps;
+  a.offset = n.weight_offset;
+  return a;
+}
+
+}  // namespace
+
+size_t norm_workspace_bytes(int64_t rows) { return PARTIALS * sizeof(unsigned int) + static_cast<size_t>(rows) * sizeof(float); }
+
+int launch_rms_norm(const nvfp4_norm_t& n, void* y, int64_t y_stride, cudaStream_t stream) {
+  NormArgs a = args_of(n);
+  a.out = y;
+  a.y_stride = y_stride;
+  int grid;
+  return launch_out<OUT_BF16>(a, res_of(n), &grid, stream);
+}
+
+int launch_rms_norm_e4m3(const nvfp4_norm_t& n, uint8_t* codes, float* scales, cudaStream_t stream) {
+  NormArgs a = args_of(n);
+  a.out = codes;
+  a.scales = scales;
+  int grid;
+  return launch_out<OUT_E4M3>(a, res_of(n), &grid, stream);
+}
+
+int launch_rms_norm_quantize(const nvfp4_norm_t& n, uint8_t* codes, uint8_t* scales, float* s_t, int s_t_mode,
+                             int scale_layout, void* workspace, cudaStream_t stream) {
+  NormArgs a = args_of(n);
+  a.out = codes;
+  a.scales = scales;
+  a.mma = scale_layout == NVFP4_SCALES_MMA;
+  a.cols4 = mma_scale_cols(n.K);
+  const int rows_p = a.mma ? static_cast<int>(mma_scale_rows(a.rows)) : a.rows;
+  int grid;
+  if (s_t_mode == NVFP4_ST_GIVEN) {
+    a.s_t = s_t;
+    a.rows_p = rows_p;
+    return launch_out<OUT_NVFP4>(a, res_of(n), &grid, stream);
+  }
+  a.partial = static_cast<unsigned int*>(workspace);
+  a.row_r = reinterpret_cast<float*>(a.partial + PARTIALS);
+  grid = 0;
+  if (a.rows > 0)
+    if (int rc = launch_out<OUT_STATS>(a, res_of(n), &grid, stream)) return rc;
+  a.rows_p = rows_p;
+  const int res = res_of(n);
+  const void* s = res == RES_NONE ? n.x : n.residual_out;
+  const int64_t s_stride = res == RES_NONE ? n.x_stride : static_cast<int64_t>(n.heads) * n.K;
+  const int ctas = rows_p < 1 ? 1 : rows_p < 8 * sm_count() ? rows_p : 8 * sm_count();
+  return res == RES_F32
+             ? launch_ex(norm_encode_kernel<true>, dim3(ctas), dim3(256), 0, 1, true, stream, a, s, s_stride, grid, s_t)
+             : launch_ex(norm_encode_kernel<false>, dim3(ctas), dim3(256), 0, 1, true, stream, a, s, s_stride, grid, s_t);
+}
+
+}  // namespace nvfp4

@@ -94,6 +94,28 @@ NVFP4_DEV uint2 e2m1x16(const float (&v)[16], float den) {
   return e2m1x16_r(v, den, rh, rl);
 }
 
+// Half a block: the eight codes of fl(x / den), by the brackets as above.
+NVFP4_DEV uint32_t e2m1x8(const float (&v)[8], float den) {
+  float rh, rl;
+  recip_brackets(den, rh, rl);
+  if (rh != 0.f) {
+    const uint64_t RH = f32_pair(rh, rh), RL = f32_pair(rl, rl);
+    uint64_t ph[4], pl[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t xv = f32_pair(v[2 * e], v[2 * e + 1]);
+      ph[e] = mul_f32x2(xv, RH);
+      pl[e] = mul_f32x2(xv, RL);
+    }
+    const uint32_t h = e2m1x8_of_pairs(ph[0], ph[1], ph[2], ph[3]), l = e2m1x8_of_pairs(pl[0], pl[1], pl[2], pl[3]);
+    if (h == l) return h;
+  }
+  float q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(v[j], den);
+  return f32x8_to_e2m1x8(q);
+}
+
 // E4M3 code of fl(ab / d) (ab >= 0): RN(ab rdl) <= fl(ab / d) <= RN(ab rdh)
 // for brackets rdl < 1 / d < rdh (recip_brackets), and the E4M3 rounding is
 // monotone, so equal codes of the two products are the code of the quotient;
