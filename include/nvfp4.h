@@ -486,7 +486,8 @@ int nvfp4_kv_compact(nvfp4_kv_cache_t cache, int32_t* table, int64_t table_strid
  *   K         a multiple of 8 (NVFP4 output: of 16), at most 32768
  *   tokens * heads <= 2^30; eps >= 0, finite.
  * All base pointers 16-byte aligned. Sums of squares are fp32: rows whose mean
- * square lies above 2^127 / K give zeros. A NaN in a row makes the row NaN. */
+ * square lies above 2^127 / K give zeros. A NaN in a row makes the row NaN (NVFP4
+ * has none: the codes of such a row mean nothing). */
 typedef struct nvfp4_norm {
   const void* x;
   const void* weight;
@@ -524,6 +525,65 @@ int nvfp4_rms_norm_e4m3(nvfp4_norm_t in, uint8_t* codes, float* scales, nvfp4_st
  *      bytes, 16-byte aligned (COMPUTE only; may be NULL for GIVEN); scratch. */
 int nvfp4_rms_norm_quantize(nvfp4_norm_t in, uint8_t* codes, uint8_t* scales, float* s_t, int s_t_mode,
                             int scale_layout, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* ---- the next token ------------------------------------------------------------- */
+
+/* How a row's token is drawn. Each setting is an array of one entry for each row
+ * (nvfp4_verify_sample: for each sequence), or, where the pointer is NULL, one
+ * value for all. Values on the device are not checked; out of range they mean
+ * what is said here.
+ *   temperature  T > 0; anything else (0, negative, NaN): the first token of the
+ *                order below, with probability 1
+ *   top_k        1 .. vocab - 1; anything else: off
+ *   top_p        [0, 1); 1 and more, NaN: off; below 0: as 0
+ *   min_p        (0, 1]; 0 and less, NaN: off; above 1: as 1 */
+typedef struct nvfp4_sampling {
+  const float* temperature;   /* device */
+  const int32_t* top_k;       /* device */
+  const float* top_p;         /* device */
+  const float* min_p;         /* device */
+  float temperature_all;
+  int32_t top_k_all;
+  float top_p_all;
+  float min_p_all;
+} nvfp4_sampling_t;
+
+/* Draw a token from each row of logits. A row's tokens are ordered by falling
+ * logit, equal logits by index; tokens of -inf or NaN are not there. With
+ *   w_j = exp((l_j - l_max) / T)       (tokens of +inf: 1, beside them 0)
+ * the first top_k tokens are kept; of these the shortest first part whose mass
+ * is at least top_p times theirs (one token at least); of these the tokens with
+ * w_j >= min_p. The token drawn is the first of the order whose cumulated mass
+ * exceeds u times the mass of what is kept, u = uniform[row]:
+ *   out_ids[row]   = its index (-1 if the row has no token)
+ *   out_probs[row] = w / (mass kept)   (0 if the row has none; NULL: not wanted)
+ * Weights are held to 2^-35 of themselves (none below 2^-46) and added exactly:
+ * the token is that of the formulas in real numbers unless u or top_p lies
+ * within about 2^-35 of a border between two tokens. The same inputs give the
+ * same tokens.
+ *   logits   device, bf16 or fp32 (dtype), row r at r * stride elements,
+ *            aligned to its type; any vocab of 1 .. 524288 (stride >= vocab)
+ *   uniform  device fp32 [rows], in [0, 1); below 0 and NaN as 0, 1 and more:
+ *            the last token kept
+ *   rows     <= 2^20 */
+int nvfp4_sample(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, nvfp4_sampling_t settings,
+                 const float* uniform, int32_t* out_ids, float* out_probs, nvfp4_stream_t stream);
+
+/* Speculative verification by sampling: nvfp4_sample of every position, and the
+ * number of drafts that stand. Logits row b * (n_draft + 1) + i is sequence b
+ * at position i (as in nvfp4_verify_accept); a sequence's settings serve all its
+ * rows. For drafts that were proposed with certainty (the argmax of a draft
+ * head) this is rejection sampling: a draft stands with the probability that
+ * the settings give it, and the token drawn where the first falls is distributed
+ * as the rest. The step emits out_tokens[b][0 .. n_accepted[b]].
+ *   uniform     device fp32 [batch * (n_draft + 1)]
+ *   draft_ids   device int32 [batch][n_draft] (may be NULL for n_draft = 0)
+ *   out_tokens  device int32 [batch][n_draft + 1]
+ *   out_probs   device fp32 like out_tokens, or NULL
+ *   n_accepted  device int32 [batch]: leading drafts equal to out_tokens */
+int nvfp4_verify_sample(const void* logits, int dtype, int64_t batch, int n_draft, int64_t vocab, int64_t stride,
+                        nvfp4_sampling_t settings, const float* uniform, const int32_t* draft_ids, int32_t* out_tokens,
+                        float* out_probs, int32_t* n_accepted, nvfp4_stream_t stream);
 
 /* ---- helpers --------------------------------------------------------------- */
 

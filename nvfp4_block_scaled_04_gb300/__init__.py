@@ -33,6 +33,7 @@ EXPORTS = [
     "nvfp4_gemm_w4a16_silu_mul", "nvfp4_gemm_w4a4_quant", "nvfp4_grouped_gemm_w4a4",
     "nvfp4_kv_append", "nvfp4_paged_attention", "nvfp4_kv_reserve", "nvfp4_kv_fork", "nvfp4_kv_release",
     "nvfp4_kv_compact", "nvfp4_rms_norm", "nvfp4_rms_norm_e4m3", "nvfp4_rms_norm_quantize",
+    "nvfp4_sample", "nvfp4_verify_sample",
 ]
 _NON_INT = ("nvfp4_scales_bytes", "nvfp4_workspace_size", "nvfp4_status_string")
 
@@ -64,6 +65,13 @@ class CNorm(ctypes.Structure):
                 ("residual_out", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("x_stride", ctypes.c_int64),
                 ("heads", ctypes.c_int32), ("K", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class CSampling(ctypes.Structure):
+    """Mirror of nvfp4_sampling_t."""
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("temperature_all", ctypes.c_float), ("top_k_all", ctypes.c_int32),
+                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
 
 
 _lib = None
@@ -100,6 +108,8 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_rms_norm.argtypes = [CNorm, vp, i64, vp]
         L.nvfp4_rms_norm_e4m3.argtypes = [CNorm, vp, vp, vp]
         L.nvfp4_rms_norm_quantize.argtypes = [CNorm, vp, vp, vp, i32, i32, vp, sz, vp]
+        L.nvfp4_sample.argtypes = [vp, i32, i64, i64, i64, CSampling, vp, vp, vp, vp]
+        L.nvfp4_verify_sample.argtypes = [vp, i32, i64, i32, i64, i64, CSampling, vp, vp, vp, vp, vp, vp]
         L.nvfp4_scales_bytes.argtypes = [i64, i64, i32]
         L.nvfp4_scales_bytes.restype = sz
         L.nvfp4_workspace_size.argtypes = [i32, i64, i64, i64, i64, i64]
@@ -684,6 +694,68 @@ def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None, eps: 
         scales = scales[: rows * (K // 16)].view(rows, K // 16)
     q = QTensor(codes, scales, st, rows, K, 1, scale_layout)
     return q if s is None else (q, s)
+
+
+_LOGITS = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+_SETTINGS = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32), ("min_p", torch.float32))
+
+
+def _sampling(logits, uniform, settings, n):
+    """(the logits' type, their stride, the settings of n rows or sequences)"""
+    dtype = _LOGITS.get(logits.dtype)
+    if dtype is None or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: bf16 or fp32 [rows][vocab], rows contiguous, are needed")
+    rows, vocab = logits.shape
+    _beside(logits, uniform)
+    if uniform.dtype != torch.float32 or uniform.numel() != rows or not uniform.is_contiguous():
+        raise ValueError("uniform: a contiguous fp32 number for each row of the logits is needed")
+    ptrs, values = [None] * 4, [1.0, 0, 1.0, 0.0]
+    for i, (v, (name, kind)) in enumerate(zip(settings, _SETTINGS)):
+        if isinstance(v, torch.Tensor):
+            if v.dtype != kind or v.dim() != 1 or v.shape[0] != n or not v.is_contiguous():
+                raise ValueError(f"{name}: a number, or a contiguous {kind} tensor of {n}, is needed")
+            _beside(v)
+            ptrs[i] = v.data_ptr()
+        else:
+            values[i] = v
+    return dtype, logits.stride(0) if rows > 1 else vocab, CSampling(*ptrs, *values)
+
+
+def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """Draw a token from each row of logits (bf16 or fp32 [rows][vocab]) with the random numbers uniform (fp32 [rows],
+    in [0, 1)): (ids int32 [rows], their probabilities fp32 [rows]). Tokens are ordered by falling logit, equal ones by
+    index; the first top_k are kept (0: all), of these the shortest first part with top_p of their mass, of these the
+    tokens of at least min_p times the first one's probability. temperature 0: the largest logit. Each setting is a
+    number or a tensor with one for each row. A row of -inf and NaN gives -1."""
+    rows = logits.shape[0]
+    dtype, stride, c = _sampling(logits, uniform, (temperature, top_k, top_p, min_p), rows)
+    ids = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    probs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _check(lib().nvfp4_sample(logits.data_ptr(), dtype, rows, logits.shape[1], stride, c, uniform.data_ptr(),
+                              ids.data_ptr(), probs.data_ptr(), _stream()), "nvfp4_sample")
+    return ids, probs
+
+
+def verify_sample(logits: torch.Tensor, uniform: torch.Tensor, draft_ids: torch.Tensor, temperature=1.0, top_k=0,
+                  top_p=1.0, min_p=0.0):
+    """Speculative verify by sampling: logits [batch * (n_draft + 1)][vocab] (row b * (n_draft + 1) + i is sequence b at
+    position i), draft_ids int32 [batch][n_draft] -> (tokens int32 [batch][n_draft + 1], accepted drafts int32 [batch],
+    the tokens' probabilities fp32 like tokens). Settings are numbers or tensors with one for each sequence."""
+    if draft_ids.dim() != 2 or draft_ids.dtype != torch.int32:
+        raise ValueError("draft_ids: int32 [batch][n_draft] is needed")
+    batch, n_draft = draft_ids.shape
+    if logits.shape[0] != batch * (n_draft + 1):
+        raise ValueError("verify_sample: logits need batch * (n_draft + 1) rows")
+    dtype, stride, c = _sampling(logits, uniform, (temperature, top_k, top_p, min_p), batch)
+    draft_ids = draft_ids.contiguous()
+    _beside(logits, draft_ids)
+    tokens = torch.empty(batch, n_draft + 1, dtype=torch.int32, device=logits.device)
+    probs = torch.empty(batch, n_draft + 1, dtype=torch.float32, device=logits.device)
+    n_acc = torch.empty(batch, dtype=torch.int32, device=logits.device)
+    _check(lib().nvfp4_verify_sample(logits.data_ptr(), dtype, batch, n_draft, logits.shape[1], stride, c,
+                                     uniform.data_ptr(), draft_ids.data_ptr(), tokens.data_ptr(), probs.data_ptr(),
+                                     n_acc.data_ptr(), _stream()), "nvfp4_verify_sample")
+    return tokens, n_acc, probs
 
 
 def read_device_status() -> int:

@@ -18,7 +18,8 @@ CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = PKG / "libnvfp4.so"
 SOURCES = ["api.cu", "quantize.cu", "gemv.cu", "moe.cu", "gemm_w4a4.cu", "noalloc.cu", "tma_host.cu",
-           "kv_cache.cu", "attention.cu", "norm.cu"]
+           "kv_cache.cu", "attention.cu", "norm.cu",
+           "sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-Xptxas", "-warn-spills", f"-I{ROOT / 'include'}"]

@@ -109,6 +109,16 @@ int norm_check(const nvfp4_norm_t& n, int granule) {
   return NVFP4_OK;
 }
 
+int logits_check(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const float* uniform) {
+  if (dtype != NVFP4_DTYPE_F32 && dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_INVALID_ARG;
+  if (rows < 0 || vocab < 1 || stride < vocab) return NVFP4_ERR_INVALID_ARG;
+  if (vocab > 524288 || rows > (1 << 20)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return NVFP4_OK;
+  if (!logits || !uniform) return NVFP4_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) % (dtype == NVFP4_DTYPE_F32 ? 4 : 2) != 0) return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
 }  // namespace
 }  // namespace nvfp4
 
@@ -437,6 +447,29 @@ int nvfp4_rms_norm_quantize(nvfp4_norm_t in, uint8_t* codes, uint8_t* scales, fl
   }
   return launch_rms_norm_quantize(in, codes, scales, s_t, s_t_mode, scale_layout, workspace,
                                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_sample(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, nvfp4_sampling_t settings,
+                 const float* uniform, int32_t* out_ids, float* out_probs, nvfp4_stream_t stream) {
+  if (int rc = logits_check(logits, dtype, rows, vocab, stride, uniform)) return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (!out_ids) return NVFP4_ERR_INVALID_ARG;
+  return launch_sample(logits, dtype, rows, vocab, stride, settings, 1, uniform, out_ids, out_probs,
+                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_verify_sample(const void* logits, int dtype, int64_t batch, int n_draft, int64_t vocab, int64_t stride,
+                        nvfp4_sampling_t settings, const float* uniform, const int32_t* draft_ids, int32_t* out_tokens,
+                        float* out_probs, int32_t* n_accepted, nvfp4_stream_t stream) {
+  if (batch < 0 || n_draft < 0 || n_draft >= (1 << 20) || batch > (1 << 20)) return NVFP4_ERR_INVALID_ARG;
+  const int64_t rows = batch * (n_draft + 1);
+  if (int rc = logits_check(logits, dtype, rows, vocab, stride, uniform)) return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (!out_tokens || !n_accepted || (n_draft > 0 && !draft_ids)) return NVFP4_ERR_INVALID_ARG;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (int rc = launch_sample(logits, dtype, rows, vocab, stride, settings, n_draft + 1, uniform, out_tokens, out_probs, s))
+    return rc;
+  return launch_accept(out_tokens, draft_ids, batch, n_draft, n_accepted, s);
 }
 
 int nvfp4_read_device_status(int* out, nvfp4_stream_t stream) {

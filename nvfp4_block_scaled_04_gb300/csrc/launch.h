@@ -146,6 +146,12 @@ int launch_rms_norm_e4m3(const nvfp4_norm_t& n, uint8_t* codes, float* scales, c
 int launch_rms_norm_quantize(const nvfp4_norm_t& n, uint8_t* codes, uint8_t* scales, float* s_t, int s_t_mode,
                              int scale_layout, void* workspace, cudaStream_t stream);
 
+// ---- sample.cu: rows_each rows share one entry of the settings
+int launch_sample(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const nvfp4_sampling_t& set,
+                  int rows_each, const float* uniform, int32_t* ids, float* probs, cudaStream_t stream);
+int launch_accept(const int32_t* tokens, const int32_t* drafts, int64_t batch, int n_draft, int32_t* accepted,
+                  cudaStream_t stream);
+
 // ---- paged key-value cache (kv_cache.cu, attention.cu)
 // The sequences of a call (nvfp4_kv_seqs_t) and the number of rows that the
 // caller's arrays of new tokens hold. Lengths, page ids and offsets come from
