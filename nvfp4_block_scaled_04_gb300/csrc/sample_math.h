@@ -61,7 +61,6 @@ struct Key {
   static constexpr uint32_t PINF = F32 ? 0xFF800000u : 0xFF80u;  // key of +inf
   static constexpr uint32_t LOWEST = F32 ? 0x00800000u : 0x80u;  // key of the lowest finite value
   static constexpr int LOW = F32 ? 16 : 0;                       // bits of a key below the bins'
-  static constexpr int NB2 = F32 ? 2048 : 1024;                  // bins of a finer count
 };
 
 // 0 for what is never drawn (-inf, NaN); -0 is 0.
@@ -87,25 +86,34 @@ constexpr uint32_t POS_TOP = 0x8000u + (E_HI << 7);        // from here up: bin 
 constexpr uint32_t POS_LOW = 0x8000u + (E_LO << 7);        // the lowest positive h with a bin of its own
 constexpr uint32_t NEG_TOP = 0x7FFFu - (E_LO << 7);        // the highest negative one
 constexpr uint32_t NEG_LOW = 0x7FFFu - (E_HI << 7) + 1;    // the lowest
-constexpr int B_MID = OUTER + 1, B_LAST = 2 * OUTER + 2, NB = 2 * OUTER + 3;
+constexpr int B_MID = OUTER + 1, B_LAST = 2 * OUTER + 3, NB = 2 * OUTER + 4;   // B_MID: 0 and up, B_MID + 1: below 0
 
 NVFP4_HD int bin_of(uint32_t h) {
   if (h & 0x8000u) {
     const int b = static_cast<int>(POS_TOP) - static_cast<int>(h);
     return b < 0 ? 0 : b > B_MID ? B_MID : b;
   }
-  const int b = B_MID + 1 + static_cast<int>(NEG_TOP) - static_cast<int>(h);
-  return b < B_MID ? B_MID : b > B_LAST ? B_LAST : b;
+  const int b = B_MID + 2 + static_cast<int>(NEG_TOP) - static_cast<int>(h);
+  return b < B_MID + 1 ? B_MID + 1 : b > B_LAST ? B_LAST : b;
 }
 
-NVFP4_HD bool wide_bin(int b) { return b == 0 || b == B_MID || b == B_LAST; }
+// The four bins of many values, by number, and -1 for the others.
+NVFP4_HD int wide_bin(int b) { return b == 0 ? 0 : b == B_MID ? 1 : b == B_MID + 1 ? 2 : b == B_LAST ? 3 : -1; }
 
 // The upper halves of the keys of a bin.
 NVFP4_HD void bin_range(int b, uint32_t& lo, uint32_t& hi) {
   if (b == 0) lo = POS_TOP, hi = 0xFF80u;
-  else if (b == B_MID) lo = NEG_TOP + 1, hi = POS_LOW - 1;
+  else if (b == B_MID) lo = 0x8000u, hi = POS_LOW - 1;
+  else if (b == B_MID + 1) lo = NEG_TOP + 1, hi = 0x7FFFu;
   else if (b == B_LAST) lo = 0x80u, hi = NEG_LOW - 1;
-  else lo = hi = b < B_MID ? POS_TOP - b : NEG_TOP + B_MID + 1 - b;
+  else lo = hi = b < B_MID ? POS_TOP - b : NEG_TOP + B_MID + 2 - b;
+}
+
+// Two bf16 logits of one word: (bin of each) = B_MID - (its signed half of what is returned), for magnitudes of
+// 2^-10 and more (infinities and NaN fall into the first and the last bin). sign: 0xFFFF where negative.
+constexpr uint32_t MAG_LOW = E_LO << 7, MAG_TOP = E_HI << 7;
+NVFP4_HD uint32_t bin_steps(uint32_t clamped_magnitudes, uint32_t sign) {
+  return (clamped_magnitudes - (MAG_LOW - 1) * 0x10001u) ^ sign;
 }
 
 // ---- weights
@@ -177,6 +185,15 @@ NVFP4_HD unsigned long long weight(float ref, float x, const Slope& c, const uns
   int n;
   const unsigned long long w = weight_and_scale(ref, x, c, table, n);
   return (w + ((1ull << n) >> 1)) >> n;
+}
+
+// ceil(x / w) where that is below 2^21 (w = 0: 0).
+NVFP4_HD uint32_t few_times(unsigned long long x, unsigned long long w) {
+  if (w == 0) return 0;
+  uint32_t n = static_cast<uint32_t>(f32_div(static_cast<float>(x), static_cast<float>(w)));   // off by one at most
+  if (n > 0 && (n - 1) * w >= x) --n;
+  while (n * w < x) ++n;
+  return n;
 }
 
 // floor(v * x) for 0 <= v < 1, and whether something was cut off.

@@ -25,6 +25,9 @@ float value32(unsigned k) { return value_of<true>(k); }
 int bin(unsigned h) { return bin_of(h); }
 void range(int b, unsigned* r) { uint32_t lo, hi; bin_range(b, lo, hi); r[0] = lo; r[1] = hi; }
 int sizes(int i) { return i == 0 ? NB : i == 1 ? B_MID : B_LAST; }
+int wide(int b) { return wide_bin(b); }
+unsigned steps(unsigned m, unsigned sign) { return bin_steps(m, sign); }
+unsigned few(unsigned long long x, unsigned long long w) { return few_times(x, w); }
 unsigned long long weigh(float ref, float x, float t) { return weight(ref, x, slope_of(t), EXP2_TABLE); }
 unsigned long long part(unsigned long long x, float v, int* cut) { bool c = false; const unsigned long long r = times(x, v, c); *cut = c; return r; }
 }
@@ -41,6 +44,8 @@ def lib(tmp_path_factory):
     L.key16.restype = L.key32.restype = ctypes.c_uint
     L.weigh.restype = L.part.restype = ctypes.c_ulonglong
     L.weigh.argtypes = [ctypes.c_float] * 3
+    L.few.argtypes = [ctypes.c_ulonglong] * 2
+    L.few.restype = L.steps.restype = ctypes.c_uint
     L.part.argtypes = [ctypes.c_ulonglong, ctypes.c_float, ctypes.POINTER(ctypes.c_int)]
     return L
 
@@ -75,11 +80,40 @@ def test_bins_cover_the_keys_in_falling_order(lib):
         lib.range(b, r)
         mine = h[bins == b]
         assert (r[0], r[1]) == (mine.min(), mine.max())
-        assert b in (0, mid, last) or r[0] == r[1]
+        assert lib.wide(b) == {0: 0, mid: 1, mid + 1: 2, last: 3}.get(b, -1)
+        assert lib.wide(b) >= 0 or r[0] == r[1]
     # a bin of its own for every value of magnitude 2^-10 .. 2^7
     v = np.array([lib.value16(int(i)) for i in h])
-    wide = np.isin(bins, (0, mid, last))
+    wide = np.isin(bins, (0, mid, mid + 1, last))
     assert np.array_equal(wide, ~((np.abs(v) >= 2.0 ** -10) & (np.abs(v) < 128)))
+
+
+def test_bins_of_packed_words(lib):
+    """Every bf16 of magnitude 2^-10 and more, infinities and NaN among them, in each half of a word."""
+    nb, mid, last = (lib.sizes(i) for i in range(3))
+    low, top = 117 << 7, 134 << 7
+    for b in range(0, 1 << 16, 3):
+        m, other = b & 0x7FFF, 0x4123
+        if m < low:
+            continue
+        clamp = min(max(m, low - 1), top)
+        sign = 0xFFFF if b & 0x8000 else 0
+        k = lib.key16(b)
+        want = lib.bin(k) if k else last if sign else 0
+        for at in (0, 16):
+            s = lib.steps((clamp << at) | (other << (16 - at)), sign << at)
+            half = (s >> at) & 0xFFFF
+            assert mid - (half - 0x10000 if half & 0x8000 else half) == want, hex(b)
+
+
+def test_quotients(lib):
+    rng = random.Random(5)
+    for _ in range(20000):
+        w = rng.randrange(1, 1 << rng.randrange(1, 45))
+        n = rng.randrange(0, 1 << rng.randrange(1, 20))
+        for x in (n * w, n * w + 1, max(0, n * w - 1), n * w + rng.randrange(0, w)):
+            assert lib.few(x, w) == -(-x // w), (x, w)
+    assert lib.few(5, 0) == 0
 
 
 def f32(x):
