@@ -593,48 +593,64 @@ def kv_compact(cache: KVCache, table: torch.Tensor, refs: torch.Tensor,
     return live
 
 
-def _beside(x, *ts):
-    """x on the current device, and every tensor of ts beside it."""
-    d = x.device
-    if d.type != "cuda":
+# (a private name of torch's; the public call looks whether CUDA is up, too)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _where(x) -> int:
+    """The device of x: the current one."""
+    d = x.get_device()
+    if d < 0:
         _require_cuda(x)
-    if d.index != torch.cuda.current_device():
+    if d != _device():
         raise RuntimeError("nvfp4: tensors must live on the current device")
+    return d
+
+
+def _beside(d, *ts):
     for t in ts:
-        if t is not None and t.device != d:
+        if t.get_device() != d:
             raise RuntimeError("nvfp4: tensors must live on one CUDA device (no CPU path exists)")
 
 
 def _norm(x, weight, eps, residual, residual_out, weight_offset):
-    """(x as the kernels take it, its CNorm, the stream that goes on or None)"""
+    """(x as the kernels take it, its CNorm, the stream that goes on or None, its device)"""
     shape = x.shape
-    if x.dtype != torch.bfloat16 or len(shape) not in (2, 3):
+    n = len(shape)
+    if x.dtype != torch.bfloat16 or (n != 2 and n != 3):
         raise ValueError("rms_norm: x is bf16 [rows][K] or [tokens][heads][K]")
-    _beside(x, weight, residual, residual_out)
-    K, heads = shape[-1], shape[1] if len(shape) == 3 else 1
-    row = heads * K
-    st = x.stride()
-    stride = st[0] if shape[0] > 1 else row
-    if (st[-1] != 1 and K > 1) or (heads > 1 and st[1] != K) or stride % 8 or stride < row or x.data_ptr() % 16:
-        x, stride = x.clone(memory_format=torch.contiguous_format), row
+    d = _where(x)
+    K, heads = shape[-1], shape[1] if n == 3 else 1
+    stride = row = heads * K
+    ptr = x.data_ptr()
+    if not x.is_contiguous() or ptr % 16 or K % 8:
+        st = x.stride()
+        stride = st[0] if shape[0] > 1 else row
+        if (st[-1] != 1 and K > 1) or (heads > 1 and st[1] != K) or stride % 8 or stride < row or ptr % 16:
+            x, stride = x.clone(memory_format=torch.contiguous_format), row
+            ptr = x.data_ptr()
     w = None
     if weight is not None:
-        if weight.dtype != torch.bfloat16 or weight.shape != shape[-1:] or not weight.is_contiguous():
+        if weight.dtype != torch.bfloat16 or weight.numel() != K or not weight.is_contiguous():
             raise ValueError("rms_norm: weight is contiguous bf16 [K]")
+        _beside(d, weight)
         w = weight.data_ptr()
     if residual is None:
         if residual_out is not None:
             raise ValueError("rms_norm: residual_out needs a residual")
-        return x, CNorm(x.data_ptr(), w, None, None, shape[0], stride, heads, K, DTYPE_BF16, eps, weight_offset, 0), None
+        return x, CNorm(ptr, w, None, None, shape[0], stride, heads, K, DTYPE_BF16, eps, weight_offset, 0), None, d
+    kind = residual.dtype
+    if kind != torch.bfloat16 and kind != torch.float32:
+        raise ValueError("rms_norm: a residual is bf16 or fp32")
     if residual_out is None:
         residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
-    for t in (residual, residual_out):
-        if t.shape != shape or t.dtype != residual.dtype or not t.is_contiguous():
-            raise ValueError("rms_norm: residual and residual_out are contiguous, of x's shape and of one type")
-    if residual.dtype != torch.bfloat16 and residual.dtype != torch.float32:
-        raise ValueError("rms_norm: a residual is bf16 or fp32")
-    return x, CNorm(x.data_ptr(), w, residual.data_ptr(), residual_out.data_ptr(), shape[0], stride, heads, K,
-                    DTYPE_BF16 if residual.dtype == torch.bfloat16 else DTYPE_F32, eps, weight_offset, 0), residual_out
+    elif residual_out.dtype != kind or residual_out.shape != shape or not residual_out.is_contiguous():
+        raise ValueError("rms_norm: residual_out is contiguous, of x's shape and the residual's type")
+    if residual.shape != shape or not residual.is_contiguous():
+        raise ValueError("rms_norm: residual is contiguous, of x's shape")
+    _beside(d, residual, residual_out)
+    return x, CNorm(ptr, w, residual.data_ptr(), residual_out.data_ptr(), shape[0], stride, heads, K,
+                    DTYPE_BF16 if kind == torch.bfloat16 else DTYPE_F32, eps, weight_offset, 0), residual_out, d
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
@@ -644,18 +660,17 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1
     x [rows][K], or [tokens][heads][K] (each head by itself; slices of a fused
     projection are read in place). With a residual (bf16 or fp32): (y, s), s in
     residual_out (a new tensor if None; may be residual). out may be x."""
-    x0 = x
-    x, c, s = _norm(x, weight, eps, residual, residual_out, weight_offset)
-    row = c.heads * c.K
+    x, c, s, d = _norm(x, weight, eps, residual, residual_out, weight_offset)
+    stride = c.heads * c.K
     if out is None:
-        out = torch.empty(x0.shape, dtype=x0.dtype, device=x0.device)
-        stride = row
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         st = out.stride()
-        stride = st[0] if x0.shape[0] > 1 else row
-        if out.shape != x0.shape or out.dtype != torch.bfloat16 or st[-1] != 1 or (c.heads > 1 and st[1] != c.K):
+        if out.shape != x.shape or out.dtype != torch.bfloat16 or st[-1] != 1 or (c.heads > 1 and st[1] != c.K):
             raise ValueError("out: bf16 of x's shape, rows contiguous, is needed")
-        _beside(x, out)
+        _beside(d, out)
+        if x.shape[0] > 1:
+            stride = st[0]
     _check(lib().nvfp4_rms_norm(c, out.data_ptr(), stride, _stream()), "nvfp4_rms_norm")
     return out if s is None else (out, s)
 
@@ -665,8 +680,8 @@ def rms_norm_e4m3(x: torch.Tensor, weight: torch.Tensor | None = None, eps: floa
                   weight_offset: float = 0.0):
     """rms_norm's y as float8_e4m3fn codes of x's shape and fp32 scales [rows] (y = code * scale of its row):
     (codes, scales), with a residual (codes, scales, s)."""
-    x, c, s = _norm(x, weight, eps, residual, residual_out, weight_offset)
-    codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    x, c, s, _ = _norm(x, weight, eps, residual, residual_out, weight_offset)
+    codes = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
     scales = torch.empty(c.tokens * c.heads, dtype=torch.float32, device=x.device)
     _check(lib().nvfp4_rms_norm_e4m3(c, codes.data_ptr(), scales.data_ptr(), _stream()), "nvfp4_rms_norm_e4m3")
     return (codes, scales) if s is None else (codes, scales, s)
@@ -678,7 +693,7 @@ def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None, eps: 
                       workspace: torch.Tensor | None = None):
     """rms_norm's y as NVFP4 (a QTensor of tokens * heads rows), the input of a W4A4 linear; with a residual
     (QTensor, s). s_t None -> computed from y (amax / 2688); else a 1-element fp32 tensor to use."""
-    x, c, s = _norm(x, weight, eps, residual, residual_out, weight_offset)
+    x, c, s, _ = _norm(x, weight, eps, residual, residual_out, weight_offset)
     rows, K, dev = c.tokens * c.heads, c.K, x.device
     codes = torch.empty(rows, K // 2, dtype=torch.uint8, device=dev)
     scales = torch.empty(max(scales_bytes(rows, K, scale_layout), 1), dtype=torch.uint8, device=dev)
@@ -701,24 +716,29 @@ _SETTINGS = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", t
 
 
 def _sampling(logits, uniform, settings, n):
-    """(the logits' type, their stride, the settings of n rows or sequences)"""
+    """(the logits' type, rows, vocabulary and stride, the settings of n rows or sequences, the device)"""
     dtype = _LOGITS.get(logits.dtype)
-    if dtype is None or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    if dtype is None or logits.dim() != 2:
         raise ValueError("logits: bf16 or fp32 [rows][vocab], rows contiguous, are needed")
     rows, vocab = logits.shape
-    _beside(logits, uniform)
+    stride, one = logits.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError("logits: bf16 or fp32 [rows][vocab], rows contiguous, are needed")
+    d = _where(logits)
     if uniform.dtype != torch.float32 or uniform.numel() != rows or not uniform.is_contiguous():
         raise ValueError("uniform: a contiguous fp32 number for each row of the logits is needed")
-    ptrs, values = [None] * 4, [1.0, 0, 1.0, 0.0]
-    for i, (v, (name, kind)) in enumerate(zip(settings, _SETTINGS)):
+    _beside(d, uniform)
+    args = [None, None, None, None, 1.0, 0, 1.0, 0.0]
+    for i, v in enumerate(settings):
         if isinstance(v, torch.Tensor):
-            if v.dtype != kind or v.dim() != 1 or v.shape[0] != n or not v.is_contiguous():
+            name, kind = _SETTINGS[i]
+            if v.dtype != kind or v.shape != (n,) or not v.is_contiguous():
                 raise ValueError(f"{name}: a number, or a contiguous {kind} tensor of {n}, is needed")
-            _beside(v)
-            ptrs[i] = v.data_ptr()
+            _beside(d, v)
+            args[i] = v.data_ptr()
         else:
-            values[i] = v
-    return dtype, logits.stride(0) if rows > 1 else vocab, CSampling(*ptrs, *values)
+            args[4 + i] = v
+    return dtype, rows, vocab, stride if rows > 1 else vocab, CSampling(*args), d
 
 
 def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
@@ -727,12 +747,11 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
     index; the first top_k are kept (0: all), of these the shortest first part with top_p of their mass, of these the
     tokens of at least min_p times the first one's probability. temperature 0: the largest logit. Each setting is a
     number or a tensor with one for each row. A row of -inf and NaN gives -1."""
-    rows = logits.shape[0]
-    dtype, stride, c = _sampling(logits, uniform, (temperature, top_k, top_p, min_p), rows)
+    dtype, rows, vocab, stride, c, _ = _sampling(logits, uniform, (temperature, top_k, top_p, min_p), logits.shape[0])
     ids = torch.empty(rows, dtype=torch.int32, device=logits.device)
     probs = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    _check(lib().nvfp4_sample(logits.data_ptr(), dtype, rows, logits.shape[1], stride, c, uniform.data_ptr(),
-                              ids.data_ptr(), probs.data_ptr(), _stream()), "nvfp4_sample")
+    _check(lib().nvfp4_sample(logits.data_ptr(), dtype, rows, vocab, stride, c, uniform.data_ptr(), ids.data_ptr(),
+                              probs.data_ptr(), _stream()), "nvfp4_sample")
     return ids, probs
 
 
@@ -746,13 +765,13 @@ def verify_sample(logits: torch.Tensor, uniform: torch.Tensor, draft_ids: torch.
     batch, n_draft = draft_ids.shape
     if logits.shape[0] != batch * (n_draft + 1):
         raise ValueError("verify_sample: logits need batch * (n_draft + 1) rows")
-    dtype, stride, c = _sampling(logits, uniform, (temperature, top_k, top_p, min_p), batch)
+    dtype, _, vocab, stride, c, d = _sampling(logits, uniform, (temperature, top_k, top_p, min_p), batch)
+    _beside(d, draft_ids)
     draft_ids = draft_ids.contiguous()
-    _beside(logits, draft_ids)
     tokens = torch.empty(batch, n_draft + 1, dtype=torch.int32, device=logits.device)
-    probs = torch.empty(batch, n_draft + 1, dtype=torch.float32, device=logits.device)
+    probs = torch.empty_like(tokens, dtype=torch.float32)
     n_acc = torch.empty(batch, dtype=torch.int32, device=logits.device)
-    _check(lib().nvfp4_verify_sample(logits.data_ptr(), dtype, batch, n_draft, logits.shape[1], stride, c,
+    _check(lib().nvfp4_verify_sample(logits.data_ptr(), dtype, batch, n_draft, vocab, stride, c,
                                      uniform.data_ptr(), draft_ids.data_ptr(), tokens.data_ptr(), probs.data_ptr(),
                                      n_acc.data_ptr(), _stream()), "nvfp4_verify_sample")
     return tokens, n_acc, probs

@@ -149,42 +149,73 @@ NVFP4_HD Slope slope_of(float t) {
   return s;
 }
 
-// exp((x - ref) / T) for x <= ref as 2^(-44 - n) times what is returned, to 2^-35 of itself: 2^-y by a table of 64 steps and a short series
-// (Tang, 1989), with y = (ref - x) log2(e) / T carried in two floats. Equal values weigh one, also
-// infinite ones; 0 below 2^-46. (The series' second term is rounded four times at 2^-14 and 2^-25, q twice by 2^-38, the table's
-// factor by 2^-32 of l, the term left out is 2^-39: 2^-36 together.)
-NVFP4_HD unsigned long long weight_and_scale(float ref, float x, const Slope& c, const unsigned long long* table, int& n) {
-  n = 0;
-  if (x == ref) return ONE;
-  if (c.hi == 0.f) return ref - ref == 0.f ? ONE : 0ull;        // an infinite temperature
-  const float nx = -x;
-  const float d = f32_add(ref, nx);                           // d + dl = ref - x exactly
-  const float b = f32_sub(d, ref);
-  const float dl = f32_add(f32_sub(ref, f32_sub(d, b)), f32_sub(nx, b));
-  const float p = f32_mul(d, c.hi);
-  if (!(p < 46.f)) return 0ull;
-  const float pl = f32_fma(d, c.lo, f32_fma(dl, c.hi, f32_fma(d, c.hi, -p)));
-  const float whole = floorf(p);
-  const float f = f32_sub(p, whole);
-  const int i = static_cast<int>(f * 64.f);
-  const float r0 = f32_fma(static_cast<float>(i), -0.015625f, f);   // exact, below 2^-6
-  const float r = f32_add(r0, pl), rl = f32_sub(pl, f32_sub(r, r0));
-  const float ln2 = 6.93147182e-01f, ln2_lo = -1.90465421e-09f;
-  const float l = f32_mul(r, ln2);
-  const float ll = f32_add(f32_fma(r, ln2, -l), f32_fma(r, ln2_lo, f32_mul(rl, ln2)));
+// exp((x - ref) / T) for x <= ref as 2^(-44 - n) times what is returned, to 2^-35 of itself: 2^-y by a table of 64
+// steps and a short series (Tang, 1989), with y = (ref - x) log2(e) / T carried in two floats. Equal values weigh
+// one, also infinite ones; 0 where y >= 46 and for a NaN. (|l| < 0.0055: the series' second term is rounded three
+// times by 2^-25 of 2^-16, q twice by 2^-38, the table's factor by 2^-31 of l, the term left out is 2^-44: 2^-36
+// together.) Written for one value (F = float, float operations) or a pair (the pair's operations).
+constexpr float W_MAGIC = 12582912.0f;   // 1.5 * 2^23: a sum with it is rounded to a whole number
+
+template <class F>
+struct WeightParts {
+  F y, t, l, tail;   // 2^-y = 2^(-k/64) (1 - l + tail), k in the lower bits of t
+};
+
+template <class F, class S>
+NVFP4_HD WeightParts<F> weight_parts(F ref, F nx, F hi, F lo, S) {
+  const F minus1 = S::all(-1.0f);
+  const F d = S::add(ref, nx);                                   // d + dl = ref - x exactly
+  const F b = S::fma(ref, minus1, d);
+  const F dl = S::add(S::fma(S::fma(b, minus1, d), minus1, ref), S::fma(b, minus1, nx));
+  WeightParts<F> p;
+  p.y = S::mul(d, hi);
+  p.t = S::fma(p.y, S::all(64.0f), S::all(W_MAGIC));
+  const F r0 = S::fma(S::add(p.t, S::all(-W_MAGIC)), S::all(-0.015625f), p.y);   // exact, at most 2^-7
+  const F yl = S::fma(d, lo, S::fma(dl, hi, S::fma(d, hi, S::mul(p.y, minus1))));
+  const F r = S::add(r0, yl), rl = S::fma(S::fma(r0, minus1, r), minus1, yl);
+  const F ln2 = S::all(6.93147182e-01f);
+  p.l = S::mul(r, ln2);
+  const F nl = S::mul(p.l, minus1);
+  const F ll = S::add(S::fma(r, ln2, nl), S::fma(r, S::all(-1.90465421e-09f), S::mul(rl, ln2)));
   // e^-(l + ll) = 1 - l + tail
-  const float tail = f32_sub(f32_mul(f32_mul(l, l), f32_fma(-l, f32_fma(-l, 0.0416666667f, 0.166666667f), 0.5f)), f32_fma(-l, ll, ll));
-  const int q = int_of_f32(-l * 0x1p37f) + int_of_f32(tail * 0x1p37f);   // below 2^31: l < 0.0109
-  const unsigned long long t = table[i];
-  n = static_cast<int>(whole);
-  return t + static_cast<unsigned long long>((static_cast<long long>((t + 2048) >> 12) * q) >> 25);
+  const F h = S::fma(nl, S::fma(nl, S::all(0.0416666667f), S::all(0.166666667f)), S::all(0.5f));
+  p.tail = S::fma(S::mul(p.l, p.l), h, S::mul(S::fma(nl, ll, ll), minus1));
+  return p;
 }
+
+struct OneFloat {
+  static NVFP4_HD float all(float v) { return v; }
+  static NVFP4_HD float add(float a, float b) { return f32_add(a, b); }
+  static NVFP4_HD float mul(float a, float b) { return f32_mul(a, b); }
+  static NVFP4_HD float fma(float a, float b, float c) { return f32_fma(a, b, c); }
+};
+
+NVFP4_HD unsigned long long weight_of_parts(float y, float t, float l, float tail, const unsigned long long* table, int& n) {
+  const int k = static_cast<int>(bits_of_f32(t) - bits_of_f32(W_MAGIC));
+  const int q = int_of_f32(l * -0x1p37f) + int_of_f32(tail * 0x1p37f);   // below 2^30
+  const unsigned long long e = table[k & 63];
+  n = (k >> 6) & 63;
+  const long long add = static_cast<long long>(static_cast<int>((e + 8192) >> 14)) * q;
+  return y < 46.f ? e + static_cast<unsigned long long>(add >> 23) : 0ull;
+}
+
+NVFP4_HD unsigned long long weight_and_scale(float ref, float x, const Slope& c, const unsigned long long* table, int& n) {
+  const WeightParts<float> p = weight_parts(ref, -x, c.hi, c.lo, OneFloat());
+  const bool some = p.y < 46.f;
+  const unsigned long long w = some ? weight_of_parts(p.y, p.t, p.l, p.tail, table, n) : 0ull;
+  // (where an infinite temperature meets a difference that has no fp32 value)
+  const bool even = x == ref || (c.hi == 0.f && ref - ref == 0.f && x - x == 0.f);
+  if (even || !some) n = 0;
+  return even ? ONE : w;
+}
+
+NVFP4_HD unsigned long long rounded_weight(unsigned long long w, int n) { return (((w << 1) >> n) + 1) >> 1; }
 
 // round(2^44 exp((x - ref) / T))
 NVFP4_HD unsigned long long weight(float ref, float x, const Slope& c, const unsigned long long* table) {
   int n;
   const unsigned long long w = weight_and_scale(ref, x, c, table, n);
-  return (w + ((1ull << n) >> 1)) >> n;
+  return rounded_weight(w, n);
 }
 
 // ceil(x / w) where that is below 2^21 (w = 0: 0).
