@@ -485,9 +485,10 @@ int nvfp4_kv_compact(nvfp4_kv_cache_t cache, int32_t* table, int64_t table_strid
  *             NULL exactly if residual is
  *   K         a multiple of 8 (NVFP4 output: of 16), at most 32768
  *   tokens * heads <= 2^30; eps >= 0, finite.
- * All base pointers 16-byte aligned. Sums of squares are fp32: rows whose mean
- * square lies above 2^127 / K give zeros. A NaN in a row makes the row NaN (NVFP4
- * has none: the codes of such a row mean nothing). */
+ * All base pointers 16-byte aligned. Squares and their sum are fp32: a row with
+ * values above 2^63 / sqrt(K) gives zeros or NaN, and with eps = 0 one of values
+ * below 2^-63 loses bits. A NaN in a row makes the row NaN (NVFP4 has none: the
+ * codes of such a row mean nothing). */
 typedef struct nvfp4_norm {
   const void* x;
   const void* weight;

@@ -170,6 +170,7 @@ class QTensor:
                        self.rows, self.K, self.batch, self.scale_layout)
 
 
+@lru_cache(maxsize=1024)
 def scales_bytes(rows: int, K: int, layout: int) -> int:
     return int(lib().nvfp4_scales_bytes(rows, K, layout))
 
@@ -259,9 +260,11 @@ def gemm_w4a4(a: QTensor, w: QTensor, out: torch.Tensor | None = None,
     """Y = s_tA s_tW (A_q @ W_q^T) on the block-scaled FP4 tensor cores."""
     _require_cuda(a.codes)
     y = out if out is not None else torch.empty(a.rows, w.rows, dtype=torch.bfloat16, device=a.codes.device)
-    ws = workspace if workspace is not None else _workspace(workspace_size(OP_GEMM_W4A4, a.rows, w.rows, a.K),
-                                                            a.codes.device)
-    _check(lib().nvfp4_gemm_w4a4(a.c(), w.c(), _ptr(y), _ptr(ws), ws.numel(), _stream()), "nvfp4_gemm_w4a4")
+    ws = workspace
+    if ws is None and (a.scale_layout != SCALES_MMA or w.scale_layout != SCALES_MMA):   # (scales to be laid out)
+        ws = _workspace(workspace_size(OP_GEMM_W4A4, a.rows, w.rows, a.K), a.codes.device)
+    _check(lib().nvfp4_gemm_w4a4(a.c(), w.c(), _ptr(y), _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
+           "nvfp4_gemm_w4a4")
     return y
 
 
@@ -701,7 +704,9 @@ def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None, eps: 
         st, mode = torch.empty(1, dtype=torch.float32, device=dev), ST_COMPUTE
         ws = _given_ws(workspace) if workspace is not None else _workspace(workspace_size(OP_RMS_NORM_QUANTIZE, rows), dev)
     else:
-        st, mode, ws = s_t.to(device=dev, dtype=torch.float32).reshape(1).contiguous(), ST_GIVEN, None
+        st, mode, ws = s_t, ST_GIVEN, None
+        if st.dtype != torch.float32 or st.shape != (1,) or st.device != dev:
+            st = st.to(device=dev, dtype=torch.float32).reshape(1).contiguous()
     _check(lib().nvfp4_rms_norm_quantize(c, codes.data_ptr(), scales.data_ptr(), st.data_ptr(), mode, scale_layout,
                                          _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
            "nvfp4_rms_norm_quantize")

@@ -12,8 +12,12 @@
 //
 // Bound by HBM for many rows, by latency (one load, one reduction, one store)
 // for few. One row stays in registers between its only read and its only
-// write. Rows of up to 1024 elements (heads of 64 or 128 among them) belong to
-// 8, 16 or 32 lanes of a warp and need no block-wide step; longer rows to a CTA.
+// write; what is read once is loaded evict-first (2048 x 2048: 7.8 -> 7.1 us,
+// 2048 x 16384 with an fp32 stream 71 -> 69). Measured in graphs of calls on
+// changing inputs, bf16 stream and output: 1 x 5120 2.4 us, 512 x 5120 5.8,
+// 8192 x 5120 56 (6.0 TB/s); E4M3 output, fp32 stream, 8192 x 5120 72 (6.4 TB/s).
+// Rows of up to 1024 elements (heads of 64 or 128 among them) belong to 8, 16 or
+// 32 lanes of a warp and need no block-wide step; longer rows to a CTA.
 #include "common.cuh"
 #include "launch.h"
 #include "quant_core.cuh"
@@ -76,12 +80,12 @@ struct Raw {
 
 template <int RES>
 NVFP4_DEV void load_raw(const uint16_t* x, const void* residual, int64_t at, Raw<RES>& raw) {
-  raw.x = *reinterpret_cast<const uint4*>(x);
-  if (RES == RES_BF16) raw.r[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(residual) + at);
+  raw.x = __ldcs(reinterpret_cast<const uint4*>(x));
+  if (RES == RES_BF16) raw.r[0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(residual) + at));
   if (RES == RES_F32) {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(residual) + at);
-    raw.r[0] = p[0];
-    raw.r[RES == RES_F32 ? 1 : 0] = p[1];
+    raw.r[0] = __ldcs(p);
+    raw.r[RES == RES_F32 ? 1 : 0] = __ldcs(p + 1);
   }
 }
 
@@ -189,7 +193,8 @@ NVFP4_DEV float e4m3_row_scale(float most, float& inv) {
 NVFP4_DEV float rms_r(float sum, const NormArgs& a) { return rsqrtf(sum / static_cast<float>(a.K) + a.eps); }
 
 // ---- a row for TPR lanes of a warp: K <= 8 * TPR * VPT
-template <int OUT, int RES, int TPR, int VPT>
+// ROWS of them at a time, where a row is one load of a lane: more bytes in flight (4096 x 40 heads of 128: 18.6 -> 16.8 us)
+template <int OUT, int RES, int TPR, int VPT, int ROWS>
 __global__ void __launch_bounds__(256) norm_lanes_kernel(const NormArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -199,53 +204,62 @@ __global__ void __launch_bounds__(256) norm_lanes_kernel(const NormArgs a) {
   const TensorScale ts = tensor_scale(OUT == OUT_NVFP4 ? *a.s_t : 1.0f);
   float most_all = 0.f;
   // (all lanes of a warp walk the same number of rows: the reductions are warp-wide)
-  for (int row0 = blockIdx.x * per_cta; row0 < a.rows_p; row0 += gridDim.x * per_cta) {
-    const int row = row0 + threadIdx.x / TPR;
-    const bool live = row < a.rows;
-    const int token = live ? row / a.heads : 0, head = live ? row - token * a.heads : 0;
-    const uint16_t* xr = a.x + token * a.x_stride + static_cast<int64_t>(head) * a.K;
-    const int64_t base = static_cast<int64_t>(row) * a.K;
-    Raw<RES> raw[VPT];
-    float t[VPT][8], sum = 0.f, most = 0.f;
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * (per_cta * ROWS); row0 < a.rows_p; row0 += static_cast<int64_t>(gridDim.x) * (per_cta * ROWS)) {
+    Raw<RES> raw[ROWS][VPT];
+    int64_t y_at[ROWS];
+    bool live[ROWS];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = lane + i * TPR;
-      if (live && v < nvec) load_raw<RES>(xr + v * 8, a.residual, base + v * 8, raw[i]);
-    }
+    for (int j = 0; j < ROWS; ++j) {
+      const int row = static_cast<int>(row0) + j * per_cta + threadIdx.x / TPR;
+      live[j] = row < a.rows;
+      const int token = live[j] ? row / a.heads : 0, head = live[j] ? row - token * a.heads : 0;
+      const uint16_t* xr = a.x + token * a.x_stride + static_cast<int64_t>(head) * a.K;
+      y_at[j] = token * a.y_stride + static_cast<int64_t>(head) * a.K;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = lane + i * TPR;
-      if (live && v < nvec) {
-        stream8<RES>(raw[i], a.residual_out, base + v * 8, t[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(t[i][e], t[i][e], sum);
-        gain8(a.weight, a.offset, v * 8, t[i]);
-        if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, amax8(t[i]));
+      for (int i = 0; i < VPT; ++i) {
+        const int v = lane + i * TPR;
+        if (live[j] && v < nvec) load_raw<RES>(xr + v * 8, a.residual, static_cast<int64_t>(row) * a.K + v * 8, raw[j][i]);
       }
     }
 #pragma unroll
-    for (int o = TPR / 2; o > 0; o >>= 1) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    }
-    const float r = rms_r(sum, a);
-    float inv = 0.f;
-    if (OUT == OUT_E4M3) {
-      const float scale = e4m3_row_scale(most * r, inv);
-      if (live && lane == 0) static_cast<float*>(a.scales)[row] = scale;
-    }
-    if (OUT == OUT_STATS) {
-      if (live && lane == 0) a.row_r[row] = r;
-      if (live) most_all = fmaxf(most_all, most * r);
-      continue;
-    }
-    const int64_t y_at = token * a.y_stride + static_cast<int64_t>(head) * a.K;
+    for (int j = 0; j < ROWS; ++j) {
+      const int row = static_cast<int>(row0) + j * per_cta + threadIdx.x / TPR;
+      const int64_t base = static_cast<int64_t>(row) * a.K;
+      float t[VPT][8], sum = 0.f, most = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = lane + i * TPR;
-      if (live && v < nvec) store8<OUT>(a, row, y_at, v * 8, t[i], r, inv, &ts);
+      for (int i = 0; i < VPT; ++i) {
+        const int v = lane + i * TPR;
+        if (live[j] && v < nvec) {
+          stream8<RES>(raw[j][i], a.residual_out, base + v * 8, t[i]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum = fmaf(t[i][e], t[i][e], sum);
+          gain8(a.weight, a.offset, v * 8, t[i]);
+          if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, amax8(t[i]));
+        }
+      }
+#pragma unroll
+      for (int o = TPR / 2; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      }
+      const float r = rms_r(sum, a);
+      float inv = 0.f;
+      if (OUT == OUT_E4M3) {
+        const float scale = e4m3_row_scale(most * r, inv);
+        if (live[j] && lane == 0) static_cast<float*>(a.scales)[row] = scale;
+      }
+      if (OUT == OUT_STATS) {
+        if (live[j] && lane == 0) a.row_r[row] = r;
+        if (live[j]) most_all = fmaxf(most_all, most * r);
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = lane + i * TPR;
+        if (live[j] && v < nvec) store8<OUT>(a, row, y_at[j], v * 8, t[i], r, inv, &ts);
+      }
+      if (OUT == OUT_NVFP4 && a.mma && row < a.rows_p) pad_scales(a, row, live[j] ? a.K >> 4 : 0, lane, TPR);
     }
-    if (OUT == OUT_NVFP4 && a.mma && row < a.rows_p) pad_scales(a, row, live ? a.K >> 4 : 0, lane, TPR);
   }
   if (OUT == OUT_STATS) {
     __shared__ unsigned int s_most;
@@ -340,47 +354,110 @@ __global__ void __launch_bounds__(VPT > 1 ? 512 : 1024) norm_cta_kernel(const No
 }
 
 // ---- the codes of a tensor whose scale had to be found first: y = s * (w + offset) * r is formed again
-// from the stream (or x) and each row's r, so both passes see the same y.
+// from the stream (or x) and each row's r, so both passes see the same y. A lane takes a block of 16, a warp 32
+// blocks of a row at a time, two such chunks in flight; the block step's constants come from tables, as in
+// the quantiser (4096 x 5120, bf16 stream: one row for a CTA, halves of blocks, reciprocals formed 33.8 us; this 17.6).
+template <bool F32>
+struct RawBlock {
+  uint4 w[F32 ? 4 : 2];
+};
+
+template <bool F32>
+NVFP4_DEV void load_block(const void* s, int64_t at, RawBlock<F32>& r) {
+  const uint4* p = F32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(s) + at)
+                       : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s) + at);
+#pragma unroll
+  for (int i = 0; i < (F32 ? 4 : 2); ++i) r.w[i] = __ldg(p + i);
+}
+
+template <bool F32>
+NVFP4_DEV void unpack_block(const RawBlock<F32>& r, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+    const uint32_t u[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (F32) {
+        v[4 * i + e] = __uint_as_float(u[e]);
+      } else {
+        v[8 * i + 2 * e] = __uint_as_float(u[e] << 16);
+        v[8 * i + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(256) norm_encode_kernel(const NormArgs a, const void* s, int64_t s_stride, int n_partial,
                                                           float* s_t) {
   __shared__ unsigned int s_most;
+  __shared__ QuantTables tab;
   pdl_wait();
   pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int bpr = a.K >> 4, cpr = (bpr + 31) >> 5;
+  const int64_t chunks = static_cast<int64_t>(a.rows) * cpr, step = static_cast<int64_t>(gridDim.x) * 8;
+  int64_t chunk = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  struct At {
+    int row, block;
+  };
+  auto at_chunk = [&](int64_t c) {
+    const int row = static_cast<int>(c / cpr);
+    return At{row, static_cast<int>(c - static_cast<int64_t>(row) * cpr) * 32 + lane};
+  };
+  auto load = [&](const At& p, RawBlock<F32>& raw, float& r) {
+    if (p.block >= bpr) return;
+    const int token = p.row / a.heads, head = p.row - token * a.heads;
+    load_block<F32>(s, token * s_stride + static_cast<int64_t>(head) * a.K + p.block * 16, raw);
+    r = a.row_r[p.row];
+  };
+  RawBlock<F32> raw = {}, next = {};
+  float r = 0.f, next_r = 0.f;
+  At at = {0, bpr};
+  if (chunk < chunks) load(at = at_chunk(chunk), raw, r);
   if (threadIdx.x == 0) s_most = 0u;
   __syncthreads();
   unsigned int m = 0u;
   for (int i = threadIdx.x; i < n_partial; i += blockDim.x) m = max(m, __ldcg(a.partial + i));
   m = __reduce_max_sync(0xffffffffu, m);
-  if ((threadIdx.x & 31) == 0) atomicMax(&s_most, m);
+  if (lane == 0) atomicMax(&s_most, m);
   __syncthreads();
   const float amax = __uint_as_float(s_most);
   const TensorScale ts = tensor_scale(amax > 0.f ? __fdiv_rn(amax, 2688.0f) : 1.0f);
   if (blockIdx.x == 0 && threadIdx.x == 0) *s_t = ts.st;
-  const int nvec = a.K >> 3;
-  for (int row = blockIdx.x; row < a.rows_p; row += gridDim.x) {
-    if (row >= a.rows) {
-      pad_scales(a, row, 0, threadIdx.x, blockDim.x);
-      continue;
-    }
-    const int token = row / a.heads, head = row - token * a.heads;
-    const int64_t at = token * s_stride + static_cast<int64_t>(head) * a.K;
-    const float r = a.row_r[row];
-    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-      float t[8];
-      if (F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(s) + at + v * 8);
-        const float4 lo = p[0], hi = p[1];
-        t[0] = lo.x; t[1] = lo.y; t[2] = lo.z; t[3] = lo.w;
-        t[4] = hi.x; t[5] = hi.y; t[6] = hi.z; t[7] = hi.w;
-      } else {
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s) + at + v * 8), t);
+  quant_tables_init(tab, ts.st);
+  __syncthreads();
+  for (; chunk < chunks; chunk += step) {
+    At then = {0, bpr};
+    if (chunk + step < chunks) load(then = at_chunk(chunk + step), next, next_r);
+    if (at.block < bpr) {
+      float t[16], most = 0.f;
+      unpack_block<F32>(raw, t);
+      if (a.weight) {
+        RawBlock<false> w;
+        load_block<false>(a.weight, at.block * 16, w);
+        float g[16];
+        unpack_block<false>(w, g);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) t[e] *= g[e] + a.offset;
       }
-      gain8(a.weight, a.offset, v * 8, t);
-      store8<OUT_NVFP4>(a, row, 0, v * 8, t, r, 0.f, &ts);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        t[e] *= r;
+        most = fmaxf(most, fabsf(t[e]));
+      }
+      uint2 codes;
+      const uint32_t sc = quant_block16_tab(t, most, ts.d, ts.rdh, ts.rdl, tab, codes);
+      reinterpret_cast<uint2*>(a.out)[static_cast<int64_t>(at.row) * bpr + at.block] = codes;
+      static_cast<uint8_t*>(a.scales)[a.mma ? mma_row_offset(at.row, a.cols4) + (at.block >> 2) * 512 + (at.block & 3)
+                                            : static_cast<int64_t>(at.row) * bpr + at.block] = static_cast<uint8_t>(sc);
     }
-    if (a.mma) pad_scales(a, row, a.K >> 4, threadIdx.x, blockDim.x);
+    at = then;
+    raw = next;
+    r = next_r;
   }
+  if (a.mma)   // the layout's padding
+    for (int row = blockIdx.x; row < a.rows_p; row += gridDim.x) pad_scales(a, row, row < a.rows ? bpr : 0, threadIdx.x, blockDim.x);
 }
 
 constexpr int PARTIALS = 2048;   // CTAs of a statistics pass at most
@@ -392,23 +469,31 @@ int launch_rows(const NormArgs& a, int* grid, cudaStream_t stream) {
   const int most = OUT == OUT_STATS ? PARTIALS : 1 << 30;
   if (a.K <= 1024) {
     const int tpr = nvec <= 8 ? 8 : nvec <= 16 ? 16 : 32, vpt = static_cast<int>(ceil_div(nvec, tpr));
-    const int64_t want = ceil_div(a.rows_p, 256 / tpr);
+    // several rows at a time only where the CTAs fill the SMs all the same
+    const bool many = vpt == 1 && a.rows_p >= static_cast<int64_t>(sm_count()) * 8 * (256 / tpr) * 4;
+    const int64_t want = ceil_div(a.rows_p, 256 / tpr * (many ? 4 : 1));
     *grid = static_cast<int>(want < most ? want : most);
-#define NVFP4_LANES(T, V) return launch_ex(norm_lanes_kernel<OUT, RES, T, V>, dim3(*grid), dim3(256), 0, 1, true, stream, a)
-    if (tpr == 8) NVFP4_LANES(8, 1);
-    if (tpr == 16) NVFP4_LANES(16, 1);
-    if (vpt == 1) NVFP4_LANES(32, 1);
-    if (vpt == 2) NVFP4_LANES(32, 2);
-    NVFP4_LANES(32, 4);
+#define NVFP4_LANES(T, V, R) \
+  return launch_ex(norm_lanes_kernel<OUT, RES, T, V, R>, dim3(*grid), dim3(256), 0, 1, true, stream, a)
+    if (tpr == 8 && many) NVFP4_LANES(8, 1, 4);
+    if (tpr == 8) NVFP4_LANES(8, 1, 1);
+    if (tpr == 16 && many) NVFP4_LANES(16, 1, 4);
+    if (tpr == 16) NVFP4_LANES(16, 1, 1);
+    if (vpt == 1 && many) NVFP4_LANES(32, 1, 4);
+    if (vpt == 1) NVFP4_LANES(32, 1, 1);
+    if (vpt == 2) NVFP4_LANES(32, 2, 1);
+    NVFP4_LANES(32, 4, 1);
 #undef NVFP4_LANES
   }
-  // few rows: as many threads as a row has vectors of eight; many rows: four vectors a thread, so that
-  // more loads are in flight for each reduction
-  const int vpt = nvec > 2048 ? 8 : nvec > 1024 || a.rows >= 4 * sm_count() ? 4 : 1;
+  // fewer rows than SMs: as many threads as a row has vectors of eight (32 x 5120: 2.5 us; two vectors a thread
+  // 2.6, four 3.0); more: two a thread (512 x 5120: 5.8 us; one 8.5, four 6.9; 8192 x 5120: 55; 108; 57), and four
+  // for the statistics pass, whose CTAs take several rows
+  const int vpt = nvec > 2048 ? 8 : nvec > 1024 ? 4 : a.rows >= sm_count() ? (OUT == OUT_STATS ? 4 : 2) : 1;
   const int threads = static_cast<int>(ceil_div(ceil_div(nvec, vpt), 32) * 32);
   *grid = a.rows_p < most ? a.rows_p : most;
 #define NVFP4_CTA(V) return launch_ex(norm_cta_kernel<OUT, RES, V>, dim3(*grid), dim3(threads), 0, 1, true, stream, a)
   if (vpt == 1) NVFP4_CTA(1);
+  if (vpt == 2) NVFP4_CTA(2);
   if (vpt == 4) NVFP4_CTA(4);
   NVFP4_CTA(8);
 #undef NVFP4_CTA
@@ -484,7 +569,8 @@ int launch_rms_norm_quantize(const nvfp4_norm_t& n, uint8_t* codes, uint8_t* sca
   const int res = res_of(n);
   const void* s = res == RES_NONE ? n.x : n.residual_out;
   const int64_t s_stride = res == RES_NONE ? n.x_stride : static_cast<int64_t>(n.heads) * n.K;
-  const int ctas = rows_p < 1 ? 1 : rows_p < 8 * sm_count() ? rows_p : 8 * sm_count();
+  const int64_t chunks = static_cast<int64_t>(rows_p) * ceil_div(n.K / 16, 32);
+  const int ctas = static_cast<int>(chunks < 8 ? 1 : chunks < 8ll * 4 * sm_count() ? ceil_div(chunks, 8) : 4 * sm_count());
   return res == RES_F32
              ? launch_ex(norm_encode_kernel<true>, dim3(ctas), dim3(256), 0, 1, true, stream, a, s, s_stride, grid, s_t)
              : launch_ex(norm_encode_kernel<false>, dim3(ctas), dim3(256), 0, 1, true, stream, a, s, s_stride, grid, s_t);
