@@ -510,7 +510,7 @@ typedef struct nvfp4_norm {
 int nvfp4_rms_norm(nvfp4_norm_t in, void* Y, int64_t y_stride, nvfp4_stream_t stream);
 
 /* y as E4M3 with one scale for each row, for linears kept in 8 bits:
- *   scales[row] = max|y| / 448 (1 for a row of zeros), codes = y / scales[row]
+ *   scales[row] = max|y| / 448 (1 for a row of zeros, else 2^-120 at least), codes = y / scales[row]
  * rounded to nearest even. A NaN of y is the code 0x7F.
  *   codes   device out uint8 [tokens][heads][K], 16-byte aligned
  *   scales  device out fp32 [tokens * heads] */
@@ -523,7 +523,8 @@ int nvfp4_rms_norm_e4m3(nvfp4_norm_t in, uint8_t* codes, float* scales, nvfp4_st
  *      GIVEN is one pass. COMPUTE finds s_t first and forms y again from s (or
  *      x), which must not change before the call has finished.
  *   workspace  >= nvfp4_workspace_size(NVFP4_OP_RMS_NORM_QUANTIZE, tokens * heads, ...)
- *      bytes, 16-byte aligned (COMPUTE only; may be NULL for GIVEN); scratch. */
+ *      bytes, 16-byte aligned (COMPUTE only; may be NULL for GIVEN); scratch of one
+ *      call at a time. */
 int nvfp4_rms_norm_quantize(nvfp4_norm_t in, uint8_t* codes, uint8_t* scales, float* s_t, int s_t_mode,
                             int scale_layout, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
 
@@ -563,7 +564,8 @@ typedef struct nvfp4_sampling {
  * within about 2^-35 of a border between two tokens. The same inputs give the
  * same tokens.
  *   logits   device, bf16 or fp32 (dtype), row r at r * stride elements,
- *            aligned to its type; any vocab of 1 .. 524288 (stride >= vocab)
+ *            aligned to its type; any vocab of 1 .. 524288; stride >= vocab, or 0:
+ *            every row draws from the same logits
  *   uniform  device fp32 [rows], in [0, 1); below 0 and NaN as 0, 1 and more:
  *            the last token kept
  *   rows     <= 2^20 */

@@ -742,7 +742,7 @@ def _sampling(logits, uniform, settings, n):
             _beside(d, v)
             args[i] = v.data_ptr()
         else:
-            args[4 + i] = v
+            args[4 + i] = v if i != 1 else max(0, min(v, 0x7FFFFFFF))   # (ctypes would cut an int's upper bits off)
     return dtype, rows, vocab, stride if rows > 1 else vocab, CSampling(*args), d
 
 

@@ -111,7 +111,7 @@ int norm_check(const nvfp4_norm_t& n, int granule) {
 
 int logits_check(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const float* uniform) {
   if (dtype != NVFP4_DTYPE_F32 && dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_INVALID_ARG;
-  if (rows < 0 || vocab < 1 || stride < vocab) return NVFP4_ERR_INVALID_ARG;
+  if (rows < 0 || vocab < 1 || (stride < vocab && stride != 0)) return NVFP4_ERR_INVALID_ARG;
   if (vocab > 524288 || rows > (1 << 20)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (rows == 0) return NVFP4_OK;
   if (!logits || !uniform) return NVFP4_ERR_INVALID_ARG;

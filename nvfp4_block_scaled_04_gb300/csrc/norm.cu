@@ -183,9 +183,10 @@ NVFP4_DEV void pad_scales(const NormArgs& a, int row, int first, int lane, int l
   for (int c = first + lane; c < a.cols4; c += lanes) p[static_cast<int64_t>(c >> 2) * 512 + (c & 3)] = 0;
 }
 
-// The row's E4M3 scale a = max|y| / 448 (1 for a row of zeros) and what y is multiplied with.
+// The row's E4M3 scale a = max|y| / 448 (1 for a row of zeros; 2^-120 at least, so that 1 / a is finite) and what y
+// is multiplied with.
 NVFP4_DEV float e4m3_row_scale(float most, float& inv) {
-  const float a = most > 0.f ? __fdiv_rn(most, 448.0f) : 1.0f;
+  const float a = most > 0.f ? fmaxf(__fdiv_rn(most, 448.0f), 0x1p-120f) : 1.0f;
   inv = __fdiv_rn(1.0f, a);
   return a;
 }

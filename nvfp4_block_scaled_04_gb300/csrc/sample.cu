@@ -282,7 +282,9 @@ struct Slice {
   NVFP4_DEV void each_of(uint32_t lo, uint32_t hi, F f) const {
     const float least = value_of<F32>(lo), most = value_of<F32>(hi);
     each([&](float x, uint32_t b, int i) {
-      if (x >= least && x <= most) f(key_of<F32>(b), i);   // (not a NaN)
+      if (!(x >= least && x <= most)) return;   // (also a NaN)
+      const uint32_t k = key_of<F32>(b);
+      if (k >= lo && k <= hi) f(k, i);          // (the highest key below 0 is that of no value, and compares as 0)
     });
   }
 };

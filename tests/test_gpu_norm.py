@@ -208,6 +208,20 @@ def test_values_that_are_not_ordinary(nv, K):
     check_nvfp4(q, y[good], float(s_t.double()), 1)
 
 
+@pytest.mark.parametrize("K", [64, 4096])
+def test_rows_next_to_the_smallest_numbers(nv, K):
+    """8-bit rows whose scale would be too small to divide by: codes and scales stay finite, and near."""
+    x, w, _ = inputs(6, K, 5, None)
+    x = (x.float() * torch.tensor([2.0 ** -126, 2.0 ** -130, 2.0 ** -133, 2.0 ** -120, 2.0 ** -110, 0.0])[:, None]).bfloat16()
+    y = norm(x, w, EPS)
+    codes, scales = nv.rms_norm_e4m3(x.cuda(), w.cuda(), EPS)
+    s = scales.cpu().double()
+    assert bool((s >= 2.0 ** -120).all()) and float(s[5]) == 1.0
+    got = codes.cpu().double() * s[:, None]
+    # half a step of E4M3, and fp32's own smallest step (2^-149) in y and the products before it
+    assert bool(((got - y).abs() <= y.abs() * (2.0 ** -4 + 4 * REL) + s[:, None] * 2.0 ** -10 + 2.0 ** -137).all())
+
+
 def test_zeros_as_nvfp4(nv):
     q = nv.rms_norm_quantize(torch.zeros(5, 64, dtype=torch.bfloat16, device="cuda"))
     assert float(q.s_t) == 1.0 and not q.codes.any() and not q.scales.any()

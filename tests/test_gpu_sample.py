@@ -102,6 +102,12 @@ def special(kind, rows, vocab, dtype, seed):
         x[:, vocab // 2] = 0.02
     elif kind == "padded":          # a padded vocabulary's columns are zero
         x[:, vocab // 2:] = 0
+    elif kind == "zeros and just below":   # many of both: the bin below zero is counted again, beside zeros that are not in it
+        x = torch.where(torch.rand(x.shape, generator=g) < 0.4, 0.0, -x.abs() * 1e-5)
+        x[:, ::7] = -0.0
+    elif kind == "zeros and around":
+        x = torch.where(torch.rand(x.shape, generator=g) < 0.4, 0.0, x * 1e-4)
+        x[:, 5] = 0.5
     elif kind == "negative":
         x = x - 40
     elif kind == "below the lowest bin":
@@ -133,7 +139,7 @@ def special(kind, rows, vocab, dtype, seed):
     return x.to(dtype)
 
 
-KINDS = ["equal", "zeros", "two values", "tiny", "tiny, one ahead", "padded", "negative", "below the lowest bin", "above the highest bin", "both sides",
+KINDS = ["equal", "zeros", "two values", "tiny", "tiny, one ahead", "padded", "zeros and just below", "zeros and around", "negative", "below the lowest bin", "above the highest bin", "both sides",
          "lowest value", "all lowest", "masked", "one left", "none left", "nan", "infinite", "infinite, one"]
 
 
@@ -154,6 +160,22 @@ def test_ends_of_the_random_numbers_and_of_the_settings(nv, dtype):
     for kw in ({}, dict(k=3), dict(p=0.5), dict(m=0.1), dict(k=1), dict(k=2000), dict(k=1999), dict(k=-4), dict(p=0.0), dict(p=-1.0), dict(p=1.5),
                dict(p=math.nan), dict(m=1.0), dict(m=3.0), dict(m=-1.0), dict(m=math.nan), dict(t=-1.0), dict(t=math.nan), dict(k=2 ** 31 - 1)):
         check(nv, x, u, **kw)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_draws_from_one_row(nv, dtype):
+    """Rows that are one row of memory (stride 0)."""
+    x = logits(1, 5000, dtype, 8)
+    many = x.cuda().expand(70, -1)
+    check(nv, x.expand(70, -1), uniform(70, 3), p=0.9, device_x=many)
+    check(nv, x.expand(70, -1), uniform(70, 4), t=0.5, device_x=many)
+
+
+def test_a_whole_number_that_32_bits_do_not_hold(nv):
+    x, u = logits(3, 900, torch.bfloat16, 2), uniform(3, 9)
+    for k in (1 << 31, (1 << 32) + 3, -(1 << 40)):
+        ids, _ = nv.sample(x.cuda(), u.cuda(), 1.0, k)
+        assert torch.equal(ids, nv.sample(x.cuda(), u.cuda())[0])
 
 
 def test_equal_tokens_are_drawn_by_index(nv):

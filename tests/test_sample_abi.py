@@ -17,7 +17,7 @@ def verify(m, logits=P, dtype=1, batch=2, drafts=3, vocab=100, stride=100, u=P, 
 
 
 BAD = [(dict(logits=None), -1), (dict(u=None), -1), (dict(ids=None), -1), (dict(dtype=2), -1), (dict(dtype=-1), -1), (dict(vocab=0), -1), (dict(vocab=-5), -1),
-       (dict(stride=99), -1), (dict(vocab=524289, stride=1 << 20), -2), (dict(logits=P + 1), -3), (dict(logits=P + 2, dtype=0), -3)]
+       (dict(stride=99), -1), (dict(stride=-100), -1), (dict(stride=1), -1), (dict(vocab=524289, stride=1 << 20), -2), (dict(logits=P + 1), -3), (dict(logits=P + 2, dtype=0), -3)]
 
 
 @pytest.mark.parametrize("kw,code", BAD)
