@@ -22,11 +22,11 @@
 // Work. A cluster of 1 to 16 CTAs takes a row, each a slice of it; counts are joined through distributed
 // shared memory, and the first warp of the cluster's first CTA searches and hands out commands. HBM sees each
 // bf16 logit once (fp32: twice where the logits exceed L2; their masses need the row's maximum first).
-//   few rows: latency, 33 thousand clocks of dependent steps, of which a third are waits at the four cluster
-//     barriers and a third the searches (1 row of 248,320 bf16: 15.9 us, in a graph; 64 rows: 25.9 us)
-//   many rows: atomics in shared memory, one for each logit, 4.5 clocks for a warp's (256 rows: 64 us, of which
-//     34 are atomics; HBM alone would take 18.7)
-//   fp32: the instructions of the weights (24 rows of 151,937: 51 us; 128 rows of 248,320: 193 us)
+//   few rows: latency, 30 thousand clocks of dependent steps, a third of them waits at the four cluster barriers and a
+//     quarter the searches (1 row of 248,320 bf16: 15.5 us, in a graph; 64 rows: 25.3 us)
+//   many rows: atomics in shared memory, one for each logit, 3.3 to 4.8 clocks for a warp's (256 rows: 64 us, of which
+//     the pass that counts takes 36 where an SM has two rows; HBM alone would take 18.7)
+//   fp32: the instructions of the weights, 60% of the issue slots (24 rows of 151,937: 51 us; 128 of 248,320: 193 us)
 // Steps that carried it: bins of two logits at a time from clamped magnitudes; one warp searching by ballots in
 // place of the CTA; one copy of each rare piece of code (instruction fetches bound the single pass); masses
 // in two 32-bit words (a 64-bit atomic is a loop: 11 to 1700 clocks); two weights to an instruction.
@@ -416,8 +416,6 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
     setting = lane == 0 ? __int_as_float(a.set.top_k_all) : lane == 1 ? a.set.top_p_all : a.set.min_p_all;
     if (p) setting = p[lane == 3 ? row : entry];
   }
-  const bool greedy = !(temperature > 0.f);
-  const Slope slope = slope_of(greedy ? 1.f : temperature);
 
   Slice<F32> slice;
   {
@@ -452,9 +450,17 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
 
   uint32_t row_max;
   bool irregular = false;
+  // (the temperature is looked at behind the pass over the logits: its load takes as long as theirs)
+  bool greedy;
+  Slope slope;
+  auto look_at_temperature = [&]() {
+    greedy = !(temperature > 0.f);
+    slope = slope_of(greedy ? 1.f : temperature);
+  };
   if (F32) {
     int holder;
     row_max = row_max_of(holder);
+    look_at_temperature();
     if (tid == 0) sh.cmd = {CMD_FIND, 0u, 0u, 0, row_max, 1u, holder};
     __syncthreads();
   } else {
@@ -500,6 +506,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
       most = __reduce_max_sync(0xffffffffu, max(most & 0xFFFFu, most >> 16));
       if (lane == 0) room_most[turn * S_WARPS + warp] = static_cast<uint16_t>(most);
     }
+    look_at_temperature();
     __syncthreads();
     {
       unsigned long long mid[2] = {0ull, 0ull};
@@ -816,8 +823,8 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
             }
             if (single || c == 0 || hi < lo) {
               key = hi;
-              const unsigned long long w = weigh(key);
-              nth = how == BY_KEY ? c : how == BY_COUNT ? static_cast<uint32_t>(target) - c0 : few_times(target - m0, w);
+              const unsigned long long w = c == 1 ? m : weigh(key);   // (a call and a division less for most drawn tokens)
+              nth = c == 1 ? 1u : how == BY_KEY ? c : how == BY_COUNT ? static_cast<uint32_t>(target) - c0 : few_times(target - m0, w);
               nth = max(1u, min(nth, c));
               through = m0 + min(nth, c) * w;
               done = true;
