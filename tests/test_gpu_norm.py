@@ -245,6 +245,29 @@ def test_neighbours_of_the_output_stay(nv):
     assert bool((big[0] == 7).all() and (big[6] == 7).all() and (big[:, 200:] == 7).all())
 
 
+def test_refusals(nv):
+    x, w, r = (cuda(t) for t in inputs(4, 64, 1))
+    for bad in (dict(weight=w[:32]), dict(weight=w.float()), dict(weight=w.repeat(2)[::2]), dict(residual=r.half()), dict(residual=r[:3]),
+                dict(residual=r.t().contiguous().t()), dict(residual=r, residual_out=r.float()), dict(residual=r, residual_out=r[:2]), dict(residual_out=r),
+                dict(out=x[:3]), dict(out=x.float()), dict(out=x.t().contiguous().t())):
+        with pytest.raises(ValueError):
+            nv.rms_norm(x, **{"weight": w, **bad})
+    for bad in (dict(weight=w.cpu()), dict(residual=r.cpu()), dict(residual=r, residual_out=r.cpu()), dict(out=x.cpu())):
+        with pytest.raises(RuntimeError, match="CUDA"):
+            nv.rms_norm(x, **{"weight": w, **bad})
+    with pytest.raises(RuntimeError, match="unsupported shape"):
+        nv.rms_norm(x[:, :60].contiguous(), None)
+    with pytest.raises(RuntimeError, match="unsupported shape"):
+        nv.rms_norm_quantize(x[:, :56].contiguous(), None)
+    with pytest.raises(RuntimeError, match="invalid argument"):
+        nv.rms_norm(x, w, eps=-1.0)
+    with pytest.raises(RuntimeError, match="workspace"):
+        nv.rms_norm_quantize(x, w, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(RuntimeError, match="misaligned"):
+        nv.rms_norm(x, w, out=torch.empty(5 * 64, dtype=torch.bfloat16, device="cuda")[1:257].view(4, 64))
+    assert torch.equal(x.cpu(), inputs(4, 64, 1)[0])
+
+
 def test_in_a_graph_on_a_side_stream(nv):
     """A captured step (norm, linear, norm in 4 bits, linear) on new inputs gives what the same calls give outside."""
     rows, K, N = 5, 512, 256

@@ -242,6 +242,32 @@ def test_verification(nv, dtype, batch, drafts, vocab):
     assert torch.equal(ids.view_as(tokens), tokens) and torch.equal(q.view_as(probs), probs)
 
 
+def test_refusals(nv):
+    x, u = logits(4, 100, torch.bfloat16, 1).cuda(), uniform(4, 1).cuda()
+    one = torch.ones(4, device="cuda")
+    for args in ((x, u.double()), (x, u[:3]), (x, u.repeat(2)[::2]), (x, u, one.double()), (x, u, one[:3]), (x, u, 1.0, one), (x, u, 1.0, 0, one.view(2, 2)),
+                 (x, u, 1.0, 0, 1.0, one.repeat(2)[::2])):
+        with pytest.raises(ValueError):
+            nv.sample(*args)
+    for args in ((x, u.cpu()), (x, u, one.cpu()), (x, u, 1.0, one.int().cpu())):
+        with pytest.raises(RuntimeError, match="CUDA"):
+            nv.sample(*args)
+    drafts = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    for args in ((x, u, drafts.long()), (x, u, drafts[:1]), (x, u, drafts, one)):
+        with pytest.raises(ValueError):
+            nv.verify_sample(*args)
+    with pytest.raises(RuntimeError, match="CUDA"):
+        nv.verify_sample(x, u, drafts.cpu())
+    with pytest.raises(RuntimeError, match="unsupported shape"):
+        nv.sample(torch.zeros(1, 524289, dtype=torch.bfloat16, device="cuda"), u[:1])
+    with pytest.raises(RuntimeError, match="invalid argument"):
+        nv.sample(x[:, :0], u)
+    ids, probs = nv.sample(x[:0], u[:0])
+    assert ids.shape == probs.shape == (0,)
+    tokens, accepted, probs = nv.verify_sample(x[:0], u[:0], drafts[:0])
+    assert tokens.shape == probs.shape == (0, 2) and accepted.shape == (0,)
+
+
 def test_in_a_graph_and_on_two_streams(nv):
     rows, vocab = 9, 20000
     x, u, t = logits(rows, vocab, torch.bfloat16, 1).cuda(), uniform(rows, 1).cuda(), torch.ones(rows, device="cuda")
