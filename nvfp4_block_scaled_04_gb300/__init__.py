@@ -666,7 +666,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1
     x, c, s, d = _norm(x, weight, eps, residual, residual_out, weight_offset)
     stride = c.heads * c.K
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        out = torch.empty_like(x) if x.is_contiguous() else torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         st = out.stride()
         if out.shape != x.shape or out.dtype != torch.bfloat16 or st[-1] != 1 or (c.heads > 1 and st[1] != c.K):

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(256) norm_lanes_kernel(const NormArgs a) {
   const int lane = threadIdx.x & (TPR - 1);
   const int per_cta = 256 / TPR;
   const int nvec = a.K >> 3;
-  const TensorScale ts = tensor_scale(OUT == OUT_NVFP4 ? *a.s_t : 1.0f);
+  const float st = OUT == OUT_NVFP4 ? *a.s_t : 1.0f;
   float most_all = 0.f;
   // (all lanes of a warp walk the same number of rows: the reductions are warp-wide)
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * (per_cta * ROWS); row0 < a.rows_p; row0 += static_cast<int64_t>(gridDim.x) * (per_cta * ROWS)) {
@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(256) norm_lanes_kernel(const NormArgs a) {
         if (live[j] && v < nvec) load_raw<RES>(xr + v * 8, a.residual, static_cast<int64_t>(row) * a.K + v * 8, raw[j][i]);
       }
     }
+    const TensorScale ts = tensor_scale(st);   // (behind the rows' loads: st is a load too)
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
       const int row = static_cast<int>(row0) + j * per_cta + threadIdx.x / TPR;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(VPT > 1 ? 512 : 1024) norm_cta_kernel(const No
   pdl_wait();
   pdl_launch_dependents();
   const int nvec = a.K >> 3, warps = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const TensorScale ts = tensor_scale(OUT == OUT_NVFP4 ? *a.s_t : 1.0f);
+  const float st = OUT == OUT_NVFP4 ? *a.s_t : 1.0f;
   float most_all = 0.f;
   int turn = 0;
   for (int row = blockIdx.x; row < a.rows_p; row += gridDim.x, turn ^= 1) {
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(VPT > 1 ? 512 : 1024) norm_cta_kernel(const No
       sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     }
+    const TensorScale ts = tensor_scale(st);   // (behind the row's loads: st is a load too)
     // (two sets of slots in turn: a warp that is a row ahead does not overwrite what a slower one still reads)
     if (lane == 0) {
       s_sum[turn][warp] = sum;

@@ -157,6 +157,7 @@ struct Shared {
   Command cmd;
   uint32_t max_key;                  // of this CTA's slice
   int min_bin;                       // bf16: its first bin that is not empty
+  uint32_t zeros[2];                 // bf16: how many logits are 0, and -0
   uint32_t list_n, noted_n, base;
   uint32_t hits[4 * S_WARPS];
 };
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
 
   if (tid < 64) sh.table[tid] = EXP2_TABLE[tid];
   if (tid < 4) sh.wide_mass[tid] = 0;
-  if (tid == 0) sh.max_key = 0, sh.min_bin = NB, sh.list_n = 0;
+  if (tid == 0) sh.max_key = 0, sh.min_bin = NB, sh.list_n = 0, sh.zeros[0] = sh.zeros[1] = 0;
   for (int b = tid; b < NB; b += S_THREADS) {
     room.count[b] = 0;
     if (F32) lower[b] = 0, upper[b] = 0;
@@ -412,7 +413,10 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
   const bool searcher = first_cta && warp == 0;   // (its lanes hold the row's settings)
   float setting = 0.f;
   if (searcher && lane < 4) {
-    const float* p = lane == 0 ? reinterpret_cast<const float*>(a.set.top_k) : lane == 1 ? a.set.top_p : lane == 2 ? a.set.min_p : a.uniform;
+    const float* p = lane == 0   ? reinterpret_cast<const float*>(a.set.top_k)
+                     : lane == 1 ? a.set.top_p
+                     : lane == 2 ? a.set.min_p
+                                 : a.uniform;
     setting = lane == 0 ? __int_as_float(a.set.top_k_all) : lane == 1 ? a.set.top_p_all : a.set.min_p_all;
     if (p) setting = p[lane == 3 ? row : entry];
   }
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
   }
   __syncthreads();
 
-  // Largest key of the row, and (greedy) the first CTA that holds it: two barriers' worth.
+  // Largest key of the row, and the first CTA that holds it (behind a cluster barrier).
   auto row_max_of = [&](int& holder) {
     float largest = __int_as_float(0xFF800000);
     slice.each([&](float x, uint32_t, int) { largest = fmaxf(largest, x); });   // (which passes over NaN)
@@ -490,10 +494,14 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const uint32_t half = (e & 1) ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu;
-            if ((half & 0x7FFFu) < MAG_LOW) {
-              const uint32_t at = atomicAdd(&sh.list_n, 1u);
-              if (at < LIST) fine_room.noted[at] = half;
+            if ((half & 0x7FFFu) >= MAG_LOW) continue;
+            if ((half & 0x7FFFu) == 0) {   // a padded vocabulary has many
+              atomicAdd(&sh.zeros[half >> 15], 1u);
+              continue;
             }
+            if (*static_cast<volatile uint32_t*>(&sh.list_n) > LIST) continue;
+            const uint32_t at = atomicAdd(&sh.list_n, 1u);   // (more than LIST: no list, an irregular row)
+            if (at < LIST) fine_room.noted[at] = half;
           }
         }
 #pragma unroll
@@ -512,13 +520,14 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
       unsigned long long mid[2] = {0ull, 0ull};
       if (tid < min(sh.list_n, static_cast<uint32_t>(LIST))) {
         const uint32_t half = fine_room.noted[tid];
-        if (half == 0x8000u) {   // -0 is 0
-          atomicSub(middle + 1, 1u);
-          atomicAdd(middle, 1u);
-        }
         const unsigned long long w = weight_call(0x1p-10f, __uint_as_float(half << 16), slope, sh.table);
         mid[0] = half > 0x8000u ? 0ull : w;
         mid[1] = half > 0x8000u ? w : 0ull;
+      }
+      if (tid == 0 && sh.zeros[0] + sh.zeros[1] > 0) {
+        middle[1] -= sh.zeros[1];   // -0 is 0
+        middle[0] += sh.zeros[1];
+        mid[0] += (sh.zeros[0] + sh.zeros[1]) * weight_call(0x1p-10f, 0.f, slope, sh.table);
       }
       add_mid(sh, mid);
     }
@@ -547,8 +556,10 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
     if (!irregular) {
       bin_range(bin, row_max, same);
       const float best = value_of<false>(row_max);
-      irregular = !greedy && ((mids && bin < B_MID && (many || slope.hi > 739.f) && weight_call(best, 0x1p-10f, slope, sh.table) > 0) ||
-                  (lows && weight_call(best, -128.f, slope, sh.table) > 0));
+      // (middle: their list has run over, or 2^-10 / T > 1/2, so that weights relative to 2^-10 lose bits)
+      irregular = !greedy &&
+                  ((mids && bin < B_MID && (many || slope.hi > 739.f) && weight_call(best, 0x1p-10f, slope, sh.table) > 0) ||
+                   (lows && weight_call(best, -128.f, slope, sh.table) > 0));
     }
     if (irregular) {
       // Largest logits in a wide bin, weights that a wide bin's figures do not serve: these bins logit by logit.
@@ -601,8 +612,9 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
         if (ordinary) {
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
-            const auto parts = weight_parts(TwoFloats::all(best), TwoFloats::pair(-__uint_as_float(raw[e]), -__uint_as_float(raw[e + 1])),
-                                            TwoFloats::all(slope.hi), TwoFloats::all(slope.lo), TwoFloats());
+            const uint64_t minus = TwoFloats::pair(-__uint_as_float(raw[e]), -__uint_as_float(raw[e + 1]));
+            const auto parts =
+                weight_parts(TwoFloats::all(best), minus, TwoFloats::all(slope.hi), TwoFloats::all(slope.lo), TwoFloats());
             float y[2], t[2], l[2], tail[2];
             TwoFloats::split(parts.y, y[0], y[1]);
             TwoFloats::split(parts.t, t[0], t[1]);
@@ -624,10 +636,12 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
           const float x = __uint_as_float(raw[e]) + 0.f;   // (-0 is 0)
           if (!(x >= -3.402823466e+38f)) continue;
           // bin_of, from the magnitude
-          const int m = static_cast<int>(__float_as_uint(x) >> 16 & 0x7FFFu), sign = static_cast<int>(__float_as_uint(x)) >> 31;
-          const int b = B_MID - ((min(max(m, static_cast<int>(MAG_LOW) - 1), static_cast<int>(MAG_TOP)) - (static_cast<int>(MAG_LOW) - 1)) ^ sign);
+          const int m = static_cast<int>(__float_as_uint(x) >> 16 & 0x7FFFu);
+          const int sign = static_cast<int>(__float_as_uint(x)) >> 31;
+          constexpr int below = static_cast<int>(MAG_LOW) - 1;
+          const int b = B_MID - ((min(max(m, below), static_cast<int>(MAG_TOP)) - below) ^ sign);
           atomicAdd(room.count + b, 1u);
-          add_mass(lower + b, upper + b, w[e]);
+          if (w[e]) add_mass(lower + b, upper + b, w[e]);   // (a mask's many equal logits weigh nothing)
         }
       }
       cluster_sync_all();
@@ -770,7 +784,9 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
             const uint32_t part_of_target = fine ? (hi - static_cast<uint32_t>(target)) >> sh.cmd.shift
                                                  : static_cast<uint32_t>(bin_of(static_cast<uint32_t>(target) >> K::LOW));
             // (a middle bin's mass is that of its parts up to a rounding)
-            unsigned long long aim = how == BY_COUNT ? target - cb : how == BY_MASS ? min(target - mb, upto.mass[S_THREADS - 1]) : 0ull;
+            const unsigned long long aim = how == BY_COUNT  ? target - cb
+                                           : how == BY_MASS ? min(target - mb, upto.mass[S_THREADS - 1])
+                                                            : 0ull;
             int t = how == BY_KEY     ? static_cast<int>(part_of_target) / n
                     : how == BY_COUNT ? first_of([&](int i) { return upto.count[i] >= aim; })
                                       : first_of([&](int i) { return upto.mass[i] >= aim && upto.mass[i] > 0; });
@@ -824,8 +840,12 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
             if (single || c == 0 || hi < lo) {
               key = hi;
               const unsigned long long w = c == 1 ? m : weigh(key);   // (a call and a division less for most drawn tokens)
-              nth = c == 1 ? 1u : how == BY_KEY ? c : how == BY_COUNT ? static_cast<uint32_t>(target) - c0 : few_times(target - m0, w);
-              nth = max(1u, min(nth, c));
+              if (c > 1) {
+                nth = how == BY_KEY     ? c
+                      : how == BY_COUNT ? static_cast<uint32_t>(target) - c0
+                                        : few_times(target - m0, w);
+                nth = max(1u, min(nth, c));
+              }
               through = m0 + min(nth, c) * w;
               done = true;
             } else if (c <= LIST) {
@@ -929,7 +949,9 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
         if (tid < each) {
           const uint32_t n = cluster_sum(fine_room.fine_count + b, ctas);
           *in_cta(fine_room.part.count + b, 0) = n;
-          *in_cta(fine_room.part.mass + b, 0) = n == 0 ? 0ull : c.shift ? mass_sum(fine_room.fine_lower + b, fine_room.fine_upper + b, ctas) : n * weigh(c.hi - b);
+          *in_cta(fine_room.part.mass + b, 0) = n == 0    ? 0ull
+                                                : c.shift ? mass_sum(fine_room.fine_lower + b, fine_room.fine_upper + b, ctas)
+                                                          : n * weigh(c.hi - b);
         }
         cluster_sync_all();
         if (first_cta) {
@@ -966,7 +988,8 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
     if (!F32) {
       n_runs = 0;
       for (int r0 = 0; r0 < all_runs; r0 += S_THREADS) {
-        const bool may = r0 + tid < all_runs && room_most[(r0 + tid) / (4 * S_WARPS) * S_WARPS + (r0 + tid) % S_WARPS] >= (value == 0.f ? 0x7FFFu : sh.cmd.key);   // (-0 is one key lower)
+        const int r = r0 + tid, turn = r / (4 * S_WARPS) * S_WARPS + r % S_WARPS;
+        const bool may = r < all_runs && room_most[turn] >= (value == 0.f ? 0x7FFFu : sh.cmd.key);   // (-0 is one key lower)
         const unsigned any = __ballot_sync(0xffffffffu, may);
         if (lane == 0) sh.scan_count[warp] = __popc(any);
         __syncthreads();
@@ -1049,10 +1072,11 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
         }
         uint32_t c = before + upto - n;
         if (c < nth && nth <= c + n) {
+          constexpr uint32_t one = F32 ? 0xFFFFFFFFu : 0xFFFFu;
           int e_at = 0;
 #pragma unroll
           for (int e = 0; e < K::GROUP; ++e)
-            if ((Slice<F32>::bits(v, e) & (F32 ? zero : zero & 0xFFFFu)) == (F32 ? raw : raw & 0xFFFFu) && ++c == nth) e_at = e;
+            if ((Slice<F32>::bits(v, e) & zero & one) == (raw & one) && ++c == nth) e_at = e;
           a.ids[row] = group_at(lo + i * S_THREADS + tid) * K::GROUP - slice.shift + e_at;
         }
       }
@@ -1093,7 +1117,8 @@ int launch_sample_type(const SampleArgs& a, int64_t rows, cudaStream_t stream) {
   while (ctas < 16 && rows * ctas <= sm_count() && a.vocab > 4096 * ctas) ctas *= 2;
   if (ctas > 8)
     if (int rc = allow_wide_clusters(reinterpret_cast<const void*>(kernel), F32)) return rc;
-  return launch_ex(kernel, dim3(static_cast<unsigned>(rows * ctas)), dim3(S_THREADS), static_cast<int>(sizeof(Room<F32>)), ctas, true, stream, a, ctas);
+  return launch_ex(kernel, dim3(static_cast<unsigned>(rows * ctas)), dim3(S_THREADS), sizeof(Room<F32>), ctas, true, stream,
+                   a, ctas);
 }
 
 }  // namespace

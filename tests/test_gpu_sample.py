@@ -102,6 +102,9 @@ def special(kind, rows, vocab, dtype, seed):
         x[:, vocab // 2] = 0.02
     elif kind == "padded":          # a padded vocabulary's columns are zero
         x[:, vocab // 2:] = 0
+    elif kind == "padded with both zeros":
+        x[:, vocab // 3:] = torch.where(torch.rand(rows, vocab - vocab // 3, generator=g) < 0.5, 0.0, -0.0)
+        x[:, : vocab // 3] -= 6
     elif kind == "zeros and just below":   # many of both: the bin below zero is counted again, beside zeros that are not in it
         x = torch.where(torch.rand(x.shape, generator=g) < 0.4, 0.0, -x.abs() * 1e-5)
         x[:, ::7] = -0.0
@@ -139,7 +142,7 @@ def special(kind, rows, vocab, dtype, seed):
     return x.to(dtype)
 
 
-KINDS = ["equal", "zeros", "two values", "tiny", "tiny, one ahead", "padded", "zeros and just below", "zeros and around", "negative", "below the lowest bin", "above the highest bin", "both sides",
+KINDS = ["equal", "zeros", "two values", "tiny", "tiny, one ahead", "padded", "padded with both zeros", "zeros and just below", "zeros and around", "negative", "below the lowest bin", "above the highest bin", "both sides",
          "lowest value", "all lowest", "masked", "one left", "none left", "nan", "infinite", "infinite, one"]
 
 
