@@ -284,25 +284,32 @@ __global__ void __launch_bounds__(VPT > 1 ? 512 : 1024) norm_cta_kernel(const No
   const float st = OUT == OUT_NVFP4 ? *a.s_t : 1.0f;
   float most_all = 0.f;
   int turn = 0;
+  // (rows of more than 16384 elements: the loads of two or four vectors at a time, as registers allow; else the next
+  // row's loads are under way while this one is summed and stored)
+  constexpr int AT_ONCE = VPT < 8 ? VPT : RES == RES_F32 ? 2 : 4;
+  Raw<RES> raw[AT_ONCE];
+  auto load_row = [&](int row, int i0) {
+    const int token = row / a.heads, head = row - token * a.heads;
+    const uint16_t* xr = a.x + token * a.x_stride + static_cast<int64_t>(head) * a.K;
+    const int64_t base = static_cast<int64_t>(row) * a.K;
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int v = threadIdx.x + (i0 + i) * blockDim.x;
+      if (v < nvec) load_raw<RES>(xr + v * 8, a.residual, base + v * 8, raw[i]);
+    }
+  };
+  if (AT_ONCE == VPT && blockIdx.x < a.rows) load_row(blockIdx.x, 0);
   for (int row = blockIdx.x; row < a.rows_p; row += gridDim.x, turn ^= 1) {
     if (row >= a.rows) {   // padding rows of the block scales (whole CTAs)
       pad_scales(a, row, 0, threadIdx.x, blockDim.x);
       continue;
     }
     const int token = row / a.heads, head = row - token * a.heads;
-    const uint16_t* xr = a.x + token * a.x_stride + static_cast<int64_t>(head) * a.K;
     const int64_t base = static_cast<int64_t>(row) * a.K;
-    // (rows of more than 16384 elements: the loads of two or four vectors at a time, as registers allow)
-    constexpr int AT_ONCE = VPT < 8 ? VPT : RES == RES_F32 ? 2 : 4;
     float t[VPT][8], sum = 0.f, most = 0.f;
 #pragma unroll
     for (int i0 = 0; i0 < VPT; i0 += AT_ONCE) {
-      Raw<RES> raw[AT_ONCE];
-#pragma unroll
-      for (int i = i0; i < i0 + AT_ONCE; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v < nvec) load_raw<RES>(xr + v * 8, a.residual, base + v * 8, raw[i - i0]);
-      }
+      if (AT_ONCE < VPT) load_row(row, i0);
 #pragma unroll
       for (int i = i0; i < i0 + AT_ONCE; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
@@ -315,6 +322,7 @@ __global__ void __launch_bounds__(VPT > 1 ? 512 : 1024) norm_cta_kernel(const No
         }
       }
     }
+    if (AT_ONCE == VPT && row + gridDim.x < a.rows) load_row(row + gridDim.x, 0);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -469,8 +477,8 @@ constexpr int PARTIALS = 2048;   // CTAs of a statistics pass at most
 template <int OUT, int RES>
 int launch_rows(const NormArgs& a, int* grid, cudaStream_t stream) {
   const int nvec = a.K / 8;
-  const int most = OUT == OUT_STATS ? PARTIALS : 1 << 30;
   if (a.K <= 1024) {
+    const int most = OUT == OUT_STATS ? PARTIALS : 1 << 30;
     const int tpr = nvec <= 8 ? 8 : nvec <= 16 ? 16 : 32, vpt = static_cast<int>(ceil_div(nvec, tpr));
     // several rows at a time only where the CTAs fill the SMs all the same
     const bool many = vpt == 1 && a.rows_p >= static_cast<int64_t>(sm_count()) * 8 * (256 / tpr) * 4;
@@ -493,7 +501,10 @@ int launch_rows(const NormArgs& a, int* grid, cudaStream_t stream) {
   // for the statistics pass, whose CTAs take several rows
   const int vpt = nvec > 2048 ? 8 : nvec > 1024 ? 4 : a.rows >= sm_count() ? (OUT == OUT_STATS ? 4 : 2) : 1;
   const int threads = static_cast<int>(ceil_div(ceil_div(nvec, vpt), 32) * 32);
-  *grid = a.rows_p < most ? a.rows_p : most;
+  // two rows to a CTA where that leaves eight CTAs an SM to start with (8192 x 5120: 54.5 -> 52.0 us; 2048 x 16384, fp32
+  // stream: 67 -> 63.5); the statistics pass as many as four CTAs an SM take (4096 x 5120 with the rest: 66 -> 62.7)
+  const int sms = sm_count();
+  *grid = OUT == OUT_STATS ? (a.rows_p < 4 * sms ? a.rows_p : 4 * sms) : a.rows_p >= 8 * sms ? (a.rows_p + 1) / 2 : a.rows_p;
 #define NVFP4_CTA(V) return launch_ex(norm_cta_kernel<OUT, RES, V>, dim3(*grid), dim3(threads), 0, 1, true, stream, a)
   if (vpt == 1) NVFP4_CTA(1);
   if (vpt == 2) NVFP4_CTA(2);
