@@ -13,9 +13,10 @@
 // Bound by HBM for many rows, by latency (one load, one reduction, one store)
 // for few. One row stays in registers between its only read and its only
 // write; what is read once is loaded evict-first (2048 x 2048: 7.8 -> 7.1 us,
-// 2048 x 16384 with an fp32 stream 71 -> 69). Measured in graphs of calls on
-// changing inputs, bf16 stream and output: 1 x 5120 2.4 us, 512 x 5120 5.8,
-// 8192 x 5120 56 (6.0 TB/s); E4M3 output, fp32 stream, 8192 x 5120 72 (6.4 TB/s).
+// 2048 x 16384 with an fp32 stream 71 -> 69), and a CTA's next row while its last
+// one is summed and stored (7.1 -> 6.3, 69 -> 64). Measured in graphs of calls on
+// changing inputs, bf16 stream and output: 1 x 5120 2.4 us, 512 x 5120 5.7,
+// 8192 x 5120 52 (6.4 TB/s); E4M3 output, fp32 stream, 8192 x 5120 70.5 (6.5 TB/s).
 // Rows of up to 1024 elements (heads of 64 or 128 among them) belong to 8, 16 or
 // 32 lanes of a warp and need no block-wide step; longer rows to a CTA.
 #include "common.cuh"
@@ -367,7 +368,8 @@ __global__ void __launch_bounds__(VPT > 1 ? 512 : 1024) norm_cta_kernel(const No
 // ---- the codes of a tensor whose scale had to be found first: y = s * (w + offset) * r is formed again
 // from the stream (or x) and each row's r, so both passes see the same y. A lane takes a block of 16, a warp 32
 // blocks of a row at a time, two such chunks in flight; the block step's constants come from tables, as in
-// the quantiser (4096 x 5120 from DRAM: rows of a CTA, halves of blocks and formed reciprocals 33.8 us; this 23.5).
+// the quantiser (4096 x 5120 from DRAM: rows of a CTA, halves of blocks and formed reciprocals 33.8 us; blocks 23.5; with
+// the gain in registers 20.9).
 template <bool F32>
 struct RawBlock {
   uint4 w[F32 ? 4 : 2];
@@ -398,8 +400,10 @@ NVFP4_DEV void unpack_block(const RawBlock<F32>& r, float (&v)[16]) {
   }
 }
 
+constexpr int encode_ctas(bool f32) { return f32 ? 3 : 4; }   // of an SM
+
 template <bool F32>
-__global__ void __launch_bounds__(256) norm_encode_kernel(const NormArgs a, const void* s, int64_t s_stride, int n_partial,
+__global__ void __launch_bounds__(256, encode_ctas(F32)) norm_encode_kernel(const NormArgs a, const void* s, int64_t s_stride, int n_partial,
                                                           float* s_t) {
   __shared__ unsigned int s_most;
   __shared__ QuantTables tab;
@@ -437,6 +441,18 @@ __global__ void __launch_bounds__(256) norm_encode_kernel(const NormArgs a, cons
   const TensorScale ts = tensor_scale(amax > 0.f ? __fdiv_rn(amax, 2688.0f) : 1.0f);
   if (blockIdx.x == 0 && threadIdx.x == 0) *s_t = ts.st;
   quant_tables_init(tab, ts.st);
+  // a warp's chunks all lie in the same columns (the grid's step is whole rows): their gain stays in registers
+  uint64_t gain[8];
+  {
+    float g[16];
+    if (a.weight && at.block < bpr) {
+      RawBlock<false> w;
+      load_block<false>(a.weight, at.block * 16, w);
+      unpack_block<false>(w, g);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) gain[e / 2] = a.weight ? f32_pair(g[e] + a.offset, g[e + 1] + a.offset) : f32_pair(1.f, 1.f);
+  }
   __syncthreads();
   for (; chunk < chunks; chunk += step) {
     At then = {0, bpr};
@@ -444,18 +460,13 @@ __global__ void __launch_bounds__(256) norm_encode_kernel(const NormArgs a, cons
     if (at.block < bpr) {
       float t[16], most = 0.f;
       unpack_block<F32>(raw, t);
-      if (a.weight) {
-        RawBlock<false> w;
-        load_block<false>(a.weight, at.block * 16, w);
-        float g[16];
-        unpack_block<false>(w, g);
+      const uint64_t rr = f32_pair(r, r);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) t[e] *= g[e] + a.offset;
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        t[e] *= r;
-        most = fmaxf(most, fabsf(t[e]));
+      for (int e = 0; e < 16; e += 2) {
+        const uint64_t y = mul_f32x2(mul_f32x2(f32_pair(t[e], t[e + 1]), gain[e / 2]), rr);
+        t[e] = __uint_as_float(static_cast<uint32_t>(y));
+        t[e + 1] = __uint_as_float(static_cast<uint32_t>(y >> 32));
+        most = fmaxf(most, fmaxf(fabsf(t[e]), fabsf(t[e + 1])));
       }
       uint2 codes;
       const uint32_t sc = quant_block16_tab(t, most, ts.d, ts.rdh, ts.rdl, tab, codes);
@@ -497,8 +508,8 @@ int launch_rows(const NormArgs& a, int* grid, cudaStream_t stream) {
 #undef NVFP4_LANES
   }
   // fewer rows than SMs: as many threads as a row has vectors of eight (32 x 5120: 2.5 us; two vectors a thread
-  // 2.6, four 3.0); more: two a thread (512 x 5120: 5.8 us; one 8.5, four 6.9; 8192 x 5120: 55; 108; 57), and four
-  // for the statistics pass, whose CTAs take several rows
+  // 2.6, four 3.0); more: two a thread (512 x 5120: 5.8 us; one 8.5, four 6.9; 8192 x 5120, a row for a CTA: 55; 108;
+  // 57), and four for the statistics pass, whose CTAs take several rows
   const int vpt = nvec > 2048 ? 8 : nvec > 1024 ? 4 : a.rows >= sm_count() ? (OUT == OUT_STATS ? 4 : 2) : 1;
   const int threads = static_cast<int>(ceil_div(ceil_div(nvec, vpt), 32) * 32);
   // two rows to a CTA where that leaves eight CTAs an SM to start with (8192 x 5120: 54.5 -> 52.0 us; 2048 x 16384, fp32
@@ -583,8 +594,14 @@ int launch_rms_norm_quantize(const nvfp4_norm_t& n, uint8_t* codes, uint8_t* sca
   const int res = res_of(n);
   const void* s = res == RES_NONE ? n.x : n.residual_out;
   const int64_t s_stride = res == RES_NONE ? n.x_stride : static_cast<int64_t>(n.heads) * n.K;
-  const int64_t chunks = static_cast<int64_t>(rows_p) * ceil_div(n.K / 16, 32);
-  const int ctas = static_cast<int>(chunks < 8 ? 1 : chunks < 8ll * 4 * sm_count() ? ceil_div(chunks, 8) : 4 * sm_count());
+  const int cpr = static_cast<int>(ceil_div(n.K / 16, 32));   // a row's chunks of 32 blocks, one for a warp
+  const int64_t chunks = static_cast<int64_t>(rows_p) * cpr;
+  const int most = encode_ctas(res_of(n) == RES_F32) * sm_count();
+  int ctas = static_cast<int>(chunks < 8 ? 1 : chunks < 8ll * most ? ceil_div(chunks, 8) : most);
+  // where a warp takes several chunks, its step is whole rows (cpr is 64 at most)
+  int unit = cpr;
+  for (int i = 0; i < 3 && unit % 2 == 0; ++i) unit /= 2;
+  if (chunks > 8ll * ctas) ctas -= ctas % unit;
   return res == RES_F32
              ? launch_ex(norm_encode_kernel<true>, dim3(ctas), dim3(256), 0, 1, true, stream, a, s, s_stride, grid, s_t)
              : launch_ex(norm_encode_kernel<false>, dim3(ctas), dim3(256), 0, 1, true, stream, a, s, s_stride, grid, s_t);
