@@ -132,6 +132,18 @@ NVFP4_DEV float amax8(const float (&t)[8]) {
   return m;
 }
 
+// The gain of eight columns, and t from it.
+NVFP4_DEV void gain_of(const uint16_t* weight, float offset, int k, float (&g)[8]) {
+  if (weight) {
+    unpack8(__ldg(reinterpret_cast<const uint4*>(weight + k)), g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] += offset;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = 1.f;
+  }
+}
+
 // Codes and block scale of eight elements of a block whose other eight are in
 // the neighbouring lane (lanes 2j, 2j + 1; both run this): the decisions of
 // the quantiser on y.
@@ -205,6 +217,14 @@ __global__ void __launch_bounds__(256) norm_lanes_kernel(const NormArgs a) {
   const int nvec = a.K >> 3;
   const float st = OUT == OUT_NVFP4 ? *a.s_t : 1.0f;
   float most_all = 0.f;
+  // a lane's columns are the same in every row: their gain stays in registers where a lane has few (15.9 -> 15.1)
+  constexpr bool KEPT = VPT <= 2;
+  float gain[KEPT ? VPT : 1][8];
+  if (KEPT) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (lane + i * TPR < nvec) gain_of(a.weight, a.offset, (lane + i * TPR) * 8, gain[KEPT ? i : 0]);
+  }
   // (all lanes of a warp walk the same number of rows: the reductions are warp-wide)
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * (per_cta * ROWS); row0 < a.rows_p; row0 += static_cast<int64_t>(gridDim.x) * (per_cta * ROWS)) {
     Raw<RES> raw[ROWS][VPT];
@@ -236,7 +256,12 @@ __global__ void __launch_bounds__(256) norm_lanes_kernel(const NormArgs a) {
           stream8<RES>(raw[j][i], a.residual_out, base + v * 8, t[i]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) sum = fmaf(t[i][e], t[i][e], sum);
-          gain8(a.weight, a.offset, v * 8, t[i]);
+          if (KEPT) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[i][e] *= gain[KEPT ? i : 0][e];
+          } else {
+            gain8(a.weight, a.offset, v * 8, t[i]);
+          }
           if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, amax8(t[i]));
         }
       }
