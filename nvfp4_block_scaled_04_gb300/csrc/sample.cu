@@ -1096,29 +1096,44 @@ __global__ void accept_kernel(const int32_t* tokens, const int32_t* drafts, int6
   accepted[b] = n;
 }
 
-// Clusters of 16 CTAs have to be allowed for a kernel, once on each device.
-int allow_wide_clusters(const void* kernel, int which) {
-  static std::atomic<unsigned long long> done[2];
+// Whether clusters of 16 CTAs of a kernel find a place: they have to be allowed, and the device has to have the SMs
+// together. Asked once on each device.
+bool wide_clusters(const void* kernel, int smem, int which) {
+  static std::atomic<unsigned long long> asked[2], found[2];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (done[which].load() & bit) return NVFP4_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return NVFP4_ERR_CUDA;
-  done[which].fetch_or(bit);
-  return NVFP4_OK;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+  const unsigned long long bit = 1ull << dev;
+  if (!(asked[which].load() & bit)) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 16;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(S_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+    if (ok) found[which].fetch_or(bit);
+    else cudaGetLastError();   // (an answer, not an error of the call)
+    asked[which].fetch_or(bit);
+  }
+  return found[which].load() & bit;
 }
 
 template <bool F32>
 int launch_sample_type(const SampleArgs& a, int64_t rows, cudaStream_t stream) {
   const auto kernel = sample_kernel<F32>;
-  if (int rc = ensure_smem(kernel, static_cast<int>(sizeof(Room<F32>)))) return rc;
+  constexpr int smem = static_cast<int>(sizeof(Room<F32>));
+  if (int rc = ensure_smem(kernel, smem)) return rc;
   // as many CTAs for a row as the rows leave room for, none with less than 4096 logits
   int ctas = 1;
   while (ctas < 16 && rows * ctas <= sm_count() && a.vocab > 4096 * ctas) ctas *= 2;
-  if (ctas > 8)
-    if (int rc = allow_wide_clusters(reinterpret_cast<const void*>(kernel), F32)) return rc;
-  return launch_ex(kernel, dim3(static_cast<unsigned>(rows * ctas)), dim3(S_THREADS), sizeof(Room<F32>), ctas, true, stream,
-                   a, ctas);
+  if (ctas > 8 && !wide_clusters(reinterpret_cast<const void*>(kernel), smem, F32)) ctas = 8;
+  return launch_ex(kernel, dim3(static_cast<unsigned>(rows * ctas)), dim3(S_THREADS), smem, ctas, true, stream, a, ctas);
 }
 
 }  // namespace

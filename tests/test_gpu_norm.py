@@ -146,11 +146,13 @@ def test_nvfp4_is_the_quantiser_s(nv, rows, K, given):
     assert (unpack_mma_scales(q.scales.cpu().numpy(), rows, K) != want.scales).mean() < 2e-3
 
 
-@pytest.mark.parametrize("tokens,heads,others,K", [(1, 40, 16, 128), (7, 8, 4, 64), (300, 5, 2, 128), (3, 2, 1, 1032), (2, 3, 0, 8)])
-@pytest.mark.parametrize("form", ["bf16", "e4m3", "nvfp4"])
+HEADS = [(1, 40, 16, 128), (7, 8, 4, 64), (300, 5, 2, 128), (3, 2, 1, 1040), (2, 3, 0, 16)]
+
+
+@pytest.mark.parametrize("tokens,heads,others,K,form", [(*h, f) for h in HEADS for f in ("bf16", "e4m3", "nvfp4")] +
+                         [(3, 2, 1, 1032, "bf16"), (3, 2, 1, 1032, "e4m3"), (2, 3, 0, 8, "bf16"), (2, 3, 0, 8, "e4m3"), (2500, 40, 3, 64, "bf16"),
+                          (2500, 40, 3, 128, "e4m3"), (1300, 40, 0, 256, "nvfp4")])
 def test_heads_of_a_fused_projection(nv, tokens, heads, others, K, form):
-    if form == "nvfp4" and K % 16:
-        pytest.skip("blocks of 16")
     g = torch.Generator().manual_seed(K)
     qkv = torch.randn(tokens, heads + others, K, generator=g).bfloat16()
     w = torch.randn(K, generator=g).bfloat16()

@@ -67,6 +67,20 @@ def test_largest_vocabulary(nv, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kw", [{}, dict(k=300, p=0.9), dict(t=0.0), dict(m=1e-4)])
+def test_largest_vocabulary_in_one_cta(nv, dtype, kw):
+    """More rows than SMs: a CTA walks the whole row (all rows are one row of memory)."""
+    rows = 200
+    x, u = logits(1, 524288, dtype, 13), uniform(rows, 13)
+    t, k, p, m = kw.get("t", 1.0), kw.get("k", 0), kw.get("p", 1.0), kw.get("m", 0.0)
+    ids, probs = nv.sample(x.cuda().expand(rows, -1), u.cuda(), t, k, p, m)
+    f = lambda v: float(torch.tensor(v))   # (settings are fp32)
+    for r in range(0, rows, 29):
+        i, q = draw(x[0].double().numpy(), float(u[r]), f(t), k, f(p), f(m))
+        assert int(ids[r]) == i and abs(float(probs[r]) - q) <= q * 2.0 ** -22
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_rows_with_settings_of_their_own(nv, dtype):
     rows, vocab = 90, 5000
     g = torch.Generator().manual_seed(1)
