@@ -510,8 +510,9 @@ typedef struct nvfp4_norm {
 int nvfp4_rms_norm(nvfp4_norm_t in, void* Y, int64_t y_stride, nvfp4_stream_t stream);
 
 /* y as E4M3 with one scale for each row, for linears kept in 8 bits:
- *   scales[row] = max|y| / 448 (1 for a row of zeros, else 2^-120 at least), codes = y / scales[row]
- * rounded to nearest even. A NaN of y is the code 0x7F.
+ *   scales[row] = max|y| / 448 (1 for a row of zeros, else 2^-120 at least)
+ *   codes       = the quotients y / scales[row] in fp32, rounded to nearest even
+ * A NaN of y is the code 0x7F.
  *   codes   device out uint8 [tokens][heads][K], 16-byte aligned
  *   scales  device out fp32 [tokens * heads] */
 int nvfp4_rms_norm_e4m3(nvfp4_norm_t in, uint8_t* codes, float* scales, nvfp4_stream_t stream);

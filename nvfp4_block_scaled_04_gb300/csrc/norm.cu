@@ -167,17 +167,23 @@ NVFP4_DEV uint32_t quant8(const float (&y)[8], const TensorScale& ts, uint32_t& 
   return e2m1x8(y, __fmul_rn(e4m3_to_f32(scale), ts.st));
 }
 
+// The E4M3 scale a of a row. Codes come from y * lift, den = a * lift and 1 / den.
+struct RowScale {
+  float a, lift, den, inv;
+};
+
 // Writes eight elements of y = t * r (k: their first column).
 template <int OUT>
-NVFP4_DEV void store8(const NormArgs& a, int row, int64_t y_at, int k, float (&t)[8], float r, float inv, const TensorScale* ts) {
+NVFP4_DEV void store8(const NormArgs& a, int row, int64_t y_at, int k, float (&t)[8], float r, const RowScale& rs, const TensorScale* ts) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) t[e] *= r;
   if (OUT == OUT_BF16) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + y_at + k) = pack8(t);
   if (OUT == OUT_E4M3) {
-    uint2 c;
-    c.x = f32x2_to_e4m3x2(t[0] * inv, t[1] * inv) | f32x2_to_e4m3x2(t[2] * inv, t[3] * inv) << 16;
-    c.y = f32x2_to_e4m3x2(t[4] * inv, t[5] * inv) | f32x2_to_e4m3x2(t[6] * inv, t[7] * inv) << 16;
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + static_cast<int64_t>(row) * a.K + k) = c;
+    if (rs.lift != 1.0f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] *= rs.lift;
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + static_cast<int64_t>(row) * a.K + k) = e4m3x8(t, rs.den, rs.inv);
   }
   if (OUT == OUT_NVFP4) {
     uint32_t sc;
@@ -196,12 +202,18 @@ NVFP4_DEV void pad_scales(const NormArgs& a, int row, int first, int lane, int l
   for (int c = first + lane; c < a.cols4; c += lanes) p[static_cast<int64_t>(c >> 2) * 512 + (c & 3)] = 0;
 }
 
-// The row's E4M3 scale a = max|y| / 448 (1 for a row of zeros; 2^-120 at least, so that 1 / a is finite) and what y
-// is multiplied with.
-NVFP4_DEV float e4m3_row_scale(float most, float& inv) {
-  const float a = most > 0.f ? fmaxf(__fdiv_rn(most, 448.0f), 0x1p-120f) : 1.0f;
-  inv = __fdiv_rn(1.0f, a);
-  return a;
+// The row's E4M3 scale a = max|y| / 448 (1 for a row of zeros; 2^-120 at least, so that 1 / a is finite). Codes are those
+// of the quotients y / a: a product with 1 / a alone gives a neighbour's where a quotient is next to a border
+// between two, and rows of few different values (a bf16 stream without a gain) have many quotients exactly on one.
+// Rows of small values are lifted by a power of two, so that the quotient's remainder has its bits above 2^-149.
+NVFP4_DEV RowScale e4m3_row_scale(float most) {
+  RowScale rs;
+  rs.a = most > 0.f ? fmaxf(__fdiv_rn(most, 448.0f), 0x1p-120f) : 1.0f;
+  rs.lift = rs.a < 0x1p-60f ? 0x1p64f : 1.0f;
+  rs.den = rs.a * rs.lift;
+  rs.inv = __frcp_rn(rs.den);
+  if (rs.inv == 0.f) rs.den = 0.f;   // (an infinite scale: finite values are 0 beside it)
+  return rs;
 }
 
 NVFP4_DEV float rms_r(float sum, const NormArgs& a) { return rsqrtf(sum / static_cast<float>(a.K) + a.eps); }
@@ -271,10 +283,10 @@ __global__ void __launch_bounds__(256) norm_lanes_kernel(const NormArgs a) {
         if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
       }
       const float r = rms_r(sum, a);
-      float inv = 0.f;
+      RowScale rs = {};
       if (OUT == OUT_E4M3) {
-        const float scale = e4m3_row_scale(most * r, inv);
-        if (live[j] && lane == 0) static_cast<float*>(a.scales)[row] = scale;
+        rs = e4m3_row_scale(most * r);
+        if (live[j] && lane == 0) static_cast<float*>(a.scales)[row] = rs.a;
       }
       if (OUT == OUT_STATS) {
         if (live[j] && lane == 0) a.row_r[row] = r;
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(256) norm_lanes_kernel(const NormArgs a) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = lane + i * TPR;
-        if (live[j] && v < nvec) store8<OUT>(a, row, y_at[j], v * 8, t[i], r, inv, &ts);
+        if (live[j] && v < nvec) store8<OUT>(a, row, y_at[j], v * 8, t[i], r, rs, &ts);
       }
       if (OUT == OUT_NVFP4 && a.mma && row < a.rows_p) pad_scales(a, row, live[j] ? a.K >> 4 : 0, lane, TPR);
     }
@@ -369,10 +381,10 @@ __global__ void __launch_bounds__(VPT > 1 ? 512 : 1024) norm_cta_kernel(const No
       if (OUT == OUT_E4M3 || OUT == OUT_STATS) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     }
     const float r = rms_r(sum, a);
-    float inv = 0.f;
+    RowScale rs = {};
     if (OUT == OUT_E4M3) {
-      const float scale = e4m3_row_scale(most * r, inv);
-      if (threadIdx.x == 0) static_cast<float*>(a.scales)[row] = scale;
+      rs = e4m3_row_scale(most * r);
+      if (threadIdx.x == 0) static_cast<float*>(a.scales)[row] = rs.a;
     }
     if (OUT == OUT_STATS) {
       if (threadIdx.x == 0) a.row_r[row] = r;
@@ -383,7 +395,7 @@ __global__ void __launch_bounds__(VPT > 1 ? 512 : 1024) norm_cta_kernel(const No
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      if (v < nvec) store8<OUT>(a, row, y_at, v * 8, t[i], r, inv, &ts);
+      if (v < nvec) store8<OUT>(a, row, y_at, v * 8, t[i], r, rs, &ts);
     }
     if (OUT == OUT_NVFP4 && a.mma) pad_scales(a, row, a.K >> 4, threadIdx.x, blockDim.x);
   }

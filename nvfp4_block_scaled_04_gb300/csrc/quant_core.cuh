@@ -20,6 +20,11 @@ NVFP4_DEV uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+NVFP4_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 NVFP4_DEV uint64_t f32_pair(float lo, float hi) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
@@ -114,6 +119,23 @@ NVFP4_DEV uint32_t e2m1x8(const float (&v)[8], float den) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(v[j], den);
   return f32x8_to_e2m1x8(q);
+}
+
+// The eight E4M3 codes of the fp32 quotients x / den (inv = RN(1 / den); a NaN: 0x7F). q = RN(x inv) is within two units
+// of the quotient, e = x - q den has no more than a rounding of itself, so q + e inv, rounded, is the nearest fp32
+// number unless the quotient lies within 3 * 2^-24 of a unit from the middle between two. Codes could differ only where
+// one of these two is a border between codes: a finite number of pairs (x, den), and on all of them it is the nearest
+// (a test walks them). No branch: a division for the few next to a border made a row wait for code that no other row had
+// fetched (2048 x 2048, bf16 stream: brackets and divisions 8.15 us, this 7.3, without the step 7.0).
+NVFP4_DEV uint2 e4m3x8(const float (&v)[8], float den, float inv) {
+  const uint64_t I = f32_pair(inv, inv), D = f32_pair(-den, -den);
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint64_t x = f32_pair(v[2 * e], v[2 * e + 1]), q0 = mul_f32x2(x, I), q = fma_f32x2(fma_f32x2(q0, D, x), I, q0);
+    c[e] = f32x2_to_e4m3x2(__uint_as_float(static_cast<uint32_t>(q)), __uint_as_float(static_cast<uint32_t>(q >> 32)));
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
 // E4M3 code of fl(ab / d) (ab >= 0): RN(ab rdl) <= fl(ab / d) <= RN(ab rdh)
