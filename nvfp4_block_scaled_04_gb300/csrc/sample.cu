@@ -151,7 +151,7 @@ enum { BY_COUNT = 0, BY_MASS = 1, BY_KEY = 2 };
 struct Shared {
   uint4 edge[2];
   unsigned long long table[64];
-  unsigned long long wide_mass[4];   // bf16: masses of the wide bins (the middle ones' relative to 2^-10 in regular rows)
+  uint32_t wide_lower[4], wide_upper[4];   // bf16: masses of the wide bins, of the row, in the first CTA
   unsigned long long scan_mass[S_WARPS];
   uint32_t scan_count[S_WARPS];
   Command cmd;
@@ -315,15 +315,12 @@ NVFP4_DEV void add_mass(uint32_t* lower, uint32_t* upper, unsigned long long w) 
   if (hi) atomicAdd(upper, hi);
 }
 
-// Adds each thread's two masses to the CTA's of the middle bins.
-NVFP4_DEV void add_mid(Shared& sh, unsigned long long (&mid)[2]) {
+// Adds each thread's mass to the row's of a wide bin (whole warps).
+NVFP4_DEV void add_wide(Shared& sh, int wide, unsigned long long m) {
+  if (!__any_sync(0xffffffffu, m != 0)) return;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (!__any_sync(0xffffffffu, mid[i] != 0)) continue;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mid[i] += __shfl_xor_sync(0xffffffffu, mid[i], o);
-    if ((threadIdx.x & 31) == 0) atomicAdd(&sh.wide_mass[1 + i], mid[i]);
-  }
+  for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+  if ((threadIdx.x & 31) == 0) add_mass(in_cta(&sh.wide_lower[wide], 0), in_cta(&sh.wide_upper[wide], 0), m);
 }
 
 // The sum over this and all earlier threads of the CTA (every thread calls it; ends behind a barrier).
@@ -399,7 +396,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
   const bool first_cta = rank == 0;
 
   if (tid < 64) sh.table[tid] = EXP2_TABLE[tid];
-  if (tid < 4) sh.wide_mass[tid] = 0;
+  if (tid < 4) sh.wide_lower[tid] = sh.wide_upper[tid] = 0;
   if (tid == 0) sh.max_key = 0, sh.min_bin = NB, sh.list_n = 0, sh.zeros[0] = sh.zeros[1] = 0;
   for (int b = tid; b < NB; b += S_THREADS) {
     room.count[b] = 0;
@@ -453,7 +450,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
   };
 
   uint32_t row_max;
-  bool irregular = false;
+  bool irregular = false, mids = false;
   // (the temperature is looked at behind the pass over the logits: its load takes as long as theirs)
   bool greedy;
   Slope slope;
@@ -469,7 +466,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
     __syncthreads();
   } else {
     // Counts. Two logits of a word at a time: clamped magnitudes give the bins. Logits of magnitudes below 2^-10
-    // are noted: what lies in the middle bins is weighed afterwards, relative to 2^-10.
+    // are noted: what lies in the middle bins is weighed afterwards, one by one.
     uint32_t* const middle = room.count + B_MID;
 #pragma unroll 1
     for (int g = slice.g0 + tid, turn = 0; g - lane < slice.g1; g += 4 * S_THREADS, ++turn) {   // (a warp's turns together)
@@ -516,22 +513,13 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
     }
     look_at_temperature();
     __syncthreads();
-    {
-      unsigned long long mid[2] = {0ull, 0ull};
-      if (tid < min(sh.list_n, static_cast<uint32_t>(LIST))) {
-        const uint32_t half = fine_room.noted[tid];
-        const unsigned long long w = weight_call(0x1p-10f, __uint_as_float(half << 16), slope, sh.table);
-        mid[0] = half > 0x8000u ? 0ull : w;
-        mid[1] = half > 0x8000u ? w : 0ull;
-      }
-      if (tid == 0 && sh.zeros[0] + sh.zeros[1] > 0) {
-        middle[1] -= sh.zeros[1];   // -0 is 0
+    if (sh.zeros[1] > 0) {   // -0 is 0
+      if (tid == 0) {
+        middle[1] -= sh.zeros[1];
         middle[0] += sh.zeros[1];
-        mid[0] += (sh.zeros[0] + sh.zeros[1]) * weight_call(0x1p-10f, 0.f, slope, sh.table);
       }
-      add_mid(sh, mid);
+      __syncthreads();
     }
-    __syncthreads();
     // the first bin that is not empty: the largest logit, where it is a bin of one value
     int bin = NB;
 #pragma unroll
@@ -549,28 +537,25 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
     const uint32_t low_any = lane < ctas ? *in_cta(room.count + B_LAST, lane) : 0u;
     bin = __reduce_min_sync(0xffffffffu, my_bin);
     int holder = __ffs(__ballot_sync(0xffffffffu, my_bin == bin)) - 1;   // (greedy: the first CTA that has it)
-    const bool mids = __any_sync(0xffffffffu, mid_any != 0), lows = __any_sync(0xffffffffu, low_any != 0);
+    const bool lows = __any_sync(0xffffffffu, low_any != 0);
+    mids = __any_sync(0xffffffffu, mid_any != 0) && bin < B_MID;
     uint32_t same;
     row_max = 0;
     irregular = bin == NB || wide_bin(bin) >= 0;
     if (!irregular) {
       bin_range(bin, row_max, same);
       const float best = value_of<false>(row_max);
-      // (middle: their list has run over, or 2^-10 / T > 1/2, so that weights relative to 2^-10 lose bits)
-      irregular = !greedy &&
-                  ((mids && bin < B_MID && (many || slope.hi > 739.f) && weight_call(best, 0x1p-10f, slope, sh.table) > 0) ||
-                   (lows && weight_call(best, -128.f, slope, sh.table) > 0));
+      // (middle: their list has run over)
+      irregular = !greedy && ((mids && many && weight_call(best, 0x1p-10f, slope, sh.table) > 0) ||
+                              (lows && weight_call(best, -128.f, slope, sh.table) > 0));
     }
     if (irregular) {
       // Largest logits in a wide bin, weights that a wide bin's figures do not serve: these bins logit by logit.
       row_max = row_max_of(holder);
-      if (tid < 4) {
-        sh.wide_mass[tid] = 0;
-        room.count[tid == 0 ? 0 : tid == 3 ? B_LAST : B_MID + tid - 1] = 0;
-      }
+      if (tid < 4) room.count[tid == 0 ? 0 : tid == 3 ? B_LAST : B_MID + tid - 1] = 0;
       __syncthreads();
       const float best = value_of<false>(row_max);
-      unsigned long long mid[2] = {0ull, 0ull}, ends[2] = {0ull, 0ull};
+      unsigned long long masses[4] = {0ull, 0ull, 0ull, 0ull};
       uint32_t last = 0;   // (runs of one value are common: a mask, a padded vocabulary)
       unsigned long long last_w = 0;
       slice.each([&](float, uint32_t bits, int) {
@@ -579,16 +564,11 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
         if (n < 0) return;
         atomicAdd(room.count + b, 1u);
         if (k != last) last = k, last_w = weight_call(best, value_of<false>(k), slope, sh.table);
-        if (n == 1 || n == 2) mid[n - 1] += last_w;
-        else ends[n == 3] += last_w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) masses[i] += n == i ? last_w : 0ull;
       });
-      add_mid(sh, mid);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ends[i] += __shfl_xor_sync(0xffffffffu, ends[i], o);
-        if (lane == 0 && ends[i]) atomicAdd(&sh.wide_mass[3 * i], ends[i]);
-      }
+      for (int i = 0; i < 4; ++i) add_wide(sh, i, masses[i]);
       cluster_sync_all();
     }
     if (tid == 0) sh.cmd = {CMD_FIND, 0u, 0u, 0, row_max, 1u, holder};
@@ -659,18 +639,24 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
           uint32_t h, same;
           bin_range(b, h, same);
           m = c * weight(best, value_of<false>(h), slope, sh.table);
-        } else if (irregular) {
-          m = cluster_sum(&sh.wide_mass[wide], ctas);
-        } else if (wide == 3) {
+        } else if (wide == 3 && !irregular) {
           c = 0;   // nothing in it weighs anything (and -inf and NaN were counted too)
-        } else {   // a middle bin, relative to 2^-10 so far
-          m = cluster_sum(&sh.wide_mass[wide], ctas);
-          const unsigned long long w = weight_call(best, 0x1p-10f, slope, sh.table);
-          m = __umul64hi(m, w) << (64 - W_BITS) | (m * w) >> W_BITS;
         }
       }
       *in_cta(room.merged + b, 0) = c;
       *in_cta(room.merged_mass + b, 0) = m;
+    }
+    if (!F32 && mids && !irregular) {   // the middle bins' masses are those of their tokens, as lists and finer counts have them
+      uint32_t half = 0;
+      unsigned long long w = 0;
+      if (tid < min(sh.list_n, static_cast<uint32_t>(LIST))) {
+        half = fine_room.noted[tid];
+        w = weigh(key_of<false>(half));
+      }
+      add_wide(sh, 2, half > 0x8000u ? w : 0ull);
+      if (half > 0x8000u) w = 0;
+      if (tid == 0 && sh.zeros[0] + sh.zeros[1] > 0) w += (sh.zeros[0] + sh.zeros[1]) * weigh(key_of<false>(0u));
+      add_wide(sh, 1, w);
     }
     cluster_sync_all();
 
@@ -681,6 +667,8 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
       for (int i = 0; i < PER; ++i) {
         const int b = tid * PER + i;
         if (b < NB) {
+          const int wide = F32 ? -1 : wide_bin(b);
+          if (wide >= 0) room.merged_mass[b] = static_cast<unsigned long long>(sh.wide_upper[wide]) << 32 | sh.wide_lower[wide];
           c += room.merged[b];
           m += room.merged_mass[b];
         }
@@ -783,7 +771,6 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
             unsigned long long mb = fine ? m0 : 0ull;
             const uint32_t part_of_target = fine ? (hi - static_cast<uint32_t>(target)) >> sh.cmd.shift
                                                  : static_cast<uint32_t>(bin_of(static_cast<uint32_t>(target) >> K::LOW));
-            // (a middle bin's mass is that of its parts up to a rounding)
             const unsigned long long aim = how == BY_COUNT  ? target - cb
                                            : how == BY_MASS ? min(target - mb, upto.mass[S_THREADS - 1])
                                                             : 0ull;
