@@ -560,15 +560,18 @@ typedef struct nvfp4_sampling {
  * exceeds u times the mass of what is kept, u = uniform[row]:
  *   out_ids[row]   = its index (-1 if the row has no token)
  *   out_probs[row] = w / (mass kept)   (0 if the row has none; NULL: not wanted)
- * Weights are held to 2^-35 of themselves (none below 2^-46) and added exactly:
- * the token is that of the formulas in real numbers unless u or top_p lies
- * within about 2^-35 of a border between two tokens. The same inputs give the
- * same tokens.
+ * A weight is held as a multiple of 2^-44, off by at most 2^-35 of itself and
+ * 2^-45 (one below 2^-45 counts as 0, and its token is not drawn), and weights
+ * are added exactly. So the token is that of the formulas in real numbers unless
+ * u or top_p lies within 2^-34 + vocab * 2^-45 of a border between two tokens
+ * (vocab = 248,320: 2^-27, near one step of u; the second term is of a row whose
+ * first token has most of the mass, and falls with that share), or a weight
+ * within 2^-35 of itself and 2^-45 of min_p. The same inputs give the same tokens.
  *   logits   device, bf16 or fp32 (dtype), row r at r * stride elements,
  *            aligned to its type; any vocab of 1 .. 524288; stride >= vocab, or 0:
  *            every row draws from the same logits
  *   uniform  device fp32 [rows], in [0, 1); below 0 and NaN as 0, 1 and more:
- *            the last token kept
+ *            the last token kept that has a weight
  *   rows     <= 2^20 */
 int nvfp4_sample(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, nvfp4_sampling_t settings,
                  const float* uniform, int32_t* out_ids, float* out_probs, nvfp4_stream_t stream);

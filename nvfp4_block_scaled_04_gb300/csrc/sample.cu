@@ -16,8 +16,10 @@
 // whose largest key is smaller are not read again for it.
 //
 // Exactness. The token has to be the one that the definition names, so masses are 64-bit integers: a weight is
-// round(2^44 w) with a relative error below 2^-35 (sample_math.h), sums of up to 2^19 of them are exact and
-// do not depend on order, and u * W and p * W are compared exactly. The result is the same from call to call.
+// round(2^44 w), off by 2^-35 of itself (sample_math.h) and half a unit, sums of up to 2^19 of them are exact and
+// do not depend on order, and u * W and p * W are compared exactly. A border between two tokens is then within
+// 2^-34 + vocab * 2^-45 of its place (many light tokens below one heavy one are what the second term is for: 2^-27 for
+// 248,320, where an fp32 sum is off by 2^-24 and more). The result is the same from call to call.
 //
 // Work. A cluster of 1 to 16 CTAs takes a row, each a slice of it; counts are joined through distributed
 // shared memory, and the first warp of the cluster's first CTA searches and hands out commands. HBM sees each

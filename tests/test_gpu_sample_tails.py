@@ -70,3 +70,14 @@ def test_one_logit_above_values_next_to_zero(nv, lib, best, t, vocab, tiny):
     u = tail_numbers(Row(lib, x.numpy(), t), 40, vocab)
     for kw in ({}, dict(p=0.99999), dict(k=tiny // 2), dict(m=1e-10)):
         check(nv, lib, x, t, u, **kw)
+
+
+@pytest.mark.parametrize("depth", [10.0, 23.0, 29.0, 31.25])
+def test_flat_tails(nv, lib, depth):
+    """Two tokens next to each other above a flat tail, down to weights that are rounded away."""
+    x = torch.full((248320,), -depth)
+    x[0], x[1] = 0.0, -2.0 ** -29
+    u = tail_numbers(Row(lib, x.numpy(), 1.0), 30, 1)
+    u = np.concatenate((u, np.float32([0.5, 0.25, 0.75])))
+    for kw in ({}, dict(p=0.999999), dict(m=2e-13), dict(k=100000)):
+        check(nv, lib, x, 1.0, u, **kw)
