@@ -48,14 +48,20 @@ constexpr int S_WARPS = S_THREADS / 32;
 constexpr int NB2 = S_THREADS;    // parts of a finer count
 constexpr int LIST = S_THREADS;   // tokens that the first CTA puts in order at once
 
+// What weights need beside a slope (in shared memory).
+struct Weigher {
+  unsigned long long table[64];
+  float scale;
+};
+
 // (one copy of the code: a call runs most of its code once, and waits for instructions more than for data)
-__device__ __noinline__ unsigned long long weight_copy(float ref, float x, float hi, float lo, const unsigned long long* table) {
+__device__ __noinline__ unsigned long long weight_copy(float ref, float x, float hi, float lo, const Weigher* by) {
   int n;
-  const unsigned long long w = weight_and_scale(ref, x, Slope{hi, lo}, table, n);
+  const unsigned long long w = weight_and_scale(ref, x, Slope{hi, lo, by->scale}, by->table, n);
   return w | static_cast<unsigned long long>(n) << 48;   // (w <= 2^44)
 }
-NVFP4_DEV unsigned long long weight_call(float ref, float x, const Slope& c, const unsigned long long* table) {
-  const unsigned long long v = weight_copy(ref, x, c.hi, c.lo, table), w = v & ((1ull << 48) - 1);
+NVFP4_DEV unsigned long long weight_call(float ref, float x, const Slope& c, const Weigher& by) {
+  const unsigned long long v = weight_copy(ref, x, c.hi, c.lo, &by), w = v & ((1ull << 48) - 1);
   return rounded_weight(w, static_cast<int>(v >> 48));
 }
 
@@ -152,7 +158,7 @@ enum { BY_COUNT = 0, BY_MASS = 1, BY_KEY = 2 };
 
 struct Shared {
   uint4 edge[2];
-  unsigned long long table[64];
+  Weigher by;
   uint32_t wide_lower[4], wide_upper[4];   // bf16: masses of the wide bins, of the row, in the first CTA
   unsigned long long scan_mass[S_WARPS];
   uint32_t scan_count[S_WARPS];
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
   const int rank = static_cast<int>(blockIdx.x) % ctas, row = static_cast<int>(blockIdx.x) / ctas;
   const bool first_cta = rank == 0;
 
-  if (tid < 64) sh.table[tid] = EXP2_TABLE[tid];
+  if (tid < 64) sh.by.table[tid] = EXP2_TABLE[tid];
   if (tid < 4) sh.wide_lower[tid] = sh.wide_upper[tid] = 0;
   if (tid == 0) sh.max_key = 0, sh.min_bin = NB, sh.list_n = 0, sh.zeros[0] = sh.zeros[1] = 0;
   for (int b = tid; b < NB; b += S_THREADS) {
@@ -453,12 +459,13 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
 
   uint32_t row_max;
   bool irregular = false, mids = false;
-  // (the temperature is looked at behind the pass over the logits: its load takes as long as theirs)
+  // (the temperature is looked at behind the pass over the logits: its load takes as long as theirs; a barrier behind it)
   bool greedy;
   Slope slope;
   auto look_at_temperature = [&]() {
     greedy = !(temperature > 0.f);
     slope = slope_of(greedy ? 1.f : temperature);
+    if (tid == 0) sh.by.scale = slope.scale;
   };
   if (F32) {
     int holder;
@@ -548,8 +555,8 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
       bin_range(bin, row_max, same);
       const float best = value_of<false>(row_max);
       // (middle: their list has run over)
-      irregular = !greedy && ((mids && many && weight_call(best, 0x1p-10f, slope, sh.table) > 0) ||
-                              (lows && weight_call(best, -128.f, slope, sh.table) > 0));
+      irregular = !greedy && ((mids && many && weight_call(best, 0x1p-10f, slope, sh.by) > 0) ||
+                              (lows && weight_call(best, -128.f, slope, sh.by) > 0));
     }
     if (irregular) {
       // Largest logits in a wide bin, weights that a wide bin's figures do not serve: these bins logit by logit.
@@ -565,7 +572,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
         const int b = bin_of(k), n = k ? wide_bin(b) : -1;
         if (n < 0) return;
         atomicAdd(room.count + b, 1u);
-        if (k != last) last = k, last_w = weight_call(best, value_of<false>(k), slope, sh.table);
+        if (k != last) last = k, last_w = weight_call(best, value_of<false>(k), slope, sh.by);
 #pragma unroll
         for (int i = 0; i < 4; ++i) masses[i] += n == i ? last_w : 0ull;
       });
@@ -578,12 +585,12 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
   }
   const float best = value_of<F32>(row_max);
   const bool drawn = row_max != 0 && !greedy;    // the same in every CTA of the cluster
-  auto weigh = [&](uint32_t key) { return weight_call(best, value_of<F32>(key), slope, sh.table); };
+  auto weigh = [&](uint32_t key) { return weight_call(best, value_of<F32>(key), slope, sh.by); };
 
   if (drawn) {
     if (F32) {
       // (the four weights of a group side by side, two to an instruction: their instructions bound this)
-      const bool ordinary = slope.hi > 0.f && slope.hi < 1e30f && best < __int_as_float(0x7F800000);
+      const bool ordinary = slope.scale == 1.f && best < __int_as_float(0x7F800000);
       uint4 ahead = slice.g0 + tid < slice.g1 ? slice.load(slice.g0 + tid) : uint4{};
 #pragma unroll 1
       for (int g = slice.g0 + tid; g < slice.g1; g += S_THREADS) {
@@ -605,13 +612,13 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               int n;
-              const unsigned long long v = weight_of_parts(y[i], t[i], l[i], tail[i], sh.table, n);
+              const unsigned long long v = weight_of_parts(y[i], t[i], l[i], tail[i], sh.by.table, n);
               w[e + i] = rounded_weight(v, n);
             }
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = weight_call(best, __uint_as_float(raw[e]), slope, sh.table);
+          for (int e = 0; e < 4; ++e) w[e] = weight_call(best, __uint_as_float(raw[e]), slope, sh.by);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -640,7 +647,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
         } else if (wide < 0) {
           uint32_t h, same;
           bin_range(b, h, same);
-          m = c * weight(best, value_of<false>(h), slope, sh.table);
+          m = c * weight(best, value_of<false>(h), Slope{slope.hi, slope.lo, sh.by.scale}, sh.by.table);
         } else if (wide == 3 && !irregular) {
           c = 0;   // nothing in it weighs anything (and -inf and NaN were counted too)
         }
@@ -861,7 +868,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
             continue;
           }
           // (a light token's probability has more bits than its rounded weight)
-          const unsigned long long v = weight_copy(best, value_of<F32>(key), slope.hi, slope.lo, sh.table);
+          const unsigned long long v = weight_copy(best, value_of<F32>(key), slope.hi, slope.lo, &sh.by);
           const float w = __ull2float_rn(v & ((1ull << 48) - 1)) * __uint_as_float((127u - static_cast<uint32_t>(v >> 48)) << 23);
           if (lane == 0 && a.probs) a.probs[row] = w / __ull2float_rn(W);
           next = {CMD_END, 0u, 0u, 0, 0u, 0u, 0};

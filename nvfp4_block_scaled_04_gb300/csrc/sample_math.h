@@ -136,14 +136,18 @@ const unsigned long long EXP2_TABLE[64] = {
     0x8b95c1e3ea9ull, 0x8a14d575497ull, 0x88980e8092eull, 0x871f61969e9ull, 0x85aac367cc5ull, 0x843a28c3aceull, 0x82cd8698ac3ull, 0x8164d1f3bc0ull,
 };
 
-// log2(e) / T in two floats (the remainder of the division is exact).
+// log2(e) / T in two floats (the remainder of the division is exact), and the power of two that T and the logits are taken
+// times first: one, but for a T at which log2(e) / T or a difference of two logits may have no fp32 value. (Logits that
+// lose bits by it are small beside such a T; those that overflow differ by more than 46 T or not at all.)
 struct Slope {
-  float hi, lo;
+  float hi, lo, scale;
 };
 
 NVFP4_HD Slope slope_of(float t) {
   const float l_hi = 1.44269502e+00f, l_lo = 1.92596303e-08f;   // log2(e) = l_hi + l_lo to 2^-50
   Slope s;
+  s.scale = t >= 0x1p64f ? 0x1p-64f : t < 0x1p-64f ? 0x1p64f : 1.0f;
+  t = f32_mul(t, s.scale);
   s.hi = f32_div(l_hi, t);
   s.lo = f32_div(f32_add(f32_fma(-s.hi, t, l_hi), l_lo), t);
   return s;
@@ -200,10 +204,10 @@ NVFP4_HD unsigned long long weight_of_parts(float y, float t, float l, float tai
 }
 
 NVFP4_HD unsigned long long weight_and_scale(float ref, float x, const Slope& c, const unsigned long long* table, int& n) {
-  const WeightParts<float> p = weight_parts(ref, -x, c.hi, c.lo, OneFloat());
+  const WeightParts<float> p = weight_parts(f32_mul(ref, c.scale), f32_mul(-x, c.scale), c.hi, c.lo, OneFloat());
   const bool some = p.y < 46.f;
   const unsigned long long w = some ? weight_of_parts(p.y, p.t, p.l, p.tail, table, n) : 0ull;
-  // (where an infinite temperature meets a difference that has no fp32 value)
+  // (an infinite temperature: all finite logits)
   const bool even = x == ref || (c.hi == 0.f && ref - ref == 0.f && x - x == 0.f);
   if (even || !some) n = 0;
   return even ? ONE : w;

@@ -81,3 +81,30 @@ def test_flat_tails(nv, lib, depth):
     u = np.concatenate((u, np.float32([0.5, 0.25, 0.75])))
     for kw in ({}, dict(p=0.999999), dict(m=2e-13), dict(k=100000)):
         check(nv, lib, x, 1.0, u, **kw)
+
+
+@pytest.mark.parametrize("t", [3e38, 1e38, 2e37, 2.0 ** 64, 2.0 ** 63.5, 2.0 ** -63.9, 2.0 ** -64.1, 1e-37, 2.0 ** -128, 2.0 ** -149])
+def test_temperatures_at_the_ends_of_fp32(nv, lib, t):
+    """Logits as far apart as such a temperature asks for; next to the largest number their difference overflows."""
+    t = float(np.float32(t))
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(5000, generator=g).double() * 3 * t
+    x = x.clamp(-3e38, 3e38).float().bfloat16().float()
+    x[7], x[8] = max(float(x.max()), min(9 * t, 3e38)), -3e38
+    x = x.bfloat16().float()
+    u = np.concatenate((np.random.default_rng(1).random(40).astype(np.float32), np.float32([0.0, 0.5, 1 - 2.0 ** -24, 1.0])))
+    for kw in ({}, dict(p=0.7), dict(k=40), dict(m=0.01)):
+        check(nv, lib, x, t, u, **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_two_logits_whose_difference_overflows(nv, dtype):
+    """3 10^38 and its negative at a temperature of 3 10^38: the second token weighs e^-2."""
+    x = torch.tensor([[3e38, -3e38]]).to(dtype)
+    t = float(np.float32(3e38))
+    u = torch.tensor([0.0, 0.5, 0.87, 0.89, 0.95])
+    ids, probs = nv.sample(x.cuda().expand(5, -1), u.cuda(), t)
+    share = 1 / (1 + np.exp(-2 * float(x[0, 0].double()) / t))
+    assert ids.tolist() == [int(float(v) > share) for v in u] == [0, 0, 0, 1, 1]
+    want = torch.tensor([share, share, share, 1 - share, 1 - share])
+    assert bool(((probs.cpu().double() - want).abs() <= 2.0 ** -22).all())
