@@ -412,12 +412,13 @@ struct RawBlock {
   uint4 w[F32 ? 4 : 2];
 };
 
+// (ordinary loads: the stream was written by the statistics pass, beside which this grid may start)
 template <bool F32>
 NVFP4_DEV void load_block(const void* s, int64_t at, RawBlock<F32>& r) {
   const uint4* p = F32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(s) + at)
                        : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s) + at);
 #pragma unroll
-  for (int i = 0; i < (F32 ? 4 : 2); ++i) r.w[i] = __ldg(p + i);
+  for (int i = 0; i < (F32 ? 4 : 2); ++i) r.w[i] = p[i];
 }
 
 template <bool F32>

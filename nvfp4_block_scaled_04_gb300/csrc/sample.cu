@@ -227,7 +227,8 @@ NVFP4_DEV uint32_t* upper_of(Room<false>& r) { return r.upper; }
 NVFP4_DEV uint32_t* upper_of(Room<true>& r) { return r.slice.upper; }
 
 // This CTA's part of a row: 16-byte groups g0 .. g1 - 1, group g holding logits g * GROUP - shift onwards
-// (groups lie on 16-byte boundaries wherever the row starts; logits outside the row read as -inf).
+// (groups lie on 16-byte boundaries wherever the row starts; logits outside the row read as -inf). Ordinary loads: the
+// grid ahead may still be writing the logits when this one starts, so they are not constant for the kernel's life.
 template <bool F32>
 struct Slice {
   using K = Key<F32>;
@@ -250,15 +251,15 @@ struct Slice {
       const int j = g * K::GROUP - shift + e;
       if (j < 0 || j >= vocab) continue;
       if (F32) {
-        w[e] = __ldg(reinterpret_cast<const uint32_t*>(base) + g * 4 + e);
+        w[e] = reinterpret_cast<const uint32_t*>(base)[g * 4 + e];
       } else {
-        const uint32_t h = __ldg(reinterpret_cast<const unsigned short*>(base) + g * 8 + e);
+        const uint32_t h = reinterpret_cast<const unsigned short*>(base)[g * 8 + e];
         w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xFFFFu) | h << 16 : (w[e >> 1] & 0xFFFF0000u) | h;
       }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  NVFP4_DEV uint4 load(int g) const { return whole(g) ? __ldg(reinterpret_cast<const uint4*>(base) + g) : edge[g != 0]; }
+  NVFP4_DEV uint4 load(int g) const { return whole(g) ? reinterpret_cast<const uint4*>(base)[g] : edge[g != 0]; }
 
   static NVFP4_DEV uint32_t bits(const uint4& u, int e) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
