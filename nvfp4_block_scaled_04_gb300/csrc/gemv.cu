@@ -26,8 +26,6 @@ __global__ void __launch_bounds__(XPREP_THREADS) xprep_dense_kernel(const uint16
                                                                      unsigned int* counters, int n_counters) {
   pdl_wait();
   pdl_launch_dependents();
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0u;
   const int64_t out_row = static_cast<int64_t>(blockIdx.y) * GV_MCHUNK + blockIdx.x;
   const uint16_t* src = out_row < M ? X + out_row * K : nullptr;
   const int64_t n8 = K / 8;
@@ -35,6 +33,8 @@ __global__ void __launch_bounds__(XPREP_THREADS) xprep_dense_kernel(const uint16
   else if (n8 <= 2 * XPREP_THREADS) xprep_row_regs<2>(src, K, out_row, xfrag, pexp);
   else if (n8 <= 4 * XPREP_THREADS) xprep_row_regs<4>(src, K, out_row, xfrag, pexp);
   else xprep_row(src, K, out_row, xfrag, pexp);
+  if (blockIdx.x == 0 && blockIdx.y == 0)   // (behind the row's loads)
+    for (int i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0u;
 }
 
 // Row j of the compact copy = row idx[j] of W (codes and row-major scales),

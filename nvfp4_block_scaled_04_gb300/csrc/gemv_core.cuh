@@ -49,6 +49,7 @@ inline size_t xfrag_bytes(int64_t chunks, int64_t K) {
 //   src     bf16 row of K elements, or nullptr for a padding row (zeros)
 //   out_row index of the row in chunk order (chunk = out_row / 32)
 // Writes p (the power-of-two shift) to pexp[out_row]. One CTA per row.
+// (Ordinary loads: the kernel may start beside the grid that still writes the row.)
 NVFP4_DEV void xprep_row(const uint16_t* src, int64_t K, int64_t out_row, uint4* xfrag, int* pexp) {
   __shared__ float red[32];
   const int tid = threadIdx.x;
@@ -56,7 +57,7 @@ NVFP4_DEV void xprep_row(const uint16_t* src, int64_t K, int64_t out_row, uint4*
   float amax = 0.f;
   if (src != nullptr) {
     for (int64_t q = tid; q < n8; q += blockDim.x) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + q);
+      const uint4 v = reinterpret_cast<const uint4*>(src)[q];
       const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -89,7 +90,7 @@ NVFP4_DEV void xprep_row(const uint16_t* src, int64_t K, int64_t out_row, uint4*
   for (int64_t q = tid; q < n8; q += blockDim.x) {
     uint4 o = make_uint4(0, 0, 0, 0);
     if (src != nullptr) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + q);
+      const uint4 v = reinterpret_cast<const uint4*>(src)[q];
       o.x = f32x2_to_f16x2(bf16_bits_to_f32(v.x & 0xFFFFu) * mul, bf16_bits_to_f32(v.x >> 16) * mul);
       o.y = f32x2_to_f16x2(bf16_bits_to_f32(v.y & 0xFFFFu) * mul, bf16_bits_to_f32(v.y >> 16) * mul);
       o.z = f32x2_to_f16x2(bf16_bits_to_f32(v.z & 0xFFFFu) * mul, bf16_bits_to_f32(v.z >> 16) * mul);
@@ -116,7 +117,7 @@ NVFP4_DEV void xprep_row_regs(const uint16_t* src, int64_t K, int64_t out_row, u
   for (int c = 0; c < CHUNKS; ++c) {
     const int64_t q = tid + static_cast<int64_t>(c) * nthr;
     v[c] = make_uint4(0, 0, 0, 0);
-    if (src != nullptr && q < n8) v[c] = __ldg(reinterpret_cast<const uint4*>(src) + q);
+    if (src != nullptr && q < n8) v[c] = reinterpret_cast<const uint4*>(src)[q];
     const uint32_t w4[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

@@ -19,3 +19,12 @@ def test_the_draw_reads_logits_by_ordinary_loads():
 def test_the_norm_reads_only_its_gain_through_the_read_only_path():
     loads = read_only_loads("norm.cu")
     assert loads and all("(weight + k)" in line for line in loads), loads
+
+
+def test_activation_rows_are_read_by_ordinary_loads():
+    """(The loads of a decode linear's activations: its first kernel starts beside a norm, an attention or a linear.)"""
+    text = (CSRC / "gemv_core.cuh").read_text()
+    for name in ("xprep_row(", "xprep_row_regs("):
+        at = text.index("NVFP4_DEV void " + name)
+        body = text[at:text.index("\n}\n", at)]
+        assert "src)" in body and "__ldg" not in body, name
