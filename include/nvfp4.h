@@ -587,7 +587,8 @@ int nvfp4_sample(const void* logits, int dtype, int64_t rows, int64_t vocab, int
  *   draft_ids   device int32 [batch][n_draft] (may be NULL for n_draft = 0)
  *   out_tokens  device int32 [batch][n_draft + 1]
  *   out_probs   device fp32 like out_tokens, or NULL
- *   n_accepted  device int32 [batch]: leading drafts equal to out_tokens */
+ *   n_accepted  device int32 [batch]: leading drafts equal to out_tokens (a -1
+ *               is no token: a draft of -1 never stands) */
 int nvfp4_verify_sample(const void* logits, int dtype, int64_t batch, int n_draft, int64_t vocab, int64_t stride,
                         nvfp4_sampling_t settings, const float* uniform, const int32_t* draft_ids, int32_t* out_tokens,
                         float* out_probs, int32_t* n_accepted, nvfp4_stream_t stream);

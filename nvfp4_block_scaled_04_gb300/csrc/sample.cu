@@ -1082,14 +1082,17 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
   cluster_sync_all();   // no CTA leaves while another may read its shared memory
 }
 
-// Accepted drafts: the leading ones that are the token drawn at their position.
+// Accepted drafts: the leading ones that are the token drawn at their position (-1, in a row without a token, is none).
 __global__ void accept_kernel(const int32_t* tokens, const int32_t* drafts, int64_t batch, int n_draft, int32_t* accepted) {
   pdl_wait();
   pdl_launch_dependents();
   const int64_t b = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (b >= batch) return;
   int n = 0;
-  while (n < n_draft && tokens[b * (n_draft + 1) + n] == drafts[b * n_draft + n]) ++n;
+  for (; n < n_draft; ++n) {
+    const int32_t token = tokens[b * (n_draft + 1) + n];
+    if (token < 0 || token != drafts[b * n_draft + n]) break;
+  }
   accepted[b] = n;
 }
 
