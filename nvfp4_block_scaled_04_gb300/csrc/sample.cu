@@ -159,7 +159,7 @@ enum { BY_COUNT = 0, BY_MASS = 1, BY_KEY = 2 };
 struct Shared {
   uint4 edge[2];
   Weigher by;
-  uint32_t wide_lower[4], wide_upper[4];   // bf16: masses of the wide bins, of the row, in the first CTA
+  uint32_t wide[4][3];   // bf16: masses of the wide bins, of the row, in the first CTA: sums of 22 bits, 22 and the rest
   unsigned long long scan_mass[S_WARPS];
   uint32_t scan_count[S_WARPS];
   Command cmd;
@@ -324,12 +324,18 @@ NVFP4_DEV void add_mass(uint32_t* lower, uint32_t* upper, unsigned long long w) 
   if (hi) atomicAdd(upper, hi);
 }
 
-// Adds each thread's mass to the row's of a wide bin (whole warps).
+// Adds each thread's mass to the row's of a wide bin (whole warps; 256 of them at most, so that no part runs over, and no
+// add waits for a carry from the first CTA: 1 row of 248,320 15.7 us, with one 15.85).
 NVFP4_DEV void add_wide(Shared& sh, int wide, unsigned long long m) {
   if (!__any_sync(0xffffffffu, m != 0)) return;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-  if ((threadIdx.x & 31) == 0) add_mass(in_cta(&sh.wide_lower[wide], 0), in_cta(&sh.wide_upper[wide], 0), m);
+  if ((threadIdx.x & 31) == 0) {
+    uint32_t* const to = in_cta(sh.wide[wide], 0);
+    atomicAdd(to, static_cast<uint32_t>(m) & 0x3FFFFFu);
+    atomicAdd(to + 1, static_cast<uint32_t>(m >> 22) & 0x3FFFFFu);
+    atomicAdd(to + 2, static_cast<uint32_t>(m >> 44));
+  }
 }
 
 // The sum over this and all earlier threads of the CTA (every thread calls it; ends behind a barrier).
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
   const bool first_cta = rank == 0;
 
   if (tid < 64) sh.by.table[tid] = EXP2_TABLE[tid];
-  if (tid < 4) sh.wide_lower[tid] = sh.wide_upper[tid] = 0;
+  if (tid < 12) sh.wide[tid / 3][tid % 3] = 0;
   if (tid == 0) sh.max_key = 0, sh.min_bin = NB, sh.list_n = 0, sh.zeros[0] = sh.zeros[1] = 0;
   for (int b = tid; b < NB; b += S_THREADS) {
     room.count[b] = 0;
@@ -657,15 +663,16 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
       *in_cta(room.merged_mass + b, 0) = m;
     }
     if (!F32 && mids && !irregular) {   // the middle bins' masses are those of their tokens, as lists and finer counts have them
+      const int at = S_THREADS - 1 - tid;   // (the last warps had the fewest bins to join: 15.7 -> 15.35 us)
       uint32_t half = 0;
       unsigned long long w = 0;
-      if (tid < min(sh.list_n, static_cast<uint32_t>(LIST))) {
-        half = fine_room.noted[tid];
+      if (at < min(sh.list_n, static_cast<uint32_t>(LIST))) {
+        half = fine_room.noted[at];
         w = weigh(key_of<false>(half));
       }
       add_wide(sh, 2, half > 0x8000u ? w : 0ull);
       if (half > 0x8000u) w = 0;
-      if (tid == 0 && sh.zeros[0] + sh.zeros[1] > 0) w += (sh.zeros[0] + sh.zeros[1]) * weigh(key_of<false>(0u));
+      if (at == 0 && sh.zeros[0] + sh.zeros[1] > 0) w += (sh.zeros[0] + sh.zeros[1]) * weigh(key_of<false>(0u));
       add_wide(sh, 1, w);
     }
     cluster_sync_all();
@@ -678,7 +685,8 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
         const int b = tid * PER + i;
         if (b < NB) {
           const int wide = F32 ? -1 : wide_bin(b);
-          if (wide >= 0) room.merged_mass[b] = static_cast<unsigned long long>(sh.wide_upper[wide]) << 32 | sh.wide_lower[wide];
+          if (wide >= 0) room.merged_mass[b] = sh.wide[wide][0] + (static_cast<unsigned long long>(sh.wide[wide][1]) << 22) +
+                                                (static_cast<unsigned long long>(sh.wide[wide][2]) << 44);
           c += room.merged[b];
           m += room.merged_mass[b];
         }
