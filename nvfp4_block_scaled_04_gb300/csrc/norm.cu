@@ -16,7 +16,7 @@
 // 2048 x 16384 with an fp32 stream 71 -> 69), and a CTA's next row while its last
 // one is summed and stored (7.1 -> 6.3, 69 -> 64). Measured in graphs of calls on
 // changing inputs, bf16 stream and output: 1 x 5120 2.4 us, 512 x 5120 5.7,
-// 8192 x 5120 52 (6.4 TB/s); E4M3 output, fp32 stream, 8192 x 5120 70.5 (6.5 TB/s).
+// 8192 x 5120 52 (6.4 TB/s); E4M3 output, fp32 stream, 8192 x 5120 70.4 (6.5 TB/s).
 // Rows of up to 1024 elements (heads of 64 or 128 among them) belong to 8, 16 or
 // 32 lanes of a warp and need no block-wide step; longer rows to a CTA.
 #include "common.cuh"

@@ -22,13 +22,17 @@
 // 248,320, where an fp32 sum is off by 2^-24 and more). The result is the same from call to call.
 //
 // Work. A cluster of 1 to 16 CTAs takes a row, each a slice of it; counts are joined through distributed
-// shared memory, and the first warp of the cluster's first CTA searches and hands out commands. HBM sees each
-// bf16 logit once (fp32: twice where the logits exceed L2; their masses need the row's maximum first).
+// shared memory, and the first warp of the cluster's first CTA searches and hands out commands. Every bf16 logit is read
+// once for the counts, every fp32 one twice (masses need the row's maximum first); each list and finer count reads the
+// slice again, and the token's search the runs that may hold it (fp32: all), from L2 where the logits fit.
+// Times in a graph of calls on changing inputs (one card; others differ by up to 3%):
 //   few rows: latency, 30 thousand clocks of dependent steps, a third of them waits at the four cluster barriers and a
-//     quarter the searches (1 row of 248,320 bf16: 15.5 us, in a graph; 64 rows: 25.3 us)
+//     quarter the searches (248,320 bf16 logits without a filter: 1 row 15.7 us, 64 rows 25.6; top-k 20 and top-p 0.8: 17.2
+//     and 25.4)
 //   many rows: atomics in shared memory, one for each logit, 3.3 to 4.8 clocks for a warp's (256 rows: 64 us, of which
 //     the pass that counts takes 36 where an SM has two rows; HBM alone would take 18.7)
-//   fp32: the instructions of the weights, 60% of the issue slots (24 rows of 151,937: 51 us; 128 of 248,320: 193 us)
+//   fp32: the instructions of the weights, 60% of the issue slots (24 rows of 151,937, top-p 0.95: 52 us; 128 of 248,320
+//     without a filter: 198 us)
 // Steps that carried it: bins of two logits at a time from clamped magnitudes; one warp searching by ballots in
 // place of the CTA; one copy of each rare piece of code (instruction fetches bound the single pass); masses
 // in two 32-bit words (a 64-bit atomic is a loop: 11 to 1700 clocks); two weights to an instruction.
@@ -325,7 +329,7 @@ NVFP4_DEV void add_mass(uint32_t* lower, uint32_t* upper, unsigned long long w) 
 }
 
 // Adds each thread's mass to the row's of a wide bin (whole warps; 256 of them at most, so that no part runs over, and no
-// add waits for a carry from the first CTA: 1 row of 248,320 15.7 us, with one 15.85).
+// add waits for a carry from the first CTA: 1 row of 248,320 1% faster).
 NVFP4_DEV void add_wide(Shared& sh, int wide, unsigned long long m) {
   if (!__any_sync(0xffffffffu, m != 0)) return;
 #pragma unroll
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) sample_kernel(const SampleArgs a
       *in_cta(room.merged_mass + b, 0) = m;
     }
     if (!F32 && mids && !irregular) {   // the middle bins' masses are those of their tokens, as lists and finer counts have them
-      const int at = S_THREADS - 1 - tid;   // (the last warps had the fewest bins to join: 15.7 -> 15.35 us)
+      const int at = S_THREADS - 1 - tid;   // (the last warps had the fewest bins to join: 1 row of 248,320 2% faster)
       uint32_t half = 0;
       unsigned long long w = 0;
       if (at < min(sh.list_n, static_cast<uint32_t>(LIST))) {
