@@ -564,9 +564,10 @@ typedef struct nvfp4_sampling {
  * 2^-45 (one below 2^-45 counts as 0, and its token is not drawn), and weights
  * are added exactly. So the token is that of the formulas in real numbers unless
  * u or top_p lies within 2^-34 + vocab * 2^-45 of a border between two tokens
- * (vocab = 248,320: 2^-27, near one step of u; the second term is of a row whose
- * first token has most of the mass, and falls with that share), or a weight
- * within 2^-35 of itself and 2^-45 of min_p. The same inputs give the same tokens.
+ * (vocab = 248,320: 2^-27, an eighth of the step between two values of u next to
+ * 1; the second term is for a row whose first token has most of the mass, and
+ * falls with that share), or a weight within 2^-35 of itself and 2^-45 of min_p.
+ * The same inputs give the same tokens.
  *   logits   device, bf16 or fp32 (dtype), row r at r * stride elements,
  *            aligned to its type; any vocab of 1 .. 524288; stride >= vocab, or 0:
  *            every row draws from the same logits
